@@ -77,7 +77,7 @@ typedef enum { CTR_SRC_FULL = 0, CTR_SRC_ROWS = 1 } ctr_src_layout_t;
 
 /* Library version (major*10000 + minor*100 + patch).  0.2.0 added src_layout (ctr_unique_ids,
  * ctr_embbag_bwd_sgd*), out_dtype (ctr_embbag_fwd) and z_dtype (ctr_dot_interaction_fwd/bwd,
- * ctr_step_t). */
+ * ctr_step_t); 0.3.0 the experts (ctr_expert_*) and gradient clipping (ctr_grad_clip*). */
 int32_t ctr_version(void);
 
 /* Text of a status code (static storage). */
@@ -654,6 +654,123 @@ int32_t ctr_dense_bwd_sgd(const float* X, int64_t x_stride, int64_t M, int32_t K
 int32_t ctr_logistic_ne(const float* logits, int64_t logit_stride, const float* labels,
                         int64_t M, float* prob, float* dlogits, int64_t dl_stride, float* stats,
                         void* stream);
+
+/*
+ * ---------------------------------------------------------------- experts
+ * A mixture of fully connected layers: a gate chooses k of E experts for every token (a
+ * sample of the batch), the tokens' rows are sorted by expert, each expert applies its own
+ * layer to its rows, and the results come back to the tokens with the gate's weights.
+ * Common to these calls: dtype CTR_F32, CTR_BF16 or CTR_F16; weights of the gate, biases and
+ * parameter gradients fp32; sums fp32, each result rounded once (nearest-even) at its store;
+ * row strides in elements, at least the row; any alignment to the element (16-byte aligned
+ * rows take the wide loads); 1 <= num_experts <= 1024, 1 <= k <= 64, T <= 2^25 and T * k
+ * below 2^31.  T = 0 or n = 0 is legal.  No two arrays of a call overlap unless it says so.
+ * All results are the same in every run (no floating-point atomics).
+ *
+ * Slot i = t*k + j is token t's j-th choice.  n = T*k.
+ *
+ * ctr_expert_route_fwd -- for every token the k experts of the largest logits, the larger
+ * first and among equals the lower expert (k <= num_experts):
+ *   experts[t, j] = e_j,   weights[t, j] = exp(x[e_j]) / sum over S of exp(x[e])
+ * with S the chosen experts if renormalize, else all.  A logit of -inf or NaN closes its
+ * expert: it is never chosen and adds nothing.  Where fewer than k are open, the experts left
+ * over are -1 with weight 0.
+ * ctr_expert_route_bwd -- with w, dw the row's weights and their gradients and q the softmax
+ * that the weights were taken from (0 for closed experts):
+ *   dlogits[t, e] = q_e * ((e chosen, e = e_j ? dw_j : 0) - sum_j w_j dw_j)
+ * experts and weights are the forward's; dlogits has logits' dtype.
+ */
+int32_t ctr_expert_route_fwd(const void* logits, int32_t dtype, int64_t logit_stride, int64_t T,
+                             int32_t num_experts, int32_t k, int32_t renormalize,
+                             int32_t* experts, float* weights, void* stream);
+int32_t ctr_expert_route_bwd(const void* logits, int32_t dtype, int64_t logit_stride, int64_t T,
+                             int32_t num_experts, int32_t k, int32_t renormalize,
+                             const int32_t* experts, const float* weights, const float* dweights,
+                             void* dlogits, int64_t dl_stride, void* stream);
+
+/*
+ * ctr_expert_sort -- the slots sorted by expert, those of one expert in slot order.  A slot
+ * whose expert is not in [0, num_experts) is dropped: it has no position.
+ *   offsets[e]  first position of expert e; offsets[num_experts] = slots not dropped  [E + 1]
+ *   slots[i]    position of slot i, or -1                                            [n]
+ *   order[p]    slot at position p; -1 for p >= offsets[num_experts]                 [n]
+ * All int32.  Workspace: two-call query.
+ */
+int32_t ctr_expert_sort(const int32_t* experts, int64_t T, int32_t k, int32_t num_experts,
+                        int32_t* offsets, int32_t* slots, int32_t* order, void* workspace,
+                        size_t* workspace_bytes, void* stream);
+
+/*
+ * Rows there and back, D values each; P has n rows.  slots and offsets are ctr_expert_sort's.
+ * ctr_expert_dispatch     P[slots[t*k + j], :] = X[t, :];  rows from offsets[E] on are zero.
+ * ctr_expert_combine_fwd  Y[t, :] = sum_j weights[t, j] P[slots[t*k + j], :]  (in the order of
+ *     j, dropped slots add nothing).  weights NULL: all 1; with P = dP this is the gradient of
+ *     ctr_expert_dispatch.
+ * ctr_expert_combine_bwd  dP[slots[t*k + j], :] = weights[t, j] dY[t, :]  (NULL: 1), rows from
+ *     offsets[E] on zero;  dweights[t, j] = <dY[t, :], P[slots[t*k + j], :]>, 0 for dropped
+ *     slots (dweights NULL: not computed, P not read).
+ */
+int32_t ctr_expert_dispatch(const void* X, int32_t dtype, int64_t x_stride, int64_t T, int32_t k,
+                            int32_t D, const int32_t* slots, const int32_t* offsets,
+                            int32_t num_experts, void* P, int64_t p_stride, void* stream);
+int32_t ctr_expert_combine_fwd(const void* P, int32_t dtype, int64_t p_stride, int64_t T,
+                               int32_t k, int32_t D, const int32_t* slots, const float* weights,
+                               void* Y, int64_t y_stride, void* stream);
+int32_t ctr_expert_combine_bwd(const void* dY, int32_t dtype, int64_t dy_stride, int64_t T,
+                               int32_t k, int32_t D, const void* P, int64_t p_stride,
+                               const int32_t* slots, const int32_t* offsets, int32_t num_experts,
+                               const float* weights, void* dP, int64_t dp_stride,
+                               float* dweights, void* stream);
+
+/*
+ * ctr_expert_dense_fwd -- each expert's layer over its rows, p in [offsets[e], offsets[e+1]):
+ *   Y[p, :] = act(W[e] x(p) + b[e]),   act = max(., 0) if relu (NaN gives 0) else the identity
+ * x(p) = X[p, :] (order NULL), or X[order[p] / k, :]: the tokens' rows read in place, without
+ * ctr_expert_dispatch (order is ctr_expert_sort's and k its k; a row outside [0, x_rows) reads
+ * as zeros).  W: [E, N, K] of dtype, contiguous; b: fp32 [E, N] or NULL; Y: [n, N] of dtype,
+ * rows from offsets[E] on are zero.  1 <= K, N <= 65536.
+ *
+ * ctr_expert_dense_bwd -- given dY = the gradient of W[e] x(p) + b[e] (dtype):
+ *   dX[p, :] = W[e]^T dY[p, :], times [x(p) > 0] if x_relu; rows from offsets[E] on are zero
+ *   dW[e]    = sum over p of dY[p, :] x(p)^T      fp32 [E, N, K] (an expert without rows: 0)
+ *   db[e]    = sum over p of dY[p, :]             fp32 [E, N]
+ * x_relu: X holds the rectified outputs of the layer before (whose forward had relu), and dX
+ * becomes the gradient of that layer's W x + b.  dX is by position (ctr_expert_combine_fwd
+ * without weights takes it back to the tokens).  dX, dW, db may each be NULL.
+ * Workspace: two-call query.
+ */
+int32_t ctr_expert_dense_fwd(const void* X, int32_t dtype, int64_t x_stride, int64_t x_rows,
+                             const int32_t* order, int32_t k, const int32_t* offsets, int64_t n,
+                             int32_t num_experts, int32_t K, const void* W, const float* b,
+                             int32_t N, int32_t relu, void* Y, int64_t y_stride, void* stream);
+int32_t ctr_expert_dense_bwd(const void* X, int32_t dtype, int64_t x_stride, int64_t x_rows,
+                             const int32_t* order, int32_t k, const int32_t* offsets, int64_t n,
+                             int32_t num_experts, int32_t K, const void* W, int32_t N,
+                             int32_t x_relu, const void* dY, int64_t dy_stride, void* dX,
+                             int64_t dx_stride, float* dW, float* db, void* workspace,
+                             size_t* workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------- gradient clipping
+ * The gradients of a whole step, num tensors of sizes[i] contiguous elements and dtypes[i]:
+ *   norm = sqrt(sum over all elements of g^2)       (binary64 sums)
+ *   scale = norm > max_norm ? max_norm / norm : 1   (a NaN norm gives a NaN scale)
+ *   stats[0] = norm, stats[1] = scale               (fp32 [2], device)
+ * ctr_grad_clip      outs[i] = scale * grads[i], rounded to dtypes[i]; outs NULL, or outs[i]
+ *                    NULL or equal to grads[i]: in place (not written where scale is 1).
+ * ctr_grad_clip_sgd  params[i] = params[i] - (lr * scale) * grads[i], one fp32 fused
+ *                    multiply-add, rounded to param_dtypes[i]; the gradients are kept.
+ * grads, sizes, dtypes, outs, params, param_dtypes: HOST arrays, read before the call returns;
+ * the tensors they name are device memory, aligned to their elements.  num = 0 is legal
+ * (norm 0).  Workspace: two-call query.
+ */
+int32_t ctr_grad_clip(int32_t num, const void* const* grads, const int64_t* sizes,
+                      const int32_t* dtypes, void* const* outs, float max_norm, float* stats,
+                      void* workspace, size_t* workspace_bytes, void* stream);
+int32_t ctr_grad_clip_sgd(int32_t num, const void* const* grads, const int64_t* sizes,
+                          const int32_t* dtypes, void* const* params,
+                          const int32_t* param_dtypes, float lr, float max_norm, float* stats,
+                          void* workspace, size_t* workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

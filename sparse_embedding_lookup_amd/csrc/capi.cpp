@@ -87,7 +87,8 @@ hipError_t record_mark(void* ev, hipStream_t s) {
 extern "C" {
 
 // 0.2.0: sorted_src layouts (src_layout), bf16 pooled vectors (out_dtype) and bf16 Z (z_dtype)
-int32_t ctr_version(void) { return 200; }
+// 0.3.0: experts (ctr_expert_*) and gradient clipping (ctr_grad_clip*)
+int32_t ctr_version(void) { return 300; }
 
 const char* ctr_status_string(int32_t status) {
   switch (status) {
@@ -853,6 +854,336 @@ int32_t ctr_logistic_ne(const float* logits, int64_t logit_stride, const float* 
   return hip_status(ctr::launch_logistic_ne(logits, logit_stride, labels, M, prob, dlogits,
                                             dl_stride, stats, (hipStream_t)stream),
                     "ctr_logistic_ne");
+}
+
+// ------------------------------------------------------------------------------- experts
+// Limits of the expert entry points: experts and slots of a token are registers and shared
+// memory of the router and the sort; tokens and tiles are blocks of one launch (a grid has
+// fewer than 2^32 threads).
+static constexpr int32_t kMaxExperts = 1024, kMaxChosen = 64;
+static constexpr int64_t kMaxTokens = (int64_t)1 << 25, kMaxBlocks = (int64_t)1 << 23;
+
+static bool elt_ok(int32_t dtype) {
+  return dtype == CTR_F32 || dtype == CTR_BF16 || dtype == CTR_F16;
+}
+// Aligned to its element (NULL is).
+static bool elt_aligned(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == CTR_F32 ? 3u : 1u)) == 0;
+}
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int32_t check_experts(int64_t T, int32_t k, int32_t E) {
+  if (T < 0 || k < 1 || E < 1)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "need T >= 0, k >= 1, num_experts >= 1");
+  if (E > kMaxExperts)
+    return fail(CTR_ERR_UNSUPPORTED, "num_experts %d above %d", E, kMaxExperts);
+  if (k > kMaxChosen) return fail(CTR_ERR_UNSUPPORTED, "k %d above %d", k, kMaxChosen);
+  if (T > kMaxTokens || T * k > kMaxElems)
+    return fail(CTR_ERR_UNSUPPORTED, "T above 2^25, or T * k not below 2^31");
+  return CTR_OK;
+}
+
+static int32_t check_route(const void* logits, int32_t dtype, int64_t stride, int64_t T,
+                           int32_t E, int32_t k) {
+  int32_t st = check_experts(T, k, E);
+  if (st) return st;
+  if (!elt_ok(dtype))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "dtype %d is not CTR_F32, CTR_BF16 or CTR_F16", dtype);
+  if (k > E) return fail(CTR_ERR_INVALID_ARGUMENT, "k %d above num_experts %d", k, E);
+  if (stride < E) return fail(CTR_ERR_INVALID_ARGUMENT, "logit_stride < num_experts");
+  if (T > 0 && !logits) return fail(CTR_ERR_INVALID_ARGUMENT, "logits is required");
+  if (!elt_aligned(logits, dtype))
+    return fail(CTR_ERR_UNSUPPORTED, "logits is not aligned to its elements");
+  return CTR_OK;
+}
+
+int32_t ctr_expert_route_fwd(const void* logits, int32_t dtype, int64_t logit_stride, int64_t T,
+                             int32_t num_experts, int32_t k, int32_t renormalize,
+                             int32_t* experts, float* weights, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_route(logits, dtype, logit_stride, T, num_experts, k);
+  if (st) return st;
+  if (T > 0 && (!experts || !weights))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "experts and weights are required");
+  if (!aligned4(experts) || !aligned4(weights))
+    return fail(CTR_ERR_UNSUPPORTED, "experts and weights must be 4-byte aligned");
+  return hip_status(ctr::launch_expert_route_fwd(logits, dtype, logit_stride, T, num_experts, k,
+                                                 renormalize != 0, experts, weights,
+                                                 (hipStream_t)stream),
+                    "ctr_expert_route_fwd");
+}
+
+int32_t ctr_expert_route_bwd(const void* logits, int32_t dtype, int64_t logit_stride, int64_t T,
+                             int32_t num_experts, int32_t k, int32_t renormalize,
+                             const int32_t* experts, const float* weights, const float* dweights,
+                             void* dlogits, int64_t dl_stride, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_route(logits, dtype, logit_stride, T, num_experts, k);
+  if (st) return st;
+  if (dl_stride < num_experts)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "dl_stride < num_experts");
+  if (T > 0 && (!experts || !weights || !dweights || !dlogits))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "experts, weights, dweights and dlogits are required");
+  if (!aligned4(experts) || !aligned4(weights) || !aligned4(dweights) ||
+      !elt_aligned(dlogits, dtype))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_expert_route_bwd(logits, dtype, logit_stride, T, num_experts, k,
+                                                 renormalize != 0, experts, weights, dweights,
+                                                 dlogits, dl_stride, (hipStream_t)stream),
+                    "ctr_expert_route_bwd");
+}
+
+int32_t ctr_expert_sort(const int32_t* experts, int64_t T, int32_t k, int32_t num_experts,
+                        int32_t* offsets, int32_t* slots, int32_t* order, void* workspace,
+                        size_t* workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_experts(T, k, num_experts);
+  if (st) return st;
+  if (!workspace_bytes) return fail(CTR_ERR_INVALID_ARGUMENT, "workspace_bytes is required");
+  const size_t need = ctr::expert_sort_workspace_bytes(T * k, num_experts);
+  if (!workspace) {
+    *workspace_bytes = need;
+    return CTR_OK;
+  }
+  if (*workspace_bytes < need)
+    return fail(CTR_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need,
+                *workspace_bytes);
+  if (!aligned16(workspace)) return fail(CTR_ERR_UNSUPPORTED, "workspace is not 16-byte aligned");
+  if (!offsets || (T > 0 && (!experts || !slots || !order)))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "experts, offsets, slots and order are required");
+  if (!aligned4(experts) || !aligned4(offsets) || !aligned4(slots) || !aligned4(order))
+    return fail(CTR_ERR_UNSUPPORTED, "experts, offsets, slots and order must be 4-byte aligned");
+  return hip_status(ctr::launch_expert_sort(experts, T * k, num_experts, offsets, slots, order,
+                                            workspace, (hipStream_t)stream),
+                    "ctr_expert_sort");
+}
+
+static int32_t check_rows(int64_t T, int32_t k, int32_t E, int32_t D, int32_t dtype) {
+  int32_t st = check_experts(T, k, E);
+  if (st) return st;
+  if (!elt_ok(dtype))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "dtype %d is not CTR_F32, CTR_BF16 or CTR_F16", dtype);
+  if (D < 1 || D > 65536) return fail(CTR_ERR_INVALID_ARGUMENT, "D must be in [1, 65536]");
+  return CTR_OK;
+}
+
+int32_t ctr_expert_dispatch(const void* X, int32_t dtype, int64_t x_stride, int64_t T, int32_t k,
+                            int32_t D, const int32_t* slots, const int32_t* offsets,
+                            int32_t num_experts, void* P, int64_t p_stride, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_rows(T, k, num_experts, D, dtype);
+  if (st) return st;
+  if (x_stride < D || p_stride < D)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "x_stride and p_stride must be at least D");
+  if (T > 0 && (!X || !slots || !offsets || !P))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "X, slots, offsets and P are required");
+  if (!elt_aligned(X, dtype) || !elt_aligned(P, dtype) || !aligned4(slots) || !aligned4(offsets))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_expert_dispatch(X, dtype, x_stride, T, k, D, slots, offsets,
+                                                num_experts, P, p_stride, (hipStream_t)stream),
+                    "ctr_expert_dispatch");
+}
+
+int32_t ctr_expert_combine_fwd(const void* P, int32_t dtype, int64_t p_stride, int64_t T,
+                               int32_t k, int32_t D, const int32_t* slots, const float* weights,
+                               void* Y, int64_t y_stride, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_rows(T, k, 1, D, dtype);
+  if (st) return st;
+  if (p_stride < D || y_stride < D)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "p_stride and y_stride must be at least D");
+  if (T > 0 && (!P || !slots || !Y))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "P, slots and Y are required");
+  if (!elt_aligned(P, dtype) || !elt_aligned(Y, dtype) || !aligned4(slots) || !aligned4(weights))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_expert_combine_fwd(P, dtype, p_stride, T, k, D, slots, weights, Y,
+                                                   y_stride, (hipStream_t)stream),
+                    "ctr_expert_combine_fwd");
+}
+
+int32_t ctr_expert_combine_bwd(const void* dY, int32_t dtype, int64_t dy_stride, int64_t T,
+                               int32_t k, int32_t D, const void* P, int64_t p_stride,
+                               const int32_t* slots, const int32_t* offsets, int32_t num_experts,
+                               const float* weights, void* dP, int64_t dp_stride,
+                               float* dweights, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_rows(T, k, num_experts, D, dtype);
+  if (st) return st;
+  if (dy_stride < D || dp_stride < D || (dweights && p_stride < D))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "strides must be at least D");
+  if (T > 0 && (!dY || !slots || !offsets || !dP || (dweights && !P)))
+    return fail(CTR_ERR_INVALID_ARGUMENT,
+                "dY, slots, offsets, dP (and P with dweights) are required");
+  if (!elt_aligned(dY, dtype) || !elt_aligned(P, dtype) || !elt_aligned(dP, dtype) ||
+      !aligned4(slots) || !aligned4(offsets) || !aligned4(weights) || !aligned4(dweights))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_expert_combine_bwd(dY, dtype, dy_stride, T, k, D, P, p_stride,
+                                                   slots, offsets, num_experts, weights, dP,
+                                                   dp_stride, dweights, (hipStream_t)stream),
+                    "ctr_expert_combine_bwd");
+}
+
+static int32_t check_product(const void* X, int32_t dtype, int64_t x_stride, int64_t x_rows,
+                             const int32_t* order, int32_t k, int64_t n, int32_t E, int32_t K,
+                             int32_t N) {
+  if (n < 0 || n > kMaxElems || x_rows < 0 || x_rows > kMaxElems)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "n and x_rows must be in [0, 2^31)");
+  if (!elt_ok(dtype))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "dtype %d is not CTR_F32, CTR_BF16 or CTR_F16", dtype);
+  if (E < 1) return fail(CTR_ERR_INVALID_ARGUMENT, "num_experts must be at least 1");
+  if (E > kMaxExperts)
+    return fail(CTR_ERR_UNSUPPORTED, "num_experts %d above %d", E, kMaxExperts);
+  if (order && k < 1) return fail(CTR_ERR_INVALID_ARGUMENT, "order needs k >= 1");
+  if (K < 1 || K > kMaxWidth || N < 1 || N > kMaxWidth)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "layer widths must be in [1, %d] (got K=%d, N=%d)",
+                kMaxWidth, K, N);
+  if (x_stride < K) return fail(CTR_ERR_INVALID_ARGUMENT, "x_stride < K");
+  if (!order && x_rows < n) return fail(CTR_ERR_INVALID_ARGUMENT, "X has fewer rows than n");
+  const int64_t kt = (K + 63) / 64, nt = (N + 63) / 64;
+  if ((n / 64 + E + 1) * (kt > nt ? kt : nt) > kMaxBlocks || E * kt * nt > kMaxBlocks)
+    return fail(CTR_ERR_UNSUPPORTED, "more than 2^23 tiles of 64 x 64");
+  if (!elt_aligned(X, dtype) || !aligned4(order))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return CTR_OK;
+}
+
+int32_t ctr_expert_dense_fwd(const void* X, int32_t dtype, int64_t x_stride, int64_t x_rows,
+                             const int32_t* order, int32_t k, const int32_t* offsets, int64_t n,
+                             int32_t num_experts, int32_t K, const void* W, const float* b,
+                             int32_t N, int32_t relu, void* Y, int64_t y_stride, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_product(X, dtype, x_stride, x_rows, order, k, n, num_experts, K, N);
+  if (st) return st;
+  if (y_stride < N) return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride < N");
+  if (n > 0 && (!X || !offsets || !W || !Y))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "X, offsets, W and Y are required");
+  if (!elt_aligned(W, dtype) || !elt_aligned(Y, dtype) || !aligned4(offsets) || !aligned4(b))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_expert_dense_fwd(X, dtype, x_stride, x_rows, order, k, offsets, n,
+                                                 num_experts, K, W, b, N, relu != 0, Y, y_stride,
+                                                 (hipStream_t)stream),
+                    "ctr_expert_dense_fwd");
+}
+
+int32_t ctr_expert_dense_bwd(const void* X, int32_t dtype, int64_t x_stride, int64_t x_rows,
+                             const int32_t* order, int32_t k, const int32_t* offsets, int64_t n,
+                             int32_t num_experts, int32_t K, const void* W, int32_t N,
+                             int32_t x_relu, const void* dY, int64_t dy_stride, void* dX,
+                             int64_t dx_stride, float* dW, float* db, void* workspace,
+                             size_t* workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_product(X, dtype, x_stride, x_rows, order, k, n, num_experts, K, N);
+  if (st) return st;
+  if (dy_stride < N) return fail(CTR_ERR_INVALID_ARGUMENT, "dy_stride < N");
+  if (dX && dx_stride < K) return fail(CTR_ERR_INVALID_ARGUMENT, "dx_stride < K");
+  if (!workspace_bytes) return fail(CTR_ERR_INVALID_ARGUMENT, "workspace_bytes is required");
+  const size_t need = ctr::expert_dense_bwd_workspace_bytes(n, num_experts, K, N, dtype);
+  if (!workspace) {
+    *workspace_bytes = need;
+    return CTR_OK;
+  }
+  if (*workspace_bytes < need)
+    return fail(CTR_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need,
+                *workspace_bytes);
+  if (!aligned16(workspace)) return fail(CTR_ERR_UNSUPPORTED, "workspace is not 16-byte aligned");
+  if (!offsets || (n > 0 && (!dY || ((dW || (dX && x_relu)) && !X) || (dX && !W))))
+    return fail(CTR_ERR_INVALID_ARGUMENT,
+                "offsets and dY (X with dW or x_relu, W with dX) are required");
+  if (!elt_aligned(W, dtype) || !elt_aligned(dY, dtype) || !elt_aligned(dX, dtype) ||
+      !aligned4(offsets) || !aligned4(dW) || !aligned4(db))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_expert_dense_bwd(X, dtype, x_stride, x_rows, order, k, offsets, n,
+                                                 num_experts, K, W, N, x_relu != 0, dY, dy_stride,
+                                                 dX, dx_stride, dW, db, workspace,
+                                                 (hipStream_t)stream),
+                    "ctr_expert_dense_bwd");
+}
+
+// ------------------------------------------------------------------------ gradient clipping
+static int32_t check_clip(int32_t num, const void* const* grads, const int64_t* sizes,
+                          const int32_t* dtypes, float max_norm, const float* stats) {
+  if (num < 0 || num > 65536) return fail(CTR_ERR_INVALID_ARGUMENT, "num %d out of [0, 65536]", num);
+  if (num > 0 && (!grads || !sizes || !dtypes))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "grads, sizes and dtypes are required");
+  if (!(max_norm >= 0.f)) return fail(CTR_ERR_INVALID_ARGUMENT, "max_norm must be >= 0");
+  if (!stats) return fail(CTR_ERR_INVALID_ARGUMENT, "stats is required");
+  if (!aligned4(stats)) return fail(CTR_ERR_UNSUPPORTED, "stats is not 4-byte aligned");
+  int64_t total = 0;
+  for (int32_t i = 0; i < num; ++i) {
+    if (sizes[i] < 0 || sizes[i] > ((int64_t)1 << 40))
+      return fail(CTR_ERR_INVALID_ARGUMENT, "sizes[%d] out of [0, 2^40]", i);
+    total += sizes[i];
+    if (total > ((int64_t)1 << 40))
+      return fail(CTR_ERR_UNSUPPORTED, "more than 2^40 elements in all");
+    if (!elt_ok(dtypes[i]))
+      return fail(CTR_ERR_INVALID_ARGUMENT, "dtype %d of gradient %d is not a type", dtypes[i], i);
+    if (sizes[i] > 0 && !grads[i])
+      return fail(CTR_ERR_INVALID_ARGUMENT, "gradient %d is NULL", i);
+    if (!elt_aligned(grads[i], dtypes[i]))
+      return fail(CTR_ERR_UNSUPPORTED, "gradient %d is not aligned to its elements", i);
+  }
+  return CTR_OK;
+}
+
+static int32_t clip_workspace(int32_t num, const void* workspace, size_t* workspace_bytes,
+                              bool* query) {
+  *query = false;
+  if (!workspace_bytes) return fail(CTR_ERR_INVALID_ARGUMENT, "workspace_bytes is required");
+  if (num < 0 || num > 65536) return fail(CTR_ERR_INVALID_ARGUMENT, "num %d out of [0, 65536]", num);
+  const size_t need = ctr::grad_clip_workspace_bytes(num);
+  if (!workspace) {
+    *workspace_bytes = need;
+    *query = true;
+    return CTR_OK;
+  }
+  if (*workspace_bytes < need)
+    return fail(CTR_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need,
+                *workspace_bytes);
+  if (!aligned16(workspace)) return fail(CTR_ERR_UNSUPPORTED, "workspace is not 16-byte aligned");
+  return CTR_OK;
+}
+
+int32_t ctr_grad_clip(int32_t num, const void* const* grads, const int64_t* sizes,
+                      const int32_t* dtypes, void* const* outs, float max_norm, float* stats,
+                      void* workspace, size_t* workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  bool query;
+  int32_t st = clip_workspace(num, workspace, workspace_bytes, &query);
+  if (st || query) return st;
+  st = check_clip(num, grads, sizes, dtypes, max_norm, stats);
+  if (st) return st;
+  for (int32_t i = 0; outs && i < num; ++i)
+    if (!elt_aligned(outs[i], dtypes[i]))
+      return fail(CTR_ERR_UNSUPPORTED, "output %d is not aligned to its elements", i);
+  return hip_status(ctr::launch_grad_clip(num, grads, sizes, dtypes, outs, nullptr, false, 0.f,
+                                          max_norm, stats, workspace, (hipStream_t)stream),
+                    "ctr_grad_clip");
+}
+
+int32_t ctr_grad_clip_sgd(int32_t num, const void* const* grads, const int64_t* sizes,
+                          const int32_t* dtypes, void* const* params,
+                          const int32_t* param_dtypes, float lr, float max_norm, float* stats,
+                          void* workspace, size_t* workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  bool query;
+  int32_t st = clip_workspace(num, workspace, workspace_bytes, &query);
+  if (st || query) return st;
+  st = check_clip(num, grads, sizes, dtypes, max_norm, stats);
+  if (st) return st;
+  if (num > 0 && (!params || !param_dtypes))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "params and param_dtypes are required");
+  for (int32_t i = 0; i < num; ++i) {
+    if (!elt_ok(param_dtypes[i]))
+      return fail(CTR_ERR_INVALID_ARGUMENT, "dtype %d of parameter %d is not a type",
+                  param_dtypes[i], i);
+    if (sizes[i] > 0 && !params[i])
+      return fail(CTR_ERR_INVALID_ARGUMENT, "parameter %d is NULL", i);
+    if (!elt_aligned(params[i], param_dtypes[i]))
+      return fail(CTR_ERR_UNSUPPORTED, "parameter %d is not aligned to its elements", i);
+  }
+  return hip_status(ctr::launch_grad_clip(num, grads, sizes, dtypes, params, param_dtypes, true,
+                                          lr, max_norm, stats, workspace, (hipStream_t)stream),
+                    "ctr_grad_clip_sgd");
 }
 
 int32_t ctr_validate_csr(const void* indices, int32_t index_type, int64_t nnz,

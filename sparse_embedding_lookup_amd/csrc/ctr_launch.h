@@ -131,4 +131,45 @@ hipError_t launch_logistic_ne(const float* logits, int64_t ls, const float* labe
                               float* prob, float* dlogits, int64_t dls, float* stats,
                               hipStream_t s);
 
+// expert_rows.inl (dense.hip): router, sort by expert, rows there and back
+hipError_t launch_expert_route_fwd(const void* logits, int dtype, int64_t ls, int64_t T, int E,
+                                   int k, bool renorm, int32_t* experts, float* weights,
+                                   hipStream_t s);
+hipError_t launch_expert_route_bwd(const void* logits, int dtype, int64_t ls, int64_t T, int E,
+                                   int k, bool renorm, const int32_t* experts,
+                                   const float* weights, const float* dweights, void* dlogits,
+                                   int64_t dls, hipStream_t s);
+size_t expert_sort_workspace_bytes(int64_t n, int E);
+hipError_t launch_expert_sort(const int32_t* experts, int64_t n, int E, int32_t* offsets,
+                              int32_t* slots, int32_t* order, void* workspace, hipStream_t s);
+hipError_t launch_expert_dispatch(const void* X, int dtype, int64_t xs, int64_t T, int k, int D,
+                                  const int32_t* slots, const int32_t* offsets, int E, void* P,
+                                  int64_t ps, hipStream_t s);
+hipError_t launch_expert_combine_fwd(const void* P, int dtype, int64_t ps, int64_t T, int k,
+                                     int D, const int32_t* slots, const float* weights, void* Y,
+                                     int64_t ys, hipStream_t s);
+hipError_t launch_expert_combine_bwd(const void* dY, int dtype, int64_t dys, int64_t T, int k,
+                                     int D, const void* P, int64_t ps, const int32_t* slots,
+                                     const int32_t* offsets, int E, const float* weights,
+                                     void* dP, int64_t dps, float* dweights, hipStream_t s);
+
+// expert_dense.inl (dense.hip): the experts' fully connected layers
+hipError_t launch_expert_dense_fwd(const void* X, int dtype, int64_t xs, int64_t x_rows,
+                                   const int32_t* order, int k, const int32_t* offsets, int64_t n,
+                                   int E, int K, const void* W, const float* b, int N, bool relu,
+                                   void* Y, int64_t ys, hipStream_t s);
+size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtype);
+hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t x_rows,
+                                   const int32_t* order, int k, const int32_t* offsets, int64_t n,
+                                   int E, int K, const void* W, int N, bool x_relu,
+                                   const void* dY, int64_t dys, void* dX, int64_t dxs, float* dW,
+                                   float* db, void* workspace, hipStream_t s);
+
+// grad_clip.inl (dense.hip): the norm of many gradients and the clipped gradients or update
+size_t grad_clip_workspace_bytes(int num);
+hipError_t launch_grad_clip(int num, const void* const* grads, const int64_t* sizes,
+                            const int32_t* gtypes, void* const* outs, const int32_t* otypes,
+                            bool sgd, float lr, float max_norm, float* stats, void* workspace,
+                            hipStream_t s);
+
 }  // namespace ctr

@@ -34,10 +34,11 @@
 #include <type_traits>
 
 namespace ctr {
-namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+namespace {
 
 constexpr int kBM = 128, kBN = 128;
 // k-tile: 32.  A 64-wide bf16 k-tile doubles the bytes in flight per barrier, but its LDS
@@ -663,3 +664,9 @@ hipError_t launch_logistic_ne(const float* logits, int64_t ls, const float* labe
 }
 
 }  // namespace ctr
+
+// The experts and the gradient clipping belong to this translation unit, so that every
+// library linked from the sources' objects holds them with the dense layers.
+#include "expert_rows.inl"
+#include "expert_dense.inl"
+#include "grad_clip.inl"

@@ -35,6 +35,9 @@ EXPORTED = [
     "ctr_embbag_bwd_sgd_noalloc", "ctr_embbag_bwd_noalloc_scratch_bytes",
     "ctr_noalloc_scratch_capacity", "ctr_dot_interaction_gram_fwd",
     "ctr_dot_interaction_gram_bwd",
+    "ctr_expert_route_fwd", "ctr_expert_route_bwd", "ctr_expert_sort", "ctr_expert_dispatch",
+    "ctr_expert_combine_fwd", "ctr_expert_combine_bwd", "ctr_expert_dense_fwd",
+    "ctr_expert_dense_bwd", "ctr_grad_clip", "ctr_grad_clip_sgd",
 ]
 
 CTR_STEP_POOLED_INTERACTION, CTR_STEP_BATCH_MATRIX = 0, 1
@@ -131,6 +134,19 @@ def load() -> ctypes.CDLL:
         "ctr_dense_bwd_sgd": (i32, [P, i64, i64, i32, P, P, i32, i32, P, i64, P, i32, i64, i32,
                                     f32, P, i64, P, PS, P]),
         "ctr_logistic_ne": (i32, [P, i64, P, i64, P, P, i64, P, P]),
+        "ctr_expert_route_fwd": (i32, [P, i32, i64, i64, i32, i32, i32, P, P, P]),
+        "ctr_expert_route_bwd": (i32, [P, i32, i64, i64, i32, i32, i32, P, P, P, P, i64, P]),
+        "ctr_expert_sort": (i32, [P, i64, i32, i32, P, P, P, P, PS, P]),
+        "ctr_expert_dispatch": (i32, [P, i32, i64, i64, i32, i32, P, P, i32, P, i64, P]),
+        "ctr_expert_combine_fwd": (i32, [P, i32, i64, i64, i32, i32, P, P, P, i64, P]),
+        "ctr_expert_combine_bwd": (i32, [P, i32, i64, i64, i32, i32, P, i64, P, P, i32, P, P,
+                                         i64, P, P]),
+        "ctr_expert_dense_fwd": (i32, [P, i32, i64, i64, P, i32, P, i64, i32, i32, P, P, i32,
+                                       i32, P, i64, P]),
+        "ctr_expert_dense_bwd": (i32, [P, i32, i64, i64, P, i32, P, i64, i32, i32, P, i32, i32,
+                                       P, i64, P, i64, P, P, P, PS, P]),
+        "ctr_grad_clip": (i32, [i32, P, P, P, P, f32, P, P, PS, P]),
+        "ctr_grad_clip_sgd": (i32, [i32, P, P, P, P, P, f32, f32, P, P, PS, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -173,13 +189,14 @@ def _check(fn: str, status: int) -> None:
 class Call:
     """A libctr call whose arguments were marshalled once; calling it only reads the current
     stream (so it also works under stream capture) and checks the status."""
-    __slots__ = ("name", "fn", "args", "result")
+    __slots__ = ("name", "fn", "args", "result", "keep")
 
-    def __init__(self, name: str, args: tuple, result=None):
+    def __init__(self, name: str, args: tuple, result=None, keep=None):
         self.name = name
         self.fn = getattr(load(), name)
         self.args = args
         self.result = result
+        self.keep = keep                  # a workspace that the binding allocated for the call
 
     def __call__(self, stream=None):
         st = self.fn(*self.args, _stream(stream))
@@ -188,8 +205,8 @@ class Call:
         return self.result
 
 
-def _run(name: str, args: tuple, stream, prepare: bool, result=None):
-    call = Call(name, args, result)
+def _run(name: str, args: tuple, stream, prepare: bool, result=None, keep=None):
+    call = Call(name, args, result, keep)
     return call if prepare else call(stream)
 
 
@@ -605,6 +622,356 @@ def ctr_logistic_ne(logits: torch.Tensor, labels: torch.Tensor,
         stats = torch.empty(3, dtype=torch.float32, device=logits.device)
     args = (_ptr(logits), ls, _ptr(labels), M, _ptr(prob), _ptr(dlogits), dls, _ptr(stats))
     return _run("ctr_logistic_ne", args, stream, prepare, stats)
+
+
+# ------------------------------------------------------------------------------- experts
+_DTYPE_CODES = {torch.float32: CTR_F32, torch.bfloat16: CTR_BF16, torch.float16: CTR_F16}
+
+
+def _expert_arg(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
+                device: torch.device, rows: bool = False) -> int:
+    """The address of an argument of this shape, dtype and device; contiguous, or with `rows`
+    2-D with contiguous rows of any stride."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, not %s" % (name, t.device, device))
+    if rows:
+        _row_stride(t, name)
+    elif not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from one row of a 2-D tensor to the next; the rows are contiguous and do not
+    overlap."""
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    width, stride = t.shape[1], t.stride(0)
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if t.shape[0] <= 1:
+        return max(stride, width)
+    if stride < width:
+        raise ValueError("%s must have rows that do not overlap" % name)
+    return stride
+
+
+def _expert_type(t: torch.Tensor, name: str) -> int:
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be float32, bfloat16 or float16, not %s" % (name, t.dtype))
+    return code
+
+
+def ctr_expert_route_fwd(logits: torch.Tensor, k: int, renormalize: bool = True,
+                         experts: Optional[torch.Tensor] = None,
+                         weights: Optional[torch.Tensor] = None, stream=None,
+                         prepare: bool = False):
+    """The k experts of the largest logits of every token ([T, E]; rows may be strided), the
+    larger first, ties to the lower expert, and their softmax weights (over the chosen, or over
+    all experts): (experts int32 [T, k], weights fp32 [T, k]).  -inf closes an expert."""
+    code, ls = _expert_type(logits, "logits"), _row_stride(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    if experts is None:
+        experts = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    args = (logits.data_ptr(), code, ls, T, E, k, int(bool(renormalize)),
+            _expert_arg(experts, "experts", (T, k), torch.int32, dev),
+            _expert_arg(weights, "weights", (T, k), torch.float32, dev))
+    return _run("ctr_expert_route_fwd", args, stream, prepare, (experts, weights))
+
+
+def ctr_expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor,
+                         dweights: torch.Tensor, renormalize: bool = True,
+                         dlogits: Optional[torch.Tensor] = None, stream=None,
+                         prepare: bool = False):
+    """The gradient of the logits from that of the weights; experts and weights as the forward
+    gave them."""
+    code, ls = _expert_type(logits, "logits"), _row_stride(logits, "logits")
+    T, E = logits.shape
+    dev, k = logits.device, experts.shape[-1]
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    args = (logits.data_ptr(), code, ls, T, E, k, int(bool(renormalize)),
+            _expert_arg(experts, "experts", (T, k), torch.int32, dev),
+            _expert_arg(weights, "weights", (T, k), torch.float32, dev),
+            _expert_arg(dweights, "dweights", (T, k), torch.float32, dev),
+            _expert_arg(dlogits, "dlogits", (T, E), logits.dtype, dev, rows=True),
+            _row_stride(dlogits, "dlogits"))
+    return _run("ctr_expert_route_bwd", args, stream, prepare, dlogits)
+
+
+def expert_sort_workspace_bytes(T: int, k: int, num_experts: int) -> int:
+    """Workspace of ctr_expert_sort (the library's two-call query)."""
+    wsb = ctypes.c_size_t(0)
+    _check("ctr_expert_sort", load().ctr_expert_sort(None, T, k, num_experts, None, None, None,
+                                                     None, ctypes.byref(wsb), None))
+    return wsb.value
+
+
+def ctr_expert_sort(experts: torch.Tensor, num_experts: int,
+                    offsets: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                    order: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None,
+                    prepare: bool = False):
+    """The slots of experts [T, k] sorted by expert: (offsets int32 [E + 1], slots int32 [T, k],
+    order int32 [T * k]).  An expert outside [0, num_experts) drops its slot."""
+    if experts.dim() != 2:
+        raise ValueError("experts must be [T, k]")
+    T, k = experts.shape
+    dev = experts.device
+    if offsets is None:
+        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if order is None:
+        order = torch.empty(T * k, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = _workspace(expert_sort_workspace_bytes(T, k, num_experts), dev)
+    wsb = ctypes.c_size_t(workspace.numel())
+    args = (_expert_arg(experts, "experts", (T, k), torch.int32, dev), T, k, num_experts,
+            _expert_arg(offsets, "offsets", (num_experts + 1,), torch.int32, dev),
+            _expert_arg(slots, "slots", (T, k), torch.int32, dev),
+            _expert_arg(order, "order", (T * k,), torch.int32, dev), workspace.data_ptr(),
+            ctypes.byref(wsb))
+    return _run("ctr_expert_sort", args, stream, prepare, (offsets, slots, order),
+                workspace)
+
+
+def _slot_args(slots: torch.Tensor, offsets: Optional[torch.Tensor], dev):
+    if slots.dim() != 2:
+        raise ValueError("slots must be [T, k]")
+    T, k = slots.shape
+    sp = _expert_arg(slots, "slots", (T, k), torch.int32, dev)
+    if offsets is None:
+        return T, k, sp, None, 0
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be [num_experts + 1]")
+    return T, k, sp, _expert_arg(offsets, "offsets", offsets.shape, torch.int32, dev), \
+        offsets.shape[0] - 1
+
+
+def ctr_expert_dispatch(X: torch.Tensor, slots: torch.Tensor, offsets: torch.Tensor,
+                        P: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """The tokens' rows in the experts' order: P [T * k, D], P[slots[t, j]] = X[t]; positions of
+    no slot are zero."""
+    code, dev = _expert_type(X, "X"), X.device
+    xs, D = _row_stride(X, "X"), X.shape[1]
+    T, k, sp, op, E = _slot_args(slots, offsets, dev)
+    if P is None:
+        P = torch.empty((T * k, D), dtype=X.dtype, device=dev)
+    args = (_expert_arg(X, "X", (T, D), X.dtype, dev, rows=True), code, xs, T, k, D, sp, op, E,
+            _expert_arg(P, "P", (T * k, D), X.dtype, dev, rows=True), _row_stride(P, "P"))
+    return _run("ctr_expert_dispatch", args, stream, prepare, P)
+
+
+def ctr_expert_combine_fwd(P: torch.Tensor, slots: torch.Tensor,
+                           weights: Optional[torch.Tensor], Y: Optional[torch.Tensor] = None,
+                           stream=None, prepare: bool = False):
+    """Y[t] = sum_j weights[t, j] P[slots[t, j]] (weights None: 1, the gradient of
+    ctr_expert_dispatch)."""
+    code, dev = _expert_type(P, "P"), P.device
+    ps, D = _row_stride(P, "P"), P.shape[1]
+    T, k, sp, _, _ = _slot_args(slots, None, dev)
+    if Y is None:
+        Y = torch.empty((T, D), dtype=P.dtype, device=dev)
+    wp = None if weights is None else _expert_arg(weights, "weights", (T, k), torch.float32, dev)
+    args = (_expert_arg(P, "P", (T * k, D), P.dtype, dev, rows=True), code, ps, T, k, D, sp, wp,
+            _expert_arg(Y, "Y", (T, D), P.dtype, dev, rows=True), _row_stride(Y, "Y"))
+    return _run("ctr_expert_combine_fwd", args, stream, prepare, Y)
+
+
+def ctr_expert_combine_bwd(dY: torch.Tensor, P: Optional[torch.Tensor], slots: torch.Tensor,
+                           offsets: torch.Tensor, weights: Optional[torch.Tensor],
+                           dP: Optional[torch.Tensor] = None,
+                           dweights: Optional[torch.Tensor] = None, stream=None,
+                           prepare: bool = False):
+    """(dP [T * k, D], dweights fp32 [T, k]) of ctr_expert_combine_fwd; P None: dP alone (then
+    dweights is None)."""
+    code, dev = _expert_type(dY, "dY"), dY.device
+    dys, D = _row_stride(dY, "dY"), dY.shape[1]
+    T, k, sp, op, E = _slot_args(slots, offsets, dev)
+    if dP is None:
+        dP = torch.empty((T * k, D), dtype=dY.dtype, device=dev)
+    pp, ps, dwp = None, D, None
+    if P is not None:
+        pp = _expert_arg(P, "P", (T * k, D), dY.dtype, dev, rows=True)
+        ps = _row_stride(P, "P")
+        if dweights is None:
+            dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        dwp = _expert_arg(dweights, "dweights", (T, k), torch.float32, dev)
+    elif dweights is not None:
+        raise ValueError("dweights needs P")
+    wp = None if weights is None else _expert_arg(weights, "weights", (T, k), torch.float32, dev)
+    args = (_expert_arg(dY, "dY", (T, D), dY.dtype, dev, rows=True), code, dys, T, k, D, pp, ps,
+            sp, op, E, wp, _expert_arg(dP, "dP", (T * k, D), dY.dtype, dev, rows=True),
+            _row_stride(dP, "dP"), dwp)
+    return _run("ctr_expert_combine_bwd", args, stream, prepare, (dP, dweights))
+
+
+def _product_args(X, W, offsets, order, k):
+    """What the forward and the backward of the experts' layers share: their first arguments,
+    and n, E, N, K."""
+    code, dev = _expert_type(X, "X"), X.device
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K]")
+    E, N, K = W.shape
+    xs = _row_stride(X, "X")
+    if X.shape[1] != K:
+        raise ValueError("X must have W's %d columns, not %d" % (K, X.shape[1]))
+    n = X.shape[0]
+    op = None
+    if order is not None:
+        if order.dim() != 1:
+            raise ValueError("order must be [T * k]")
+        n = order.shape[0]
+        op = _expert_arg(order, "order", (n,), torch.int32, dev)
+    wp = _expert_arg(W, "W", (E, N, K), X.dtype, dev)
+    fp = _expert_arg(offsets, "offsets", (E + 1,), torch.int32, dev)
+    return (X.data_ptr(), code, xs, X.shape[0], op, k, fp, n, E, K, wp), n, E, N, K
+
+
+def ctr_expert_dense_fwd(X: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor],
+                         offsets: torch.Tensor, relu: bool,
+                         order: Optional[torch.Tensor] = None, k: int = 1,
+                         Y: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """Each expert's layer over its rows: Y [n, N] = act(x W[e]^T + b[e]) with W [E, N, K], b
+    fp32 [E, N] or None.  x is X [n, K] by position, or with `order` (ctr_expert_sort's, and its
+    k) the token's row X [T, K]."""
+    first, n, E, N, K = _product_args(X, W, offsets, order, k)
+    dev = X.device
+    if Y is None:
+        Y = torch.empty((n, N), dtype=X.dtype, device=dev)
+    bp = None if b is None else _expert_arg(b, "b", (E, N), torch.float32, dev)
+    args = first + (bp, N, int(bool(relu)),
+                    _expert_arg(Y, "Y", (n, N), X.dtype, dev, rows=True), _row_stride(Y, "Y"))
+    return _run("ctr_expert_dense_fwd", args, stream, prepare, Y)
+
+
+def expert_dense_bwd_workspace_bytes(n: int, num_experts: int, K: int, N: int,
+                                     dtype: int = CTR_BF16) -> int:
+    """Workspace of ctr_expert_dense_bwd (the library's two-call query)."""
+    wsb = ctypes.c_size_t(0)
+    _check("ctr_expert_dense_bwd", load().ctr_expert_dense_bwd(
+        None, dtype, K, n, None, 1, None, n, num_experts, K, None, N, 0, None, N, None, K, None,
+        None, None, ctypes.byref(wsb), None))
+    return wsb.value
+
+
+def ctr_expert_dense_bwd(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
+                         dY: torch.Tensor, order: Optional[torch.Tensor] = None, k: int = 1,
+                         x_relu: bool = False, bias: bool = True, want_dx: bool = True,
+                         want_dw: bool = True, dX: Optional[torch.Tensor] = None,
+                         dW: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None,
+                         prepare: bool = False):
+    """(dX [n, K] by position, dW fp32 [E, N, K], db fp32 [E, N]) from dY [n, N], the gradient
+    before the activation; x_relu: X is a rectified output, and dX the gradient before it.  What
+    is not wanted (bias, want_dx, want_dw) is None."""
+    first, n, E, N, K = _product_args(X, W, offsets, order, k)
+    dev = X.device
+    if want_dx and dX is None:
+        dX = torch.empty((n, K), dtype=X.dtype, device=dev)
+    if want_dw and dW is None:
+        dW = torch.empty((E, N, K), dtype=torch.float32, device=dev)
+    if bias and db is None:
+        db = torch.empty((E, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _workspace(expert_dense_bwd_workspace_bytes(n, E, K, N, first[1]), dev)
+    wsb = ctypes.c_size_t(workspace.numel())
+    args = first + (
+        N, int(bool(x_relu)), _expert_arg(dY, "dY", (n, N), X.dtype, dev, rows=True),
+        _row_stride(dY, "dY"),
+        _expert_arg(dX, "dX", (n, K), X.dtype, dev, rows=True) if want_dx else None,
+        _row_stride(dX, "dX") if want_dx else K,
+        _expert_arg(dW, "dW", (E, N, K), torch.float32, dev) if want_dw else None,
+        _expert_arg(db, "db", (E, N), torch.float32, dev) if bias else None,
+        workspace.data_ptr(), ctypes.byref(wsb))
+    return _run("ctr_expert_dense_bwd", args, stream, prepare,
+                (dX if want_dx else None, dW if want_dw else None, db if bias else None),
+                workspace)
+
+
+# --------------------------------------------------------------------- gradient clipping
+def grad_clip_workspace_bytes(num: int) -> int:
+    """Workspace of ctr_grad_clip and ctr_grad_clip_sgd (the library's two-call query)."""
+    wsb = ctypes.c_size_t(0)
+    _check("ctr_grad_clip", load().ctr_grad_clip(num, None, None, None, None, 0.0, None, None,
+                                                 ctypes.byref(wsb), None))
+    return wsb.value
+
+
+def _tensor_list(ts, name: str, sizes=None, dtypes=None, device=None):
+    """Host arrays of the addresses, element counts and types of contiguous tensors."""
+    num = len(ts)
+    ptrs, counts, codes = [], [], []
+    for i, t in enumerate(ts):
+        code = _DTYPE_CODES.get(t.dtype)
+        if code is None:
+            raise TypeError("%s[%d] must be float32, bfloat16 or float16, not %s"
+                            % (name, i, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s[%d] must be contiguous" % (name, i))
+        if device is not None and t.device != device:
+            raise ValueError("%s[%d] is on %s, not %s" % (name, i, t.device, device))
+        ptrs.append(t.data_ptr())
+        counts.append(t.numel())
+        codes.append(code)
+    if sizes is not None and counts != sizes:
+        raise ValueError("%s and grads differ in number or sizes" % name)
+    if dtypes is not None and codes != dtypes:
+        raise TypeError("%s and grads differ in type" % name)
+    return (ctypes.c_void_p * num)(*ptrs), counts, codes
+
+
+def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepare, out_name):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    dev = grads[0].device
+    gp, counts, codes = _tensor_list(grads, "grads", device=dev)
+    num = len(grads)
+    if stats is None:
+        stats = torch.empty(2, dtype=torch.float32, device=dev)
+    sp = _expert_arg(stats, "stats", (2,), torch.float32, dev)
+    if workspace is None:
+        workspace = _workspace(grad_clip_workspace_bytes(num), dev)
+    wsb = ctypes.c_size_t(workspace.numel())
+    head = (num, gp, (ctypes.c_int64 * num)(*counts), (ctypes.c_int32 * num)(*codes))
+    tail = (float(max_norm), sp, workspace.data_ptr(), ctypes.byref(wsb))
+    if lr is None:
+        op = None if outs is None else _tensor_list(list(outs), out_name, counts, codes, dev)[0]
+        return _run(name, head + (op,) + tail, stream, prepare, stats, workspace)
+    pp, _, pcodes = _tensor_list(list(outs), out_name, counts, None, dev)
+    return _run(name, head + (pp, (ctypes.c_int32 * num)(*pcodes), float(lr)) + tail, stream,
+                prepare, stats, workspace)
+
+
+def ctr_grad_clip(grads: Sequence[torch.Tensor], max_norm: float,
+                  outs: Optional[Sequence[torch.Tensor]] = None,
+                  stats: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """Scales the gradients (contiguous tensors of any of the three types) so that the norm of
+    them all is at most max_norm, in place or into `outs` (same sizes and types); returns stats
+    [norm, scale] (device)."""
+    return _clip_call("ctr_grad_clip", grads, outs, None, max_norm, stats, workspace, stream,
+                      prepare, "outs")
+
+
+def ctr_grad_clip_sgd(grads: Sequence[torch.Tensor], params: Sequence[torch.Tensor], lr: float,
+                      max_norm: float, stats: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None,
+                      prepare: bool = False):
+    """The SGD step with the clipped gradients, params -= lr * scale * grads in place; the
+    gradients are kept.  Returns stats [norm, scale] (device)."""
+    return _clip_call("ctr_grad_clip_sgd", grads, params, lr, max_norm, stats, workspace, stream,
+                      prepare, "params")
 
 
 def ctr_init_tables_hash(table: torch.Tensor, rows: Sequence[int], seed: int,

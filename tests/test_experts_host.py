@@ -1,0 +1,225 @@
+"""Refusals of the expert operators and the gradient clipping, on the host alone: every call
+below fails its checks before any HIP call, or is a workspace query, so the addresses are never
+used.  The definitions the GPU tests compare with are checked here too."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from sparse_embedding_lookup_amd import ctr
+from tests import experts_ref as ref
+
+A = ctypes.c_void_p(0x10000)
+ODD = ctypes.c_void_p(0x10001)
+BAD, UNS, SMALL = ctr.CTR_ERR_INVALID_ARGUMENT, ctr.CTR_ERR_UNSUPPORTED, \
+    ctr.CTR_ERR_WORKSPACE_TOO_SMALL
+
+
+def lib():
+    if not os.path.exists(ctr.LIB_PATH):
+        from sparse_embedding_lookup_amd import build
+        build.build()
+    return ctr.load()
+
+
+def check(call, ok, cases):
+    for want, change in cases:
+        assert set(change) <= set(ok)
+        assert call(**dict(ok, **change)) == want, change
+        assert lib().ctr_last_error_message() != b"", change
+
+
+def test_route_refusals():
+    ok = dict(x=A, dt=0, ls=8, T=4, E=8, k=2, re=1, e=A, w=A, dw=A, dl=A, dls=8)
+    cases = [(BAD, dict(x=None)), (BAD, dict(dt=3)), (BAD, dict(dt=-1)), (BAD, dict(ls=7)),
+             (BAD, dict(T=-1)), (BAD, dict(E=0)), (BAD, dict(k=0)), (BAD, dict(k=9)),
+             (UNS, dict(E=1025, ls=2000, dls=2000)), (UNS, dict(T=1 << 26)), (UNS, dict(x=ODD)),
+             (UNS, dict(E=100, k=65, ls=100, dls=100)), (BAD, dict(e=None)), (BAD, dict(w=None)),
+             (UNS, dict(e=ODD)), (UNS, dict(w=ODD))]
+
+    def fwd(**a):
+        return lib().ctr_expert_route_fwd(a["x"], a["dt"], a["ls"], a["T"], a["E"], a["k"],
+                                          a["re"], a["e"], a["w"], None)
+
+    def bwd(**a):
+        return lib().ctr_expert_route_bwd(a["x"], a["dt"], a["ls"], a["T"], a["E"], a["k"],
+                                          a["re"], a["e"], a["w"], a["dw"], a["dl"], a["dls"],
+                                          None)
+    check(fwd, ok, cases)
+    check(bwd, ok, cases + [(BAD, dict(dw=None)), (BAD, dict(dl=None)), (BAD, dict(dls=7)),
+                            (UNS, dict(dw=ODD)), (UNS, dict(dl=ODD, dt=1))])
+
+
+def test_sort_refusals():
+    ok = dict(e=A, T=100, k=2, E=8, o=A, s=A, p=A, ws=A, wsb=1 << 20)
+
+    def call(**a):
+        b = None if a["wsb"] is None else ctypes.byref(ctypes.c_size_t(a["wsb"]))
+        return lib().ctr_expert_sort(a["e"], a["T"], a["k"], a["E"], a["o"], a["s"], a["p"],
+                                     a["ws"], b, None)
+    check(call, ok, [(BAD, dict(e=None)), (BAD, dict(T=-1)), (BAD, dict(k=0)), (BAD, dict(E=0)),
+                     (UNS, dict(E=1025)), (UNS, dict(k=65)), (BAD, dict(o=None)),
+                     (BAD, dict(s=None)), (BAD, dict(p=None)), (SMALL, dict(wsb=8)),
+                     (BAD, dict(wsb=None)), (UNS, dict(ws=ctypes.c_void_p(0x10008))),
+                     (UNS, dict(e=ODD)), (UNS, dict(p=ODD)), (UNS, dict(T=1 << 25, k=64))])
+    assert ctr.expert_sort_workspace_bytes(0, 2, 8) >= 1
+    assert ctr.expert_sort_workspace_bytes(1 << 20, 2, 1024) <= 256 * 1024 * 4
+
+
+def test_row_refusals():
+    ok = dict(x=A, dt=1, xs=64, T=4, k=2, D=64, s=A, o=A, E=4, w=A, p=A, ps=64, y=A, ys=64, dw=A)
+
+    def dispatch(**a):
+        return lib().ctr_expert_dispatch(a["x"], a["dt"], a["xs"], a["T"], a["k"], a["D"], a["s"],
+                                         a["o"], a["E"], a["y"], a["ys"], None)
+
+    def fwd(**a):
+        return lib().ctr_expert_combine_fwd(a["x"], a["dt"], a["xs"], a["T"], a["k"], a["D"],
+                                            a["s"], a["w"], a["y"], a["ys"], None)
+
+    def bwd(**a):
+        return lib().ctr_expert_combine_bwd(a["x"], a["dt"], a["xs"], a["T"], a["k"], a["D"],
+                                            a["p"], a["ps"], a["s"], a["o"], a["E"], a["w"],
+                                            a["y"], a["ys"], a["dw"], None)
+    both = [(BAD, dict(x=None)), (BAD, dict(dt=7)), (BAD, dict(xs=63)), (BAD, dict(T=-1)),
+            (BAD, dict(k=0)), (BAD, dict(D=0)), (BAD, dict(D=65537, xs=1 << 17, ys=1 << 17)),
+            (BAD, dict(s=None)), (BAD, dict(y=None)), (BAD, dict(ys=63)), (UNS, dict(x=ODD)),
+            (UNS, dict(y=ODD)), (UNS, dict(s=ODD)), (UNS, dict(T=1 << 26))]
+    check(dispatch, ok, both + [(BAD, dict(o=None)), (BAD, dict(E=0)), (UNS, dict(E=2000))])
+    check(fwd, ok, both + [(UNS, dict(w=ODD))])
+    check(bwd, ok, both + [(BAD, dict(o=None)), (BAD, dict(p=None)), (BAD, dict(ps=63)),
+                           (UNS, dict(p=ODD)), (UNS, dict(dw=ODD))])
+
+
+def test_product_refusals():
+    ok = dict(x=A, dt=1, xs=64, xr=100, at=None, k=1, o=A, n=100, E=4, K=64, W=A, b=A, N=32, r=1,
+              y=A, ys=64, dy=A, dys=32, dw=A, db=A, ws=A, wsb=1 << 30)
+
+    def fwd(**a):
+        return lib().ctr_expert_dense_fwd(a["x"], a["dt"], a["xs"], a["xr"], a["at"], a["k"],
+                                          a["o"], a["n"], a["E"], a["K"], a["W"], a["b"], a["N"],
+                                          a["r"], a["y"], a["ys"], None)
+
+    def bwd(**a):
+        b = None if a["wsb"] is None else ctypes.byref(ctypes.c_size_t(a["wsb"]))
+        return lib().ctr_expert_dense_bwd(a["x"], a["dt"], a["xs"], a["xr"], a["at"], a["k"],
+                                          a["o"], a["n"], a["E"], a["K"], a["W"], a["N"], a["r"],
+                                          a["dy"], a["dys"], a["y"], a["ys"], a["dw"], a["db"],
+                                          a["ws"], b, None)
+    both = [(BAD, dict(x=None)), (BAD, dict(dt=4)), (BAD, dict(xs=63)), (BAD, dict(xr=99)),
+            (BAD, dict(xr=-1)), (BAD, dict(n=-1)), (BAD, dict(n=1 << 31)), (BAD, dict(E=0)),
+            (UNS, dict(E=1025)), (BAD, dict(K=0)), (BAD, dict(N=0)), (BAD, dict(K=65537, xs=1 << 17)),
+            (BAD, dict(at=A, k=0)), (BAD, dict(o=None)), (BAD, dict(W=None)), (UNS, dict(x=ODD)),
+            (UNS, dict(W=ODD)), (UNS, dict(y=ODD)), (UNS, dict(o=ODD)), (UNS, dict(at=ODD)),
+            (UNS, dict(n=(1 << 31) - 1, xr=(1 << 31) - 1))]
+    check(fwd, ok, both + [(BAD, dict(ys=31)), (BAD, dict(y=None)), (UNS, dict(b=ODD))])
+    check(bwd, ok, both + [(BAD, dict(ys=63)), (BAD, dict(dy=None)), (BAD, dict(dys=31)),
+                           (UNS, dict(dy=ODD)), (UNS, dict(dw=ODD)), (UNS, dict(db=ODD)),
+                           (BAD, dict(wsb=None)), (SMALL, dict(wsb=1)),
+                           (UNS, dict(ws=ctypes.c_void_p(0x10008)))])
+
+
+def test_clip_refusals():
+    ok = dict(num=2, g=[0x10000, 0x20000], n=[5, 6], dt=[0, 1], p=[0x30000, 0x40000], pt=[0, 0],
+              mx=1.0, st=A, ws=A, wsb=1 << 20)
+
+    def arrays(a):
+        def make(t, v):
+            return None if v is None else (t * len(v))(*v)
+        return (make(ctypes.c_void_p, a["g"]), make(ctypes.c_int64, a["n"]),
+                make(ctypes.c_int32, a["dt"]), make(ctypes.c_void_p, a["p"]),
+                make(ctypes.c_int32, a["pt"]))
+
+    def clip(**a):
+        g, n, dt, p, _ = arrays(a)
+        b = None if a["wsb"] is None else ctypes.byref(ctypes.c_size_t(a["wsb"]))
+        return lib().ctr_grad_clip(a["num"], g, n, dt, p, a["mx"], a["st"], a["ws"], b, None)
+
+    def sgd(**a):
+        g, n, dt, p, pt = arrays(a)
+        b = None if a["wsb"] is None else ctypes.byref(ctypes.c_size_t(a["wsb"]))
+        return lib().ctr_grad_clip_sgd(a["num"], g, n, dt, p, pt, 0.1, a["mx"], a["st"], a["ws"],
+                                       b, None)
+    both = [(BAD, dict(num=-1)), (BAD, dict(num=65537)), (BAD, dict(g=None)), (BAD, dict(n=None)),
+            (BAD, dict(dt=None)), (BAD, dict(dt=[0, 3])), (BAD, dict(n=[5, -1])),
+            (BAD, dict(g=[0x10000, None])), (UNS, dict(g=[0x10002, 0x20000])),
+            (UNS, dict(n=[1 << 40, 1 << 40])), (BAD, dict(mx=-1.0)), (BAD, dict(mx=float("nan"))),
+            (BAD, dict(st=None)), (UNS, dict(st=ODD)), (SMALL, dict(wsb=8)), (BAD, dict(wsb=None)),
+            (UNS, dict(ws=ctypes.c_void_p(0x10008)))]
+    check(clip, ok, both + [(UNS, dict(p=[0x30000, 0x40001]))])
+    check(sgd, ok, both + [(BAD, dict(p=None)), (BAD, dict(pt=None)), (BAD, dict(pt=[0, 9])),
+                           (BAD, dict(p=[0x30000, None])), (UNS, dict(p=[0x30000, 0x40002]))])
+
+
+def test_binding_refusals():
+    """What the binding sees before the library: types, shapes, strides, devices."""
+    f, i = torch.zeros, torch.int32
+    with pytest.raises(TypeError):
+        ctr.ctr_expert_route_fwd(f(4, 8, dtype=torch.float64), 2)
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_route_fwd(f(8, 4).t(), 2)
+    with pytest.raises(TypeError):
+        ctr.ctr_expert_sort(f(4, 2, dtype=torch.int64), 8)
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_sort(f(8, dtype=i), 8)
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_dispatch(f(4, 8), f(5, 2, dtype=i), f(4, dtype=i))
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_combine_fwd(f(8, 8), f(4, 2, dtype=i), f(4, 3))
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_combine_fwd(f(1, 8).expand(8, 8), f(4, 2, dtype=i), None)
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_combine_bwd(f(4, 8), None, f(4, 2, dtype=i), f(4, dtype=i), None,
+                                   dweights=f(4, 2))
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_dense_fwd(f(4, 8), f(2, 4, 7), None, f(3, dtype=i), False)
+    with pytest.raises(TypeError):
+        ctr.ctr_expert_dense_fwd(f(4, 8), f(2, 4, 8, dtype=torch.bfloat16), None, f(3, dtype=i),
+                                 False)
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_dense_bwd(f(4, 8), f(2, 4, 8), f(3, dtype=i), f(5, 4))
+    with pytest.raises(ValueError):
+        ctr.ctr_grad_clip([], 1.0)
+    with pytest.raises(ValueError):
+        ctr.ctr_grad_clip([f(4, 8).t()], 1.0)
+    with pytest.raises(TypeError):
+        ctr.ctr_grad_clip([f(4, dtype=torch.float64)], 1.0)
+    with pytest.raises(ValueError):
+        ctr.ctr_grad_clip([f(4)], 1.0, [f(5)])
+    with pytest.raises(TypeError):
+        ctr.ctr_grad_clip([f(4)], 1.0, [f(4, dtype=torch.float16)])
+    with pytest.raises(ValueError):
+        ctr.ctr_grad_clip_sgd([f(4)], [f(4), f(4)], 0.1, 1.0)
+
+
+def test_definitions_agree_with_autograd():
+    """The written-out gradients of tests/experts_ref.py against torch's own, in 64 bits."""
+    g = torch.Generator().manual_seed(0)
+    T, k, E, K, N = 20, 2, 4, 6, 5
+    x = torch.randn((T, E), generator=g).double().requires_grad_()
+    dw = torch.randn((T, k), generator=g).double()
+    for renorm in (True, False):
+        experts, weights = ref.route_fwd(x.detach(), k, renorm)
+        at = experts.long()
+        z = x.gather(1, at) if renorm else x
+        w = torch.exp(x.gather(1, at) - torch.logsumexp(z, 1, keepdim=True))
+        assert torch.allclose(w, weights)
+        want, = torch.autograd.grad((w * dw).sum(), x)
+        assert torch.allclose(ref.route_bwd(x.detach(), experts, dw, renorm), want)
+    offsets, slots, order = ref.sort(experts, E)
+    X = torch.randn((T, K), generator=g).double().requires_grad_()
+    W = torch.randn((E, N, K), generator=g).double().requires_grad_()
+    b = torch.randn((E, N), generator=g).double().requires_grad_()
+    v = torch.rand((T, k), generator=g).double().requires_grad_()
+    # token by token: sum_j v_j (W[e_j] x + b[e_j])
+    y = torch.einsum("tj,tjn->tn", v, torch.einsum("tjnk,tk->tjn", W[at], X) + b[at])
+    H, _ = ref.dense_fwd(X.detach(), W.detach(), b.detach(), offsets, False, order, k, T * k)
+    assert torch.allclose(ref.combine_fwd(H, slots, v.detach())[0], y)
+    dY = torch.randn((T, N), generator=g).double()
+    want = torch.autograd.grad((y * dY).sum(), [X, W, b, v])
+    dH, dv, _ = ref.combine_bwd(dY, H, slots, v.detach())
+    got = ref.dense_bwd(X.detach(), W.detach(), offsets, dH, order, k, False)
+    dX, _ = ref.combine_fwd(got["dX"][0], slots, None)
+    for a, c in zip((dX, got["dW"][0], got["db"][0], dv), want):
+        assert torch.allclose(a, c)
