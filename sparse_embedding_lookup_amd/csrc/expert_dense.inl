@@ -33,7 +33,10 @@ struct Product {
   int64_t dys;
   void* Y;                      // Y, or dX
   int64_t ys;
-  float* dW;                    // dW, or its partial sums
+  float* dW;
+  float* part;                  // partial sums of dW
+  int64_t slice;                // positions a slice of dW's reduction
+  bool slice_big;               //   in 256 x 256 tiles
   int col_tiles, row_tiles;
 };
 
@@ -242,6 +245,448 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product g) {
   }
 }
 
+// Row tiles that the experts (and the positions of none) need.
+template <int BM>
+__device__ __forceinline__ int64_t count_tiles(const Product& g) {
+  const int lane = threadIdx.x & 63;
+  int tiles = 0;
+  for (int e = lane; e <= g.E; e += 64) {
+    int64_t lo, hi;
+    bounds_of(g, e, &lo, &hi);
+    tiles += (int)((hi - lo + BM - 1) / BM);
+  }
+  for (int d = 1; d < 64; d <<= 1) tiles += __shfl_xor(tiles, d);
+  return tiles;
+}
+
+// The block's tile among rows * inner tiles, inner first: blocks go to the 8 XCDs in turn, and
+// each XCD, which has an L2 of its own, gets a run of neighbouring tiles that share operands.
+// The split is over the tiles that there are, not over the grid, which has more.
+__device__ __forceinline__ bool place_tile(const Product& g, int64_t rows, int inner,
+                                           int64_t* row, int* in) {
+  const uint32_t total = (uint32_t)(rows * inner), b = blockIdx.x, per = total / kXcds;
+  if (b >= total) return false;
+  const uint32_t t = b < per * kXcds ? (b % kXcds) * per + b / kXcds : b;
+  *row = t / (uint32_t)inner;
+  *in = (int)(t % (uint32_t)inner);
+  return true;
+}
+
+// The weight gradient's reduction is cut into slices of g.slice positions, so that an expert
+// with many rows is many blocks' work: expert e has max(1, ceil(rows / slice)) of them.  One
+// slice writes dW itself; the sums of several go to g.part, in order, and are added after.
+struct Slice {
+  int expert, count;            // slices of this expert
+  int64_t lo, hi, partial;      // its positions; place among the partial sums, or -1
+};
+__device__ __forceinline__ int slices_of(const Product& g, int e, int64_t* lo, int64_t* hi) {
+  bounds_of(g, e, lo, hi);
+  const int c = (int)((*hi - *lo + g.slice - 1) / g.slice);
+  return c > 1 ? c : 1;
+}
+__device__ __forceinline__ int64_t count_slices(const Product& g) {
+  const int lane = threadIdx.x & 63;
+  int c = 0;
+  for (int e = lane; e < g.E; e += 64) {
+    int64_t lo, hi;
+    c += slices_of(g, e, &lo, &hi);
+  }
+  for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d);
+  return c;
+}
+// Slice `unit` of all, or (expert >= 0) the first of that expert.
+__device__ __forceinline__ bool find_slice(const Product& g, int64_t unit, int expert, Slice* u) {
+  const int lane = threadIdx.x & 63;
+  int64_t run = 0, partials = 0;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    const int e = e0 + lane;
+    int64_t lo = 0, hi = 0;
+    const int c = e < g.E ? slices_of(g, e, &lo, &hi) : 0;
+    const int m = c > 1 ? c : 0;
+    int upto = c, mupto = m;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(upto, d), x = __shfl_up(mupto, d);
+      if (lane >= d) {
+        upto += v;
+        mupto += x;
+      }
+    }
+    const uint64_t hit = expert >= 0 ? __ballot(e == expert) : __ballot(run + upto > unit);
+    if (hit) {
+      const int at = __ffsll((unsigned long long)hit) - 1;
+      const int64_t i = expert >= 0 ? 0 : unit - run - __shfl(upto - c, at);
+      const int64_t first = __shfl(lo, at), last = __shfl(hi, at);
+      u->expert = e0 + at;
+      u->count = __shfl(c, at);
+      u->lo = first + i * g.slice;
+      u->hi = last < u->lo + g.slice ? last : u->lo + g.slice;
+      u->partial = u->count > 1 ? partials + __shfl(mupto - m, at) + i : -1;
+      return true;
+    }
+    run += __shfl(upto, 63);
+    partials += __shfl(mupto, 63);
+  }
+  return false;
+}
+
+// dW of the experts with several slices: their partial sums added in order.  A block has
+// kJoin elements of one expert.
+constexpr int kJoin = 8192;
+__global__ __launch_bounds__(kThreads) void join_kernel(Product g) {
+  const int64_t count = (int64_t)g.N * g.K;
+  const int64_t each = (count + kJoin - 1) / kJoin;
+  const int e = (int)(blockIdx.x / each);
+  Slice u;
+  if (!find_slice(g, 0, e, &u) || u.count < 2) return;
+  const float* part = g.part + u.partial * count;
+  float* out = g.dW + e * count;
+  const int64_t begin = (blockIdx.x % each) * kJoin;
+  const int64_t end = count < begin + kJoin ? count : begin + kJoin;
+  for (int64_t i = begin + threadIdx.x * 4; i < end; i += kThreads * 4) {   // count % 4 == 0
+    float4 s = *reinterpret_cast<const float4*>(part + i);
+    for (int z = 1; z < u.count; ++z) {
+      const float4 x = *reinterpret_cast<const float4*>(part + z * count + i);
+      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    *reinterpret_cast<float4*>(out + i) = s;
+  }
+}
+
+// The 16-bit values of h where those of m are positive, else zero.
+template <int TY>
+__device__ __forceinline__ uint32_t keep_positive(uint32_t h, uint32_t m) {
+  return (half_lo<TY>(m) > 0.f ? h & 0xFFFFu : 0u) | (half_hi<TY>(m) > 0.f ? h & 0xFFFF0000u : 0u);
+}
+
+// ------------------------------------------------------------------ 16-bit operands, staged
+// The products of 16-bit operands in 16-byte pieces (widths and strides multiples of 8,
+// 16-byte aligned arrays).  A block has a BM x BN output tile and a wave a WM x WN part of it
+// in 32 x 32 matrix-core tiles; the reduction advances 64 at a time through two LDS buffers.
+// Tiles go from memory to LDS directly (one 16-byte load a lane, 1 KB a wave, no registers in
+// between), those of the next step while this step's products run; one barrier a step.
+//
+// An operand lies in LDS in one of two forms:
+//   by rows (64 reduction values of one row, 128 bytes): a fragment is one 16-byte read.
+//     The 16-byte piece c of row r is at c ^ (r & 7), so that eight lanes that read piece c
+//     of eight rows touch all banks.
+//   by reduction (BM or BN values of one reduction index): a fragment is two transposing
+//     reads, each giving a lane four reduction values of its row.  Sixteen lanes read four
+//     reduction rows of 32 bytes; piece c of reduction row q is at c ^ (2 (q & 3)), which
+//     spreads the four over the banks.
+// The matrix cores take the columns as their rows: a lane then holds four neighbouring
+// columns of one output row, stored together.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kStep = 64;                      // reduction values a step
+
+template <int TY>
+__device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
+  if constexpr (TY == kEltBF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// 16 bytes a lane from base + off to lds + 16 * lane (lds the same in the whole wave).
+__device__ __forceinline__ void to_lds(const char* base, uint32_t off, uint16_t* lds) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)(base + off),
+      (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void zero_lds(uint16_t* lds, int lane) {
+  *reinterpret_cast<uint4*>(lds + 8 * lane) = make_uint4(0, 0, 0, 0);
+}
+
+template <int TY, int KIND, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Product g) {
+  constexpr int WAVES = (BM / WM) * (BN / WN), WN_WAVES = BN / WN;
+  constexpr bool AROW = KIND != kWeight, BROW = KIND == kForward;
+  constexpr int TI = WM / 32, TJ = WN / 32;
+  constexpr int AE = BM * kStep / 512 / WAVES, BE = BN * kStep / 512 / WAVES;
+  __shared__ __attribute__((aligned(16))) uint16_t A0[BM * kStep], A1[BM * kStep];
+  __shared__ __attribute__((aligned(16))) uint16_t B0[BN * kStep], B1[BN * kStep];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w / WN_WAVES, wn = w % WN_WAVES;
+
+  // which tile
+  int e;
+  int64_t row0, end, r0 = 0, r1;
+  int n0;
+  float* dW = g.dW;
+  if constexpr (KIND == kWeight) {
+    Slice u;
+    int64_t unit;
+    int tile;
+    if (!place_tile(g, count_slices(g), g.row_tiles * g.col_tiles, &unit, &tile)) return;
+    if (!find_slice(g, unit, -1, &u)) return;
+    e = u.expert;
+    r0 = u.lo;
+    r1 = u.hi;
+    if (u.partial >= 0) dW = g.part + u.partial * g.N * g.K;
+    else dW += (int64_t)e * g.N * g.K;
+    row0 = (int64_t)(tile / g.col_tiles) * BM;
+    n0 = tile % g.col_tiles * BN;
+    end = g.N;
+  } else {
+    int64_t mt;
+    if (!place_tile(g, count_tiles<BM>(g), g.col_tiles, &mt, &n0)) return;
+    n0 *= BN;
+    if (!find_tile<BM>(g, mt, &e, &row0, &end)) return;
+    r1 = e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
+  }
+  const int cols = KIND == kForward ? g.N : g.K;
+  const uint16_t* W = static_cast<const uint16_t*>(g.W) + (int64_t)(e < g.E ? e : 0) * g.N * g.K;
+
+  // Lane addresses.  By rows: lane i of piece q has row 8 q + i / 8 and its 16 bytes
+  // (i % 8) ^ (i / 8); rows past the end read the tile's first row, and are not stored.
+  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;          // bytes along the reduction
+  const char *abase, *bbase;
+  uint32_t aoff[AE], boff[BE];
+  if constexpr (AROW) {
+    const uint16_t* base = static_cast<const uint16_t*>(KIND == kForward ? g.X : g.dY);
+    const int64_t ld = KIND == kForward ? g.xs : g.dys;
+    const bool gather = KIND == kForward && g.order;
+    if (!gather) base += row0 * ld;
+    abase = reinterpret_cast<const char*>(base);
+#pragma unroll
+    for (int q = 0; q < AE; ++q) {
+      const int64_t r = row0 + 8 * (q * WAVES + w) + (lane >> 3);
+      const int64_t p = r < end ? r : row0;
+      int64_t x = p - row0;
+      if (gather) {
+        x = x_row(g, p);
+        x = x < 0 ? 0 : x;
+      }
+      aoff[q] = (uint32_t)(x * ld * 2) + piece;
+    }
+  } else {
+    // columns of dY; a reduction row is BM * 2 bytes
+    abase = reinterpret_cast<const char*>(static_cast<const uint16_t*>(g.dY) + row0);
+  }
+  if constexpr (BROW) {
+    bbase = reinterpret_cast<const char*>(W + (int64_t)n0 * g.K);
+#pragma unroll
+    for (int q = 0; q < BE; ++q) {
+      const int r = 8 * (q * WAVES + w) + (lane >> 3);
+      boff[q] = (uint32_t)((n0 + r < cols ? r : 0) * (int64_t)g.K * 2) + piece;
+    }
+  }
+
+  // Loads one step's operands: reduction values [k, k + 64).
+  auto load_row = [&](const char* base, const uint32_t* off, int each, uint16_t* lds, int64_t k,
+                      auto count) {
+    const char* at = base + k * 2;
+    if (k + kStep <= r1) {
+#pragma unroll
+      for (int q = 0; q < decltype(count)::value; ++q)
+        to_lds(at, off[q], lds + (q * WAVES + w) * 512);
+    } else {
+      const bool in = k + piece / 2 < r1;
+#pragma unroll
+      for (int q = 0; q < decltype(count)::value; ++q) {
+        if (in) to_lds(at, off[q], lds + (q * WAVES + w) * 512);
+        else zero_lds(lds + (q * WAVES + w) * 512, lane);
+      }
+    }
+  };
+  // by reduction: a piece of 512 elements is 512 / WIDE reduction rows of WIDE elements
+  auto load_red = [&](const char* base, int64_t ld, int limit, uint16_t* lds, int64_t k,
+                      auto count, auto wide, auto row_of) {
+    constexpr int WIDE = decltype(wide)::value, PER = 512 / WIDE, LANES = 64 / PER;
+#pragma unroll
+    for (int q = 0; q < decltype(count)::value; ++q) {
+      const int kr = (q * WAVES + w) * PER + lane / LANES;     // reduction row in the step
+      const int c = ((lane % LANES) ^ (2 * (kr & 3))) * 8;     // first column
+      const int64_t x = row_of(k + kr);
+      if (x >= 0)
+        to_lds(base + (c < limit ? c : 0) * 2 + x * ld * 2, 0, lds + (q * WAVES + w) * 512);
+      else
+        zero_lds(lds + (q * WAVES + w) * 512, lane);
+    }
+  };
+  auto load = [&](uint16_t* A, uint16_t* B, int64_t k) {
+    if constexpr (AROW)
+      load_row(abase, aoff, AE, A, k, std::integral_constant<int, AE>{});
+    else
+      load_red(abase, g.dys, (int)(end - row0), A, k, std::integral_constant<int, AE>{},
+               std::integral_constant<int, BM>{},
+               [&](int64_t p) { return p < r1 ? p : (int64_t)-1; });
+    if constexpr (BROW)
+      load_row(bbase, boff, BE, B, k, std::integral_constant<int, BE>{});
+    else if constexpr (KIND == kInput)
+      load_red(reinterpret_cast<const char*>(W + n0), g.K, cols - n0, B, k,
+               std::integral_constant<int, BE>{}, std::integral_constant<int, BN>{},
+               [&](int64_t n) { return n < r1 ? n : (int64_t)-1; });
+    else
+      load_red(reinterpret_cast<const char*>(static_cast<const uint16_t*>(g.X) + n0), g.xs,
+               cols - n0, B, k, std::integral_constant<int, BE>{},
+               std::integral_constant<int, BN>{},
+               [&](int64_t p) { return p < r1 ? x_row(g, p) : (int64_t)-1; });
+  };
+
+  f32x16 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  const int rl = lane & 31, kg = lane >> 5;
+  // fragment of 32 rows from `row`, reduction values 16 s + 8 kg .. + 8
+  auto frag = [&](const uint16_t* L, int row, int s, auto byrow, auto wide) -> s16x8 {
+    if constexpr (decltype(byrow)::value) {
+      const int r = row + rl;
+      return *reinterpret_cast<const s16x8*>(L + r * kStep + (((2 * s + kg) ^ (r & 7)) * 8));
+    } else {
+      constexpr int WIDE = decltype(wide)::value;
+      // the 16 lanes of a group: reduction row + (lane & 15) / 4, columns 4 (lane & 3) ..
+      const int kr = 16 * s + 8 * kg + ((lane & 15) >> 2);
+      const int c = row + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+      const int at = ((c >> 3) ^ (2 * (kr & 3))) * 8 + (c & 7);
+      typedef __attribute__((address_space(3))) s16x4* P;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + kr * WIDE + at));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + (kr + 4) * WIDE + at));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  };
+  // fragments of the next 16 reduction values are read while this 16's products run
+  auto multiply = [&](const uint16_t* A, const uint16_t* B) {
+    s16x8 a[2][TI], b[2][TJ];
+    auto read = [&](int s) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        b[s & 1][j] = frag(B, WN * wn + 32 * j, s, std::integral_constant<bool, BROW>{},
+                           std::integral_constant<int, BN>{});
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+        a[s & 1][i] = frag(A, WM * wm + 32 * i, s, std::integral_constant<bool, AROW>{},
+                           std::integral_constant<int, BM>{});
+    };
+    read(0);
+#pragma unroll
+    for (int s = 0; s < kStep / 16; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (s + 1 < kStep / 16) read(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mma<TY>(b[s & 1][j], a[s & 1][i], acc[i][j]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // two steps a round; an odd one goes first
+  int64_t k = r0;
+  const int steps = (int)((r1 - r0 + kStep - 1) / kStep);
+  if (steps & 1) {
+    load(A1, B1, k);
+    __syncthreads();
+    k += kStep;
+    if (k < r1) load(A0, B0, k);
+    multiply(A1, B1);
+    __syncthreads();
+  } else {
+    if (k < r1) load(A0, B0, k);
+    __syncthreads();
+  }
+  for (int t = steps >> 1; t > 0; --t) {
+    load(A1, B1, k + kStep);
+    multiply(A0, B0);
+    __syncthreads();
+    k += 2 * kStep;
+    if (t > 1) load(A0, B0, k);
+    multiply(A1, B1);
+    __syncthreads();
+  }
+
+  // acc[i][j][v]: row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part
+  if constexpr (KIND == kWeight) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int64_t r = row0 + WM * wm + 32 * i + rl;
+      if (r >= end) continue;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = n0 + WN * wn + 32 * j + 8 * q + 4 * kg;
+          if (c < cols)
+            *reinterpret_cast<float4*>(dW + r * g.K + c) =
+                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]);
+        }
+    }
+  } else {
+    // through LDS, 32 rows at a time, so that a store is whole 16-byte pieces of rows
+    constexpr int PITCH = WN + 8;
+    uint16_t* out = (w % 2 ? A1 : A0) + (w / 2) * 32 * PITCH;
+    static_assert(32 * PITCH * ((WAVES + 1) / 2) <= BM * kStep, "the waves' parts fit");
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int64_t rw = row0 + WM * wm + 32 * i;             // the first of 32 rows
+      float live = 1.f;
+      if constexpr (KIND == kForward)
+        if (g.order && rw + rl < end && e < g.E && x_row(g, rw + rl) < 0) live = 0.f;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = 32 * j + 8 * q + 4 * kg;
+          float x[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) x[v] = acc[i][j][4 * q + v];
+          if constexpr (KIND == kForward) {
+            if (live == 0.f) x[0] = x[1] = x[2] = x[3] = 0.f;
+            const int n = n0 + WN * wn + c;
+            if (g.b && e < g.E && n < cols) {
+              const float* b = g.b + (int64_t)e * g.N + n;
+#pragma unroll
+              for (int v = 0; v < 4; ++v) x[v] += b[v];
+            }
+            if (g.relu)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) x[v] = x[v] > 0.f ? x[v] : 0.f;
+          }
+          uint2 h;
+          h.x = to_half<TY, false>(x[0], 0u) | (to_half<TY, false>(x[1], 0u) << 16);
+          h.y = to_half<TY, false>(x[2], 0u) | (to_half<TY, false>(x[3], 0u) << 16);
+          *reinterpret_cast<uint2*>(out + rl * PITCH + c) = h;
+        }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      constexpr int LR = WN / 8;                              // lanes a row
+#pragma unroll
+      for (int t = 0; t < 32 * LR / 64; ++t) {
+        const int rr = t * (64 / LR) + lane / LR, c = (lane % LR) * 8;
+        const int64_t r = rw + rr;
+        const int n = n0 + WN * wn + c;
+        uint4 h = *reinterpret_cast<const uint4*>(out + rr * PITCH + c);
+        if (r >= end || n >= cols) continue;
+        if constexpr (KIND == kInput) {
+          if (g.relu && e < g.E) {
+            const int64_t xr = x_row(g, r);
+            uint4 m = make_uint4(0, 0, 0, 0);
+            if (xr >= 0)
+              m = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.X) + xr * g.xs + n);
+            h.x = keep_positive<TY>(h.x, m.x);
+            h.y = keep_positive<TY>(h.y, m.y);
+            h.z = keep_positive<TY>(h.z, m.z);
+            h.w = keep_positive<TY>(h.w, m.w);
+          }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.Y) + r * g.ys + n) = h;
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+}
+
 // db[e, c] = sum of dY over the expert's rows: a block has 64 columns of one expert, each of
 // its four waves every fourth row; the waves' sums are added in order.
 template <int TY>
@@ -275,6 +720,74 @@ static experts::Product expert_product(const void* X, int64_t xs, int64_t x_rows
 // Row tiles that n rows in E + 1 pieces can need.
 static int64_t most_tiles(int64_t n, int E, int BM) { return n / BM + E + 1; }
 
+// Whether a product takes the staged 16-bit kernel: everything in whole 16-byte pieces, and a
+// block's rows within 32-bit byte offsets of its first (of X's first, where rows are gathered).
+static bool wide_ok(const experts::Product& g, int dtype) {
+  auto ok = [](const void* p, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % 8 == 0 &&
+           stride < ((int64_t)1 << 22);
+  };
+  if (dtype == kEltF32 || g.K % 8 || g.N % 8) return false;
+  if (!ok(g.X, g.xs) || !ok(g.W, g.K) || !ok(g.Y, g.ys) || !ok(g.dY, g.dys)) return false;
+  return !g.order || g.x_rows * g.xs < ((int64_t)1 << 31);
+}
+
+template <int TY, int KIND, int BM, int BN, int WM, int WN>
+static hipError_t launch_wide(experts::Product g, hipStream_t s) {
+  const int cols = KIND == experts::kForward ? g.N : g.K;
+  g.col_tiles = (cols + BN - 1) / BN;
+  g.row_tiles = (g.N + BM - 1) / BM;
+  const int64_t blocks = KIND == experts::kWeight
+                             ? (g.n / g.slice + g.E) * (int64_t)g.row_tiles * g.col_tiles
+                             : most_tiles(g.n, g.E, BM) * g.col_tiles;
+  experts::wide_kernel<TY, KIND, BM, BN, WM, WN>
+      <<<(unsigned)blocks, (BM / WM) * (BN / WN) * 64, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+// 256 x 256 tiles, or 128 x 128 where the larger ones are too few to fill the chip.
+static bool big_tiles(int64_t row_tiles, int cols) {
+  return row_tiles * ((cols + 255) / 256) >= 512;
+}
+
+template <int TY, int KIND>
+static hipError_t launch_product(experts::Product g, bool wide, hipStream_t s) {
+  if constexpr (TY != kEltF32) {
+    if (wide) {
+      const int cols = KIND == experts::kForward ? g.N : g.K;
+      if (KIND == experts::kWeight ? g.slice_big : big_tiles(g.n / 256 + g.E / 2, cols))
+        return launch_wide<TY, KIND, 256, 256, 128, 64>(g, s);
+      return launch_wide<TY, KIND, 128, 128, 64, 64>(g, s);
+    }
+  }
+  const int cols = KIND == experts::kForward ? g.N : g.K;
+  g.col_tiles = (cols + 63) / 64;
+  g.row_tiles = (g.N + 63) / 64;
+  const int64_t rows = KIND == experts::kWeight ? (int64_t)g.E * g.row_tiles
+                                                : most_tiles(g.n, g.E, 64);
+  experts::product_kernel<TY, KIND>
+      <<<(unsigned)(rows * g.col_tiles), experts::kThreads, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+// Positions a slice of the weight gradient's reduction: about four blocks a compute unit in
+// all, at least 512.
+static void set_slices(experts::Product& g) {
+  const int64_t big = (int64_t)((g.N + 255) / 256) * ((g.K + 255) / 256);
+  const int64_t small = (int64_t)((g.N + 127) / 128) * ((g.K + 127) / 128);
+  g.slice_big = big * g.E >= 512;
+  const int64_t tiles = g.slice_big ? big : small;
+  int64_t slice = (g.n * tiles + 1023) / 1024;
+  slice = slice < 512 ? 512 : slice;
+  g.slice = (slice + 63) / 64 * 64;
+}
+
+static int64_t most_partials(const experts::Product& g) {
+  // experts with several slices have more than `slice` rows each
+  const int64_t a = 2 * (g.n / g.slice), b = g.n / g.slice + g.E;
+  return a < b ? a : b;
+}
+
 hipError_t launch_expert_dense_fwd(const void* X, int dtype, int64_t xs, int64_t x_rows,
                                    const int32_t* order, int k, const int32_t* offsets, int64_t n,
                                    int E, int K, const void* W, const float* b, int N, bool relu,
@@ -282,16 +795,17 @@ hipError_t launch_expert_dense_fwd(const void* X, int dtype, int64_t xs, int64_t
   if (n == 0) return hipSuccess;
   experts::Product g = expert_product(X, xs, x_rows, order, k, offsets, n, E, K, W, N);
   g.b = b; g.relu = relu; g.Y = Y; g.ys = ys;
-  g.col_tiles = (N + 63) / 64;
-  const unsigned blocks = (unsigned)(most_tiles(n, E, 64) * g.col_tiles);
   return by_type(dtype, [&](auto ty) {
-    experts::product_kernel<decltype(ty)::value, experts::kForward>
-        <<<blocks, experts::kThreads, 0, s>>>(g);
-    return hipGetLastError();
+    return launch_product<decltype(ty)::value, experts::kForward>(g, wide_ok(g, dtype), s);
   });
 }
 
-size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtype) { return 256; }
+size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtype) {
+  if (dtype == kEltF32 || K % 8 || N % 8) return 256;
+  experts::Product g = expert_product(nullptr, K, n, nullptr, 1, nullptr, n, E, K, nullptr, N);
+  set_slices(g);
+  return (size_t)most_partials(g) * N * K * sizeof(float) + 256;
+}
 
 hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t x_rows,
                                    const int32_t* order, int k, const int32_t* offsets, int64_t n,
@@ -299,21 +813,31 @@ hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t
                                    const void* dY, int64_t dys, void* dX, int64_t dxs, float* dW,
                                    float* db, void* workspace, hipStream_t s) {
   experts::Product g = expert_product(X, xs, x_rows, order, k, offsets, n, E, K, W, N);
-  g.relu = x_relu; g.dY = dY; g.dys = dys; g.Y = dX; g.ys = dxs; g.dW = dW;
+  g.relu = x_relu; g.dY = dY; g.dys = dys;
   return by_type(dtype, [&](auto ty) {
     constexpr int TY = decltype(ty)::value;
+    hipError_t e = hipSuccess;
     if (dX && n > 0) {
-      g.col_tiles = (K + 63) / 64;
-      const unsigned blocks = (unsigned)(most_tiles(n, E, 64) * g.col_tiles);
-      experts::product_kernel<TY, experts::kInput><<<blocks, experts::kThreads, 0, s>>>(g);
+      experts::Product h = g;
+      if (!x_relu) {                   // X is not read
+        h.X = nullptr; h.xs = 0; h.x_rows = 0; h.order = nullptr;
+      }
+      h.Y = dX; h.ys = dxs;
+      e = launch_product<TY, experts::kInput>(h, wide_ok(h, dtype), s);
     }
-    hipError_t e = hipGetLastError();
     if (e == hipSuccess && dW) {
-      g.col_tiles = (K + 63) / 64;
-      g.row_tiles = (N + 63) / 64;
-      const unsigned blocks = (unsigned)((int64_t)E * g.row_tiles * g.col_tiles);
-      experts::product_kernel<TY, experts::kWeight><<<blocks, experts::kThreads, 0, s>>>(g);
-      e = hipGetLastError();
+      experts::Product h = g;
+      h.W = nullptr;
+      h.dW = dW;
+      h.part = static_cast<float*>(workspace);
+      set_slices(h);
+      const bool wide = wide_ok(h, dtype) && (reinterpret_cast<uintptr_t>(dW) & 15u) == 0;
+      e = launch_product<TY, experts::kWeight>(h, wide, s);
+      if (e == hipSuccess && wide && n > h.slice) {
+        const int64_t each = ((int64_t)N * K + experts::kJoin - 1) / experts::kJoin;
+        experts::join_kernel<<<(unsigned)(E * each), experts::kThreads, 0, s>>>(h);
+        e = hipGetLastError();
+      }
     }
     if (e == hipSuccess && db) {
       g.col_tiles = (N + 63) / 64;
