@@ -687,23 +687,63 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
   }
 }
 
-// db[e, c] = sum of dY over the expert's rows: a block has 64 columns of one expert, each of
-// its four waves every fourth row; the waves' sums are added in order.
-template <int TY>
-__global__ __launch_bounds__(kThreads) void bias_grad_kernel(Product g, float* __restrict__ db) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+// db[e, c] = sum of dY over the expert's rows.  Like the weight gradient's reduction it is cut
+// into slices (of g.slice rows here), which write db itself or, where an expert has several,
+// partial sums [unit, N] that bias_join_kernel adds in order.  A block has one slice and
+// LR lanes along the columns, VW columns each, times 256 / LR rows, four of them in flight.  Bound by reading dY once.
+template <int TY, int VW>
+__global__ __launch_bounds__(kThreads) void bias_grad_kernel(Product g, int LR,
+                                                             float* __restrict__ db) {
+  __shared__ float red[kThreads * VW];
+  const int t = threadIdx.x, l = t & (LR - 1), r = t / LR, R = kThreads / LR;
+  const int c = ((int)(blockIdx.x % g.col_tiles) * LR + l) * VW;
+  Slice u;
+  if (!find_slice(g, blockIdx.x / g.col_tiles, -1, &u)) return;
+  float s[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) s[e] = 0.f;
+  using P = rows::Piece<TY, (VW > 1)>;
+  if (c < g.N) {
+    int64_t p = u.lo + r;
+    for (; p + 3 * R < u.hi; p += 4 * R) {
+      P x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i].load(g.dY, (p + i * R) * g.dys + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) s[e] += x[i].v[e];
+    }
+    for (; p < u.hi; p += R) {
+      P x;
+      x.load(g.dY, p * g.dys + c);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) s[e] += x.v[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e) red[t * VW + e] = s[e];
+  for (int d = kThreads / 2; d >= LR; d >>= 1) {
+    __syncthreads();
+    if (t < d)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) red[t * VW + e] += red[(t + d) * VW + e];
+  }
+  if (t >= LR || c >= g.N) return;
+  float* out = u.partial >= 0 ? g.part + u.partial * g.N : db + (int64_t)u.expert * g.N;
+#pragma unroll
+  for (int e = 0; e < VW; ++e) out[c + e] = red[t * VW + e];
+}
+
+__global__ __launch_bounds__(kThreads) void bias_join_kernel(Product g, float* __restrict__ db) {
   const int e = (int)(blockIdx.x / g.col_tiles);
-  const int c = (int)(blockIdx.x % g.col_tiles) * 64 + lane;
-  int64_t lo, hi;
-  bounds_of(g, e, &lo, &hi);
-  float s = 0.f;
-  if (c < g.N)
-    for (int64_t p = lo + w; p < hi; p += 4) s += rows::load1<TY>(g.dY, p * g.dys + c);
-  red[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && c < g.N)
-    db[(int64_t)e * g.N + c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+  const int c = (int)(blockIdx.x % g.col_tiles) * kThreads + threadIdx.x;
+  Slice u;
+  if (!find_slice(g, 0, e, &u) || u.count < 2 || c >= g.N) return;
+  const float* part = g.part + u.partial * g.N + c;
+  float s = part[0];
+  for (int z = 1; z < u.count; ++z) s += part[(int64_t)z * g.N];
+  db[(int64_t)e * g.N + c] = s;
 }
 
 }  // namespace experts
@@ -800,11 +840,23 @@ hipError_t launch_expert_dense_fwd(const void* X, int dtype, int64_t xs, int64_t
   });
 }
 
+// Rows a slice of the bias gradient: at least 256, at most about 1024 slices.
+static int64_t bias_slice(int64_t n) {
+  const int64_t s = (n + 1023) / 1024;
+  return s < 256 ? 256 : s;
+}
+
 size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtype) {
-  if (dtype == kEltF32 || K % 8 || N % 8) return 256;
   experts::Product g = expert_product(nullptr, K, n, nullptr, 1, nullptr, n, E, K, nullptr, N);
-  set_slices(g);
-  return (size_t)most_partials(g) * N * K * sizeof(float) + 256;
+  int64_t need = 0;
+  if (dtype != kEltF32 && K % 8 == 0 && N % 8 == 0) {
+    set_slices(g);
+    need = most_partials(g) * N * K;
+  }
+  // the bias gradient's sums come after the weight gradient's are joined
+  g.slice = bias_slice(n);
+  const int64_t bias = most_partials(g) * N;
+  return (size_t)(need > bias ? need : bias) * sizeof(float) + 256;
 }
 
 hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t x_rows,
@@ -840,9 +892,21 @@ hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t
       }
     }
     if (e == hipSuccess && db) {
-      g.col_tiles = (N + 63) / 64;
-      const unsigned blocks = (unsigned)((int64_t)E * g.col_tiles);
-      experts::bias_grad_kernel<TY><<<blocks, experts::kThreads, 0, s>>>(g, db);
+      g.slice = bias_slice(n);
+      g.part = static_cast<float*>(workspace);
+      const int VW = TY == kEltF32 ? 4 : 8;
+      const bool vec = rows::row_vec(dY, dys, N, TY == kEltF32 ? 4 : 2);
+      const int LR = row_lanes(vec ? N / VW : N), wide = LR * (vec ? VW : 1);
+      g.col_tiles = (N + wide - 1) / wide;
+      const unsigned blocks = (unsigned)((n / g.slice + E) * g.col_tiles);
+      if (vec)
+        experts::bias_grad_kernel<TY, VW><<<blocks, experts::kThreads, 0, s>>>(g, LR, db);
+      else
+        experts::bias_grad_kernel<TY, 1><<<blocks, experts::kThreads, 0, s>>>(g, LR, db);
+      if (n > g.slice) {
+        g.col_tiles = (N + experts::kThreads - 1) / experts::kThreads;
+        experts::bias_join_kernel<<<(unsigned)(E * g.col_tiles), experts::kThreads, 0, s>>>(g, db);
+      }
       e = hipGetLastError();
     }
     return e;

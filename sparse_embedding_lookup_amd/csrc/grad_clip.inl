@@ -13,16 +13,21 @@ namespace ctr {
 namespace clip {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;                     // elements: 32 a thread
+constexpr int kUnit = 8;                         // elements a thread takes at a time
+constexpr int kChunk = 4096;                     // elements: two units a thread
 constexpr int kTensors = 100;                    // of one launch: their records are arguments
-constexpr int kMaxBlocks = 1024;                 // four blocks a compute unit
+constexpr int kMaxBlocks = 2048;                 // eight blocks a compute unit
 
+// A tensor's chunks are counted from `shift` elements before its first, so that every unit of
+// `out` but the first and the last is aligned, whatever the tensor's own alignment: gradients
+// are often views of one buffer, where one odd size moves all that follow off their alignment.
+// (Half a gigabyte of bf16 gradients in such a buffer, written element by element: 906 us.)
 struct Tensor {
   const void* g;
   void* out;
   int64_t n;
   int32_t first;                                 // the tensor's first chunk
-  int8_t gty, oty, vec, pad;
+  int8_t gty, oty, shift, pad;
 };
 struct Batch {
   Tensor t[kTensors];
@@ -51,27 +56,68 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return v;
 }
 
+// Eight elements as stored.  The 16-byte accesses need the element's alignment only (the
+// memory pipeline takes any), aligned ones are the fast ones.
+template <int TY>
+struct Unit {
+  static constexpr int kElem = TY == kEltF32 ? 4 : 2, kWords = kUnit * kElem / 4;
+  uint32_t u[kWords];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    __builtin_memcpy(u, static_cast<const char*>(p) + i * kElem, sizeof(u));
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    __builtin_memcpy(static_cast<char*>(p) + i * kElem, u, sizeof(u));
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (TY == kEltF32) return __uint_as_float(u[e]);
+    else return e & 1 ? half_hi<TY>(u[e >> 1]) : half_lo<TY>(u[e >> 1]);
+  }
+  __device__ __forceinline__ void set(int e, float a, float b) {       // elements e and e + 1
+    if constexpr (TY == kEltF32) {
+      u[e] = __float_as_uint(a);
+      u[e + 1] = __float_as_uint(b);
+    } else {
+      u[e >> 1] = to_half<TY, false>(a, 0u) | (to_half<TY, false>(b, 0u) << 16);
+    }
+  }
+};
+
+// Calls whole(r, i) for the chunk's units r of this thread that lie inside [0, n), i their
+// first element, and one(i) for the single elements of those that lie partly inside.
+constexpr int kUnits = kChunk / (kThreads * kUnit);
+template <typename Whole, typename One>
+__device__ __forceinline__ void walk(int64_t i0, int64_t n, Whole whole, One one) {
+#pragma unroll
+  for (int r = 0; r < kUnits; ++r) {
+    const int64_t i = i0 + (r * kThreads + (int)threadIdx.x) * kUnit;
+    if (i >= 0 && i + kUnit <= n) whole(r, i);
+    else
+      for (int e = 0; e < kUnit; ++e)
+        if (i + e >= 0 && i + e < n) one(i + e);
+  }
+}
+
 // The sum of squares of one chunk's elements that are this thread's.
 template <int TY>
-__device__ __forceinline__ double square_sum(const void* g, int64_t i0, int64_t n, bool vec) {
+__device__ __forceinline__ double square_sum(const void* g, int64_t i0, int64_t n) {
   double s = 0.0;
-  const int64_t end = n < i0 + kChunk ? n : i0 + kChunk;
-  if (vec && end - i0 == kChunk) {
-    constexpr int W = Vec<TY>::kElems, R = kChunk / (kThreads * W);
-    Vec<TY> x[R];
+  Unit<TY> x[kUnits];
+  auto add = [&](double v) { s = __builtin_fma(v, v, s); };
+  if (i0 >= 0 && i0 + kChunk <= n) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      x[r].load(static_cast<const char*>(g) +
-                (i0 + (int64_t)(r * kThreads + threadIdx.x) * W) * (TY == kEltF32 ? 4 : 2));
+    for (int r = 0; r < kUnits; ++r) x[r].load(g, i0 + (r * kThreads + (int)threadIdx.x) * kUnit);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < kUnits; ++r)
 #pragma unroll
-      for (int e = 0; e < W; ++e) s = __builtin_fma((double)x[r].v[e], (double)x[r].v[e], s);
+      for (int e = 0; e < kUnit; ++e) add(x[r].get(e));
   } else {
-    for (int64_t i = i0 + threadIdx.x; i < end; i += kThreads) {
-      const double v = rows::load1<TY>(g, i);
-      s = __builtin_fma(v, v, s);
-    }
+    walk(i0, n,
+         [&](int r, int64_t i) {
+           x[r].load(g, i);
+#pragma unroll
+           for (int e = 0; e < kUnit; ++e) add(x[r].get(e));
+         },
+         [&](int64_t i) { add(rows::load1<TY>(g, i)); });
   }
   return s;
 }
@@ -82,81 +128,59 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(Batch b, double* __restr
   for (int c = blockIdx.x; c < b.chunks; c += gridDim.x) {
     const int i = find_tensor(b, c);
     const void* g = b.t[i].g;
-    const int64_t n = b.t[i].n, i0 = (int64_t)(c - b.t[i].first) * kChunk;
-    const bool vec = b.t[i].vec;
+    const int64_t n = b.t[i].n, i0 = (int64_t)(c - b.t[i].first) * kChunk - b.t[i].shift;
     const int ty = b.t[i].gty;
-    if (ty == kEltF32) s += square_sum<kEltF32>(g, i0, n, vec);
-    else if (ty == kEltBF16) s += square_sum<kEltBF16>(g, i0, n, vec);
-    else s += square_sum<kEltF16>(g, i0, n, vec);
+    if (ty == kEltF32) s += square_sum<kEltF32>(g, i0, n);
+    else if (ty == kEltBF16) s += square_sum<kEltBF16>(g, i0, n);
+    else s += square_sum<kEltF16>(g, i0, n);
   }
   s = block_sum(s, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-template <int TY>
-__device__ __forceinline__ void scale_chunk(const void* g, void* out, int64_t i0, int64_t n,
-                                            bool vec, float c) {
-  const int64_t end = n < i0 + kChunk ? n : i0 + kChunk;
-  if (vec && end - i0 == kChunk) {
-    using P = rows::Piece<TY, true>;
-    constexpr int W = P::kElems, R = kChunk / (kThreads * W);
-    P x[R];
+// One chunk of p = f(g, p); GT and PT are the types of g and p, OLD: p is read.
+template <int GT, int PT, bool OLD, typename F>
+__device__ __forceinline__ void update_chunk(const void* g, void* p, int64_t i0, int64_t n, F f) {
+  Unit<GT> x[kUnits];
+  Unit<PT> y[kUnits];
+  auto put = [&](int r, int64_t i) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) x[r].load(g, i0 + (int64_t)(r * kThreads + threadIdx.x) * W);
+    for (int e = 0; e < kUnit; e += 2)
+      y[r].set(e, f(x[r].get(e), OLD ? y[r].get(e) : 0.f),
+               f(x[r].get(e + 1), OLD ? y[r].get(e + 1) : 0.f));
+    y[r].store(p, i);
+  };
+  if (i0 >= 0 && i0 + kChunk <= n) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int e = 0; e < W; ++e) x[r].v[e] *= c;
-      x[r].store(out, i0 + (int64_t)(r * kThreads + threadIdx.x) * W);
+    for (int r = 0; r < kUnits; ++r) {
+      const int64_t i = i0 + (r * kThreads + (int)threadIdx.x) * kUnit;
+      x[r].load(g, i);
+      if constexpr (OLD) y[r].load(p, i);
     }
+#pragma unroll
+    for (int r = 0; r < kUnits; ++r)
+      put(r, i0 + (r * kThreads + (int)threadIdx.x) * kUnit);
   } else {
-    for (int64_t i = i0 + threadIdx.x; i < end; i += kThreads)
-      rows::store1<TY>(out, i, rows::load1<TY>(g, i) * c);
-  }
-}
-
-template <int GT, int PT>
-__device__ __forceinline__ void sgd_chunk(const void* g, void* p, int64_t i0, int64_t n, bool vec,
-                                          float c) {
-  const int64_t end = n < i0 + kChunk ? n : i0 + kChunk;
-  if (vec && end - i0 == kChunk) {
-    // eight elements a thread and round, whatever the types
-    constexpr int R = kChunk / (kThreads * 8);
-    using G = rows::Piece<GT, true>;
-    using P = rows::Piece<PT, true>;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t i = i0 + (int64_t)(r * kThreads + threadIdx.x) * 8;
-      float x[8];
-#pragma unroll
-      for (int q = 0; q < 8 / G::kElems; ++q) {
-        G v;
-        v.load(g, i + q * G::kElems);
-#pragma unroll
-        for (int e = 0; e < G::kElems; ++e) x[q * G::kElems + e] = v.v[e];
-      }
-#pragma unroll
-      for (int q = 0; q < 8 / P::kElems; ++q) {
-        P v;
-        v.load(p, i + q * P::kElems);
-#pragma unroll
-        for (int e = 0; e < P::kElems; ++e)
-          v.v[e] = __builtin_fmaf(-c, x[q * P::kElems + e], v.v[e]);
-        v.store(p, i + q * P::kElems);
-      }
-    }
-  } else {
-    for (int64_t i = i0 + threadIdx.x; i < end; i += kThreads)
-      rows::store1<PT>(p, i, __builtin_fmaf(-c, rows::load1<GT>(g, i), rows::load1<PT>(p, i)));
+    walk(i0, n,
+         [&](int r, int64_t i) {
+           x[r].load(g, i);
+           if constexpr (OLD) y[r].load(p, i);
+           put(r, i);
+         },
+         [&](int64_t i) {
+           const float old = OLD ? rows::load1<PT>(p, i) : 0.f;
+           rows::store1<PT>(p, i, f(rows::load1<GT>(g, i), old));
+         });
   }
 }
 
 template <int GT>
 __device__ __forceinline__ void sgd_by_param(int pt, const void* g, void* p, int64_t i0,
-                                             int64_t n, bool vec, float c) {
-  if (pt == kEltF32) sgd_chunk<GT, kEltF32>(g, p, i0, n, vec, c);
-  else if (pt == kEltBF16) sgd_chunk<GT, kEltBF16>(g, p, i0, n, vec, c);
-  else sgd_chunk<GT, kEltF16>(g, p, i0, n, vec, c);
+                                             int64_t n, float c) {
+  auto step = [c](float x, float old) { return __builtin_fmaf(-c, x, old); };
+  if (pt == kEltF32) update_chunk<GT, kEltF32, true>(g, p, i0, n, step);
+  else if (pt == kEltBF16) update_chunk<GT, kEltBF16, true>(g, p, i0, n, step);
+  else update_chunk<GT, kEltF16, true>(g, p, i0, n, step);
 }
 
 template <bool SGD>
@@ -179,19 +203,19 @@ __global__ __launch_bounds__(kThreads) void apply_kernel(Batch b,
     const int i = find_tensor(b, q);
     const void* g = b.t[i].g;
     void* out = b.t[i].out;
-    const int64_t n = b.t[i].n, i0 = (int64_t)(q - b.t[i].first) * kChunk;
-    const bool vec = b.t[i].vec;
+    const int64_t n = b.t[i].n, i0 = (int64_t)(q - b.t[i].first) * kChunk - b.t[i].shift;
     const int gty = b.t[i].gty;
     if constexpr (SGD) {
       const int oty = b.t[i].oty;
-      if (gty == kEltF32) sgd_by_param<kEltF32>(oty, g, out, i0, n, vec, c);
-      else if (gty == kEltBF16) sgd_by_param<kEltBF16>(oty, g, out, i0, n, vec, c);
-      else sgd_by_param<kEltF16>(oty, g, out, i0, n, vec, c);
+      if (gty == kEltF32) sgd_by_param<kEltF32>(oty, g, out, i0, n, c);
+      else if (gty == kEltBF16) sgd_by_param<kEltBF16>(oty, g, out, i0, n, c);
+      else sgd_by_param<kEltF16>(oty, g, out, i0, n, c);
     } else {
       if (g == out && c == 1.f) continue;        // in place and not clipped: nothing to write
-      if (gty == kEltF32) scale_chunk<kEltF32>(g, out, i0, n, vec, c);
-      else if (gty == kEltBF16) scale_chunk<kEltBF16>(g, out, i0, n, vec, c);
-      else scale_chunk<kEltF16>(g, out, i0, n, vec, c);
+      auto scaled = [c](float x, float) { return x * c; };
+      if (gty == kEltF32) update_chunk<kEltF32, kEltF32, false>(g, out, i0, n, scaled);
+      else if (gty == kEltBF16) update_chunk<kEltBF16, kEltBF16, false>(g, out, i0, n, scaled);
+      else update_chunk<kEltF16, kEltF16, false>(g, out, i0, n, scaled);
     }
   }
 }
@@ -210,6 +234,9 @@ hipError_t launch_grad_clip(int num, const void* const* grads, const int64_t* si
                             hipStream_t s) {
   double* partial = static_cast<double*>(workspace);
   const int64_t launches = num > 0 ? clip_launches(num) : 1;
+  // every block of the second pass adds up all partial sums: fewer blocks a launch where there
+  // are several launches
+  const int most = launches > 1 ? clip::kMaxBlocks / 2 : clip::kMaxBlocks;
   int partials = 0;
   for (int pass = 0; pass < 2; ++pass)
     // the second pass takes the launches last to first, like their chunks
@@ -225,10 +252,11 @@ hipError_t launch_grad_clip(int num, const void* const* grads, const int64_t* si
         t.first = b.chunks;
         t.gty = (int8_t)gtypes[i];
         t.oty = (int8_t)(otypes ? otypes[i] : gtypes[i]);
-        t.vec = ((reinterpret_cast<uintptr_t>(t.g) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0;
-        b.chunks += (int32_t)((sizes[i] + clip::kChunk - 1) / clip::kChunk);
+        const int elem = t.oty == kEltF32 ? 4 : 2;
+        t.shift = (int8_t)((reinterpret_cast<uintptr_t>(t.out) & 15u) / elem);
+        b.chunks += (int32_t)((sizes[i] + t.shift + clip::kChunk - 1) / clip::kChunk);
       }
-      const int blocks = b.chunks < clip::kMaxBlocks ? b.chunks : clip::kMaxBlocks;
+      const int blocks = b.chunks < most ? b.chunks : most;
       if (pass == 0) {
         if (blocks == 0) continue;
         clip::norm_kernel<<<blocks, clip::kThreads, 0, s>>>(b, partial + partials);

@@ -7,6 +7,7 @@ fallback: if the library is missing or fails to load, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -177,8 +178,13 @@ def src_layout(sorted_src: Optional[torch.Tensor]) -> int:
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The address of `stream`, or of the current device's current stream (read without making
+    a torch.cuda.Stream of it, which takes 2.5 us: more than a launch)."""
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(fn: str, status: int) -> None:
@@ -206,8 +212,12 @@ class Call:
 
 
 def _run(name: str, args: tuple, stream, prepare: bool, result=None, keep=None):
-    call = Call(name, args, result, keep)
-    return call if prepare else call(stream)
+    if prepare:
+        return Call(name, args, result, keep)
+    st = getattr(_lib or load(), name)(*args, _stream(stream))
+    if st != CTR_OK:
+        _check(name, st)
+    return result
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -628,6 +638,21 @@ def ctr_logistic_ne(logits: torch.Tensor, labels: torch.Tensor,
 _DTYPE_CODES = {torch.float32: CTR_F32, torch.bfloat16: CTR_BF16, torch.float16: CTR_F16}
 
 
+def _launch(name: str, device: torch.device, args: tuple, stream, prepare: bool, result=None,
+            keep=None):
+    """_run of arguments that are all on `device`, which has to be a GPU."""
+    if device.type != "cuda":
+        raise ValueError("%s takes tensors on a GPU, not on %s" % (name, device))
+    got = _run(name, args, stream, prepare, result, keep)
+    if stream is not None and not prepare:
+        # what the binding allocated belongs to the current stream: its memory is not reused
+        # there before this stream's work is done
+        for t in (result if isinstance(result, tuple) else (result,)) + (keep,):
+            if t is not None:
+                t.record_stream(stream)
+    return got
+
+
 def _expert_arg(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
                 device: torch.device, rows: bool = False) -> int:
     """The address of an argument of this shape, dtype and device; contiguous, or with `rows`
@@ -684,7 +709,7 @@ def ctr_expert_route_fwd(logits: torch.Tensor, k: int, renormalize: bool = True,
     args = (logits.data_ptr(), code, ls, T, E, k, int(bool(renormalize)),
             _expert_arg(experts, "experts", (T, k), torch.int32, dev),
             _expert_arg(weights, "weights", (T, k), torch.float32, dev))
-    return _run("ctr_expert_route_fwd", args, stream, prepare, (experts, weights))
+    return _launch("ctr_expert_route_fwd", dev, args, stream, prepare, (experts, weights))
 
 
 def ctr_expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor,
@@ -704,9 +729,10 @@ def ctr_expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, weights: t
             _expert_arg(dweights, "dweights", (T, k), torch.float32, dev),
             _expert_arg(dlogits, "dlogits", (T, E), logits.dtype, dev, rows=True),
             _row_stride(dlogits, "dlogits"))
-    return _run("ctr_expert_route_bwd", args, stream, prepare, dlogits)
+    return _launch("ctr_expert_route_bwd", dev, args, stream, prepare, dlogits)
 
 
+@functools.lru_cache(maxsize=1024)
 def expert_sort_workspace_bytes(T: int, k: int, num_experts: int) -> int:
     """Workspace of ctr_expert_sort (the library's two-call query)."""
     wsb = ctypes.c_size_t(0)
@@ -740,7 +766,7 @@ def ctr_expert_sort(experts: torch.Tensor, num_experts: int,
             _expert_arg(slots, "slots", (T, k), torch.int32, dev),
             _expert_arg(order, "order", (T * k,), torch.int32, dev), workspace.data_ptr(),
             ctypes.byref(wsb))
-    return _run("ctr_expert_sort", args, stream, prepare, (offsets, slots, order),
+    return _launch("ctr_expert_sort", dev, args, stream, prepare, (offsets, slots, order),
                 workspace)
 
 
@@ -768,7 +794,7 @@ def ctr_expert_dispatch(X: torch.Tensor, slots: torch.Tensor, offsets: torch.Ten
         P = torch.empty((T * k, D), dtype=X.dtype, device=dev)
     args = (_expert_arg(X, "X", (T, D), X.dtype, dev, rows=True), code, xs, T, k, D, sp, op, E,
             _expert_arg(P, "P", (T * k, D), X.dtype, dev, rows=True), _row_stride(P, "P"))
-    return _run("ctr_expert_dispatch", args, stream, prepare, P)
+    return _launch("ctr_expert_dispatch", dev, args, stream, prepare, P)
 
 
 def ctr_expert_combine_fwd(P: torch.Tensor, slots: torch.Tensor,
@@ -784,7 +810,7 @@ def ctr_expert_combine_fwd(P: torch.Tensor, slots: torch.Tensor,
     wp = None if weights is None else _expert_arg(weights, "weights", (T, k), torch.float32, dev)
     args = (_expert_arg(P, "P", (T * k, D), P.dtype, dev, rows=True), code, ps, T, k, D, sp, wp,
             _expert_arg(Y, "Y", (T, D), P.dtype, dev, rows=True), _row_stride(Y, "Y"))
-    return _run("ctr_expert_combine_fwd", args, stream, prepare, Y)
+    return _launch("ctr_expert_combine_fwd", dev, args, stream, prepare, Y)
 
 
 def ctr_expert_combine_bwd(dY: torch.Tensor, P: Optional[torch.Tensor], slots: torch.Tensor,
@@ -812,7 +838,7 @@ def ctr_expert_combine_bwd(dY: torch.Tensor, P: Optional[torch.Tensor], slots: t
     args = (_expert_arg(dY, "dY", (T, D), dY.dtype, dev, rows=True), code, dys, T, k, D, pp, ps,
             sp, op, E, wp, _expert_arg(dP, "dP", (T * k, D), dY.dtype, dev, rows=True),
             _row_stride(dP, "dP"), dwp)
-    return _run("ctr_expert_combine_bwd", args, stream, prepare, (dP, dweights))
+    return _launch("ctr_expert_combine_bwd", dev, args, stream, prepare, (dP, dweights))
 
 
 def _product_args(X, W, offsets, order, k):
@@ -851,9 +877,10 @@ def ctr_expert_dense_fwd(X: torch.Tensor, W: torch.Tensor, b: Optional[torch.Ten
     bp = None if b is None else _expert_arg(b, "b", (E, N), torch.float32, dev)
     args = first + (bp, N, int(bool(relu)),
                     _expert_arg(Y, "Y", (n, N), X.dtype, dev, rows=True), _row_stride(Y, "Y"))
-    return _run("ctr_expert_dense_fwd", args, stream, prepare, Y)
+    return _launch("ctr_expert_dense_fwd", dev, args, stream, prepare, Y)
 
 
+@functools.lru_cache(maxsize=1024)
 def expert_dense_bwd_workspace_bytes(n: int, num_experts: int, K: int, N: int,
                                      dtype: int = CTR_BF16) -> int:
     """Workspace of ctr_expert_dense_bwd (the library's two-call query)."""
@@ -893,12 +920,13 @@ def ctr_expert_dense_bwd(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor
         _expert_arg(dW, "dW", (E, N, K), torch.float32, dev) if want_dw else None,
         _expert_arg(db, "db", (E, N), torch.float32, dev) if bias else None,
         workspace.data_ptr(), ctypes.byref(wsb))
-    return _run("ctr_expert_dense_bwd", args, stream, prepare,
+    return _launch("ctr_expert_dense_bwd", dev, args, stream, prepare,
                 (dX if want_dx else None, dW if want_dw else None, db if bias else None),
                 workspace)
 
 
 # --------------------------------------------------------------------- gradient clipping
+@functools.lru_cache(maxsize=1024)
 def grad_clip_workspace_bytes(num: int) -> int:
     """Workspace of ctr_grad_clip and ctr_grad_clip_sgd (the library's two-call query)."""
     wsb = ctypes.c_size_t(0)
@@ -907,27 +935,26 @@ def grad_clip_workspace_bytes(num: int) -> int:
     return wsb.value
 
 
-def _tensor_list(ts, name: str, sizes=None, dtypes=None, device=None):
-    """Host arrays of the addresses, element counts and types of contiguous tensors."""
-    num = len(ts)
-    ptrs, counts, codes = [], [], []
+def _tensor_list(ts, name: str, device: torch.device, sizes=None, dtypes=None):
+    """A host array of the addresses of contiguous tensors on one device, and their element
+    counts and types."""
+    at = -1 if device.type == "cpu" else device.index
+    codes = [_DTYPE_CODES.get(t.dtype) for t in ts]
+    if None in codes:
+        i = codes.index(None)
+        raise TypeError("%s[%d] must be float32, bfloat16 or float16, not %s"
+                        % (name, i, ts[i].dtype))
     for i, t in enumerate(ts):
-        code = _DTYPE_CODES.get(t.dtype)
-        if code is None:
-            raise TypeError("%s[%d] must be float32, bfloat16 or float16, not %s"
-                            % (name, i, t.dtype))
         if not t.is_contiguous():
             raise ValueError("%s[%d] must be contiguous" % (name, i))
-        if device is not None and t.device != device:
+        if t.get_device() != at:
             raise ValueError("%s[%d] is on %s, not %s" % (name, i, t.device, device))
-        ptrs.append(t.data_ptr())
-        counts.append(t.numel())
-        codes.append(code)
+    counts = [t.numel() for t in ts]
     if sizes is not None and counts != sizes:
         raise ValueError("%s and grads differ in number or sizes" % name)
     if dtypes is not None and codes != dtypes:
         raise TypeError("%s and grads differ in type" % name)
-    return (ctypes.c_void_p * num)(*ptrs), counts, codes
+    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts]), counts, codes
 
 
 def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepare, out_name):
@@ -935,7 +962,7 @@ def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepar
     if not grads:
         raise ValueError("no gradients")
     dev = grads[0].device
-    gp, counts, codes = _tensor_list(grads, "grads", device=dev)
+    gp, counts, codes = _tensor_list(grads, "grads", dev)
     num = len(grads)
     if stats is None:
         stats = torch.empty(2, dtype=torch.float32, device=dev)
@@ -946,10 +973,10 @@ def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepar
     head = (num, gp, (ctypes.c_int64 * num)(*counts), (ctypes.c_int32 * num)(*codes))
     tail = (float(max_norm), sp, workspace.data_ptr(), ctypes.byref(wsb))
     if lr is None:
-        op = None if outs is None else _tensor_list(list(outs), out_name, counts, codes, dev)[0]
-        return _run(name, head + (op,) + tail, stream, prepare, stats, workspace)
-    pp, _, pcodes = _tensor_list(list(outs), out_name, counts, None, dev)
-    return _run(name, head + (pp, (ctypes.c_int32 * num)(*pcodes), float(lr)) + tail, stream,
+        op = None if outs is None else _tensor_list(list(outs), out_name, dev, counts, codes)[0]
+        return _launch(name, dev, head + (op,) + tail, stream, prepare, stats, workspace)
+    pp, _, pcodes = _tensor_list(list(outs), out_name, dev, counts)
+    return _launch(name, dev, head + (pp, (ctypes.c_int32 * num)(*pcodes), float(lr)) + tail, stream,
                 prepare, stats, workspace)
 
 
