@@ -22,7 +22,8 @@ struct Product {
   const void* X;
   int64_t xs, x_rows;
   const int32_t* order;         // nullable: positions are X's rows
-  int k;
+  uint64_t kmul;                // i / k = i * kmul >> kshift for 0 <= i < 2^31
+  int kshift;
   const int32_t* offsets;
   int64_t n;
   int E, K, N;
@@ -79,12 +80,15 @@ __device__ __forceinline__ bool find_tile(const Product& g, int64_t mt, int* exp
   return false;
 }
 
-// Row of X that position p reads, or -1 (a slot outside X: its row reads as zeros).
+// Row of X of slot i (its token, i / k), or -1 (a slot outside X: its row reads as zeros).
+__device__ __forceinline__ int64_t token_of(const Product& g, int32_t i) {
+  const int64_t r = (int64_t)(((uint64_t)(uint32_t)i * g.kmul) >> g.kshift);
+  return i >= 0 && r < g.x_rows ? r : -1;
+}
+// Row of X that position p reads, or -1.
 __device__ __forceinline__ int64_t x_row(const Product& g, int64_t p) {
   if (!g.order) return p < g.x_rows ? p : -1;
-  const int64_t i = g.order[p];
-  const int64_t r = i >= 0 ? i / g.k : -1;
-  return r < g.x_rows ? r : -1;
+  return token_of(g, g.order[p]);
 }
 
 template <int TY>
@@ -361,24 +365,34 @@ __device__ __forceinline__ uint32_t keep_positive(uint32_t h, uint32_t m) {
 // ------------------------------------------------------------------ 16-bit operands, staged
 // The products of 16-bit operands in 16-byte pieces (widths and strides multiples of 8,
 // 16-byte aligned arrays).  A block has a BM x BN output tile and a wave a WM x WN part of it
-// in 32 x 32 matrix-core tiles; the reduction advances 64 at a time through two LDS buffers.
-// Tiles go from memory to LDS directly (one 16-byte load a lane, 1 KB a wave, no registers in
-// between), those of the next step while this step's products run; one barrier a step.
+// in 32 x 32 matrix-core tiles; the reduction advances 32 at a time through a ring of four LDS
+// buffers.  Tiles go from memory to LDS directly (one 16-byte load a lane, 1 KB a wave, no
+// registers in between), three steps ahead of their use; the loads' own bounds check gives
+// zeros for rows and reduction values that are not there.
 //
-// An operand lies in LDS in one of two forms:
-//   by rows (64 reduction values of one row, 128 bytes): a fragment is one 16-byte read.
-//     The 16-byte piece c of row r is at c ^ (r & 7), so that eight lanes that read piece c
-//     of eight rows touch all banks.
+// A step of a wave is a part that moves data (its fragments of the step from LDS to
+// registers, its share of the loads of the step three on) and a part that computes (16
+// matrix-core instructions in 256 x 256 tiles).  With eight waves, two on each SIMD, the
+// second four run half a step behind the first: while one of a SIMD's waves computes the
+// other moves data, and the matrix cores never wait for both.  Barriers end both parts.  With
+// four waves there are two blocks a compute unit, which interleave by themselves, and one
+// barrier a step.
+//
+// An operand lies in LDS in one of two forms; the banks serve 256 bytes at a time:
+//   by rows (32 reduction values of one row, 64 bytes): a fragment is one 16-byte read of 32
+//     rows.  The 16-byte piece c of row r is at c ^ (r / 4 & 3), so that sixteen lanes that
+//     read piece c of sixteen rows touch all banks.
 //   by reduction (BM or BN values of one reduction index): a fragment is two transposing
-//     reads, each giving a lane four reduction values of its row.  Sixteen lanes read four
-//     reduction rows of 32 bytes; piece c of reduction row q is at c ^ (2 (q & 3)), which
-//     spreads the four over the banks.
+//     reads, each giving a lane four reduction values of its row.  32 lanes read 64 bytes of
+//     four reduction rows; piece c of reduction row q is at c ^ (4 (q & 3)), which spreads
+//     the four over the banks.
 // The matrix cores take the columns as their rows: a lane then holds four neighbouring
 // columns of one output row, stored together.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kStep = 64;                      // reduction values a step
+constexpr int kStep = 32;                      // reduction values a step
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;     // an offset past every buffer: reads zeros
 
 template <int TY>
 __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
@@ -390,24 +404,45 @@ __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// 16 bytes a lane from base + off to lds + 16 * lane (lds the same in the whole wave).
-__device__ __forceinline__ void to_lds(const char* base, uint32_t off, uint16_t* lds) {
-  __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void*)(base + off),
-      (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// 16 bytes a lane from base + off to lds + 16 * lane (base and lds the same in the whole wave).
+__device__ __forceinline__ void to_lds(const void* base, uint32_t off, uint16_t* lds) {
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)kNowhere, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
+                                           (int)off, 0, 0, 0);
 }
-__device__ __forceinline__ void zero_lds(uint16_t* lds, int lane) {
-  *reinterpret_cast<uint4*>(lds + 8 * lane) = make_uint4(0, 0, 0, 0);
+
+// Ends a part: the wave's LDS reads are done and at most LOADS of its loads are in flight, in
+// every wave.
+template <int LOADS>
+__device__ __forceinline__ void arrive() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void arrive_only() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A value that is the same in the whole wave, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
 template <int TY, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Product g) {
   constexpr int WAVES = (BM / WM) * (BN / WN), WN_WAVES = BN / WN;
-  constexpr bool AROW = KIND != kWeight, BROW = KIND == kForward;
+  constexpr bool AROW = KIND != kWeight, BROW = KIND == kForward, PAIRED = WAVES == 8;
   constexpr int TI = WM / 32, TJ = WN / 32;
-  constexpr int AE = BM * kStep / 512 / WAVES, BE = BN * kStep / 512 / WAVES;
-  __shared__ __attribute__((aligned(16))) uint16_t A0[BM * kStep], A1[BM * kStep];
-  __shared__ __attribute__((aligned(16))) uint16_t B0[BN * kStep], B1[BN * kStep];
+  constexpr int AL = BM * kStep / 512 / WAVES, BL = BN * kStep / 512 / WAVES, LOADS = AL + BL;
+  __shared__ __attribute__((aligned(16))) uint16_t A0[BM * kStep], A1[BM * kStep], A2[BM * kStep],
+      A3[BM * kStep];
+  __shared__ __attribute__((aligned(16))) uint16_t B0[BN * kStep], B1[BN * kStep], B2[BN * kStep],
+      B3[BN * kStep];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / WN_WAVES, wn = w % WN_WAVES;
@@ -426,8 +461,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     e = u.expert;
     r0 = u.lo;
     r1 = u.hi;
-    if (u.partial >= 0) dW = g.part + u.partial * g.N * g.K;
-    else dW += (int64_t)e * g.N * g.K;
+    dW = u.partial >= 0 ? g.part + uniform(u.partial) * g.N * g.K
+                        : dW + uniform(e) * g.N * g.K;
     row0 = (int64_t)(tile / g.col_tiles) * BM;
     n0 = tile % g.col_tiles * BN;
     end = g.N;
@@ -438,94 +473,118 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     if (!find_tile<BM>(g, mt, &e, &row0, &end)) return;
     r1 = e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
   }
+  e = __builtin_amdgcn_readfirstlane(e);
+  n0 = __builtin_amdgcn_readfirstlane(n0);
+  row0 = uniform(row0);
+  end = uniform(end);
+  r0 = uniform(r0);
+  r1 = uniform(r1);
   const int cols = KIND == kForward ? g.N : g.K;
   const uint16_t* W = static_cast<const uint16_t*>(g.W) + (int64_t)(e < g.E ? e : 0) * g.N * g.K;
 
-  // Lane addresses.  By rows: lane i of piece q has row 8 q + i / 8 and its 16 bytes
-  // (i % 8) ^ (i / 8); rows past the end read the tile's first row, and are not stored.
-  const int piece = ((lane & 7) ^ (lane >> 3)) * 16;          // bytes along the reduction
-  const char *abase, *bbase;
-  uint32_t aoff[AE], boff[BE];
+  // Where a lane's loads are, in bytes from the operand's base at the step's first reduction
+  // value.  By rows: lane i of piece q has row 16 q + i / 4 and its 16 bytes
+  // (i % 4) ^ (i / 16).  By reduction: 512 / WIDE reduction rows a piece.
+  const int piece = ((lane & 3) ^ (lane >> 4)) * 8;            // first reduction value
+  const uint16_t* abase;
+  const uint16_t* bbase;
+  int64_t astep, bstep;                                        // elements from step to step
+  uint32_t aoff[AL], boff[BL];
+  constexpr int APER = 512 / BM, BPER = 512 / BN;              // by reduction: rows a piece
+  constexpr int ALANES = 64 / APER, BLANES = 64 / BPER;
   if constexpr (AROW) {
-    const uint16_t* base = static_cast<const uint16_t*>(KIND == kForward ? g.X : g.dY);
+    abase = static_cast<const uint16_t*>(KIND == kForward ? g.X : g.dY);
     const int64_t ld = KIND == kForward ? g.xs : g.dys;
     const bool gather = KIND == kForward && g.order;
-    if (!gather) base += row0 * ld;
-    abase = reinterpret_cast<const char*>(base);
+    if (!gather) abase += row0 * ld;
+    astep = kStep;
 #pragma unroll
-    for (int q = 0; q < AE; ++q) {
-      const int64_t r = row0 + 8 * (q * WAVES + w) + (lane >> 3);
-      const int64_t p = r < end ? r : row0;
-      int64_t x = p - row0;
-      if (gather) {
-        x = x_row(g, p);
-        x = x < 0 ? 0 : x;
-      }
-      aoff[q] = (uint32_t)(x * ld * 2) + piece;
+    for (int q = 0; q < AL; ++q) {
+      const int64_t r = row0 + 16 * (q * WAVES + w) + (lane >> 2);
+      int64_t x = r < end ? r - row0 : -1;
+      if (gather && x >= 0) x = x_row(g, r);
+      aoff[q] = x >= 0 ? (uint32_t)(x * ld + piece) * 2 : kNowhere;
     }
   } else {
-    // columns of dY; a reduction row is BM * 2 bytes
-    abase = reinterpret_cast<const char*>(static_cast<const uint16_t*>(g.dY) + row0);
-  }
-  if constexpr (BROW) {
-    bbase = reinterpret_cast<const char*>(W + (int64_t)n0 * g.K);
+    abase = static_cast<const uint16_t*>(g.dY) + r0 * g.dys + row0;
+    astep = kStep * g.dys;
 #pragma unroll
-    for (int q = 0; q < BE; ++q) {
-      const int r = 8 * (q * WAVES + w) + (lane >> 3);
-      boff[q] = (uint32_t)((n0 + r < cols ? r : 0) * (int64_t)g.K * 2) + piece;
+    for (int q = 0; q < AL; ++q) {
+      const int kr = (q * WAVES + w) * APER + lane / ALANES;
+      const int c = ((lane % ALANES) ^ (4 * (kr & 3))) * 8;
+      aoff[q] = row0 + c < end ? (uint32_t)(kr * g.dys + c) * 2 : kNowhere;
     }
   }
-
-  // Loads one step's operands: reduction values [k, k + 64).
-  auto load_row = [&](const char* base, const uint32_t* off, int each, uint16_t* lds, int64_t k,
-                      auto count) {
-    const char* at = base + k * 2;
-    if (k + kStep <= r1) {
+  const bool order = KIND == kWeight && g.order;
+  if constexpr (BROW) {
+    bbase = W + (int64_t)n0 * g.K;
+    bstep = kStep;
 #pragma unroll
-      for (int q = 0; q < decltype(count)::value; ++q)
-        to_lds(at, off[q], lds + (q * WAVES + w) * 512);
-    } else {
-      const bool in = k + piece / 2 < r1;
+    for (int q = 0; q < BL; ++q) {
+      const int r = 16 * (q * WAVES + w) + (lane >> 2);
+      boff[q] = n0 + r < cols ? (uint32_t)((int64_t)r * g.K + piece) * 2 : kNowhere;
+    }
+  } else {
+    const int64_t ld = KIND == kInput ? g.K : g.xs;
+    bbase = (KIND == kInput ? W : static_cast<const uint16_t*>(g.X)) + n0;
+    bstep = kStep * ld;
+    if (order) bstep = 0;
+    else bbase += r0 * ld;
 #pragma unroll
-      for (int q = 0; q < decltype(count)::value; ++q) {
-        if (in) to_lds(at, off[q], lds + (q * WAVES + w) * 512);
-        else zero_lds(lds + (q * WAVES + w) * 512, lane);
+    for (int q = 0; q < BL; ++q) {
+      const int kr = (q * WAVES + w) * BPER + lane / BLANES;
+      const int c = ((lane % BLANES) ^ (4 * (kr & 3))) * 8;
+      boff[q] = n0 + c < cols ? (uint32_t)((order ? 0 : kr * ld) + c) * 2 : kNowhere;
+    }
+  }
+  // with `order`: the slots of the step after the last loaded one, ahead of their use
+  // (scalar loads, which do not stand in line with the operands' loads)
+  int32_t slot[BL];
+  auto fetch_slots = [&](int64_t k) {
+    if constexpr (KIND == kWeight) {
+      const auto* o = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)g.order;
+#pragma unroll
+      for (int q = 0; q < BL; ++q) {
+        int32_t i = 0;
+#pragma unroll
+        for (int j = 0; j < BPER; ++j) {
+          const int64_t p = k + (q * WAVES + w) * BPER + j;
+          const int32_t at = o[p < r1 ? p : r1 - 1];
+          i = lane / BLANES == j ? at : i;
+        }
+        slot[q] = i;
       }
     }
   };
-  // by reduction: a piece of 512 elements is 512 / WIDE reduction rows of WIDE elements
-  auto load_red = [&](const char* base, int64_t ld, int limit, uint16_t* lds, int64_t k,
-                      auto count, auto wide, auto row_of) {
-    constexpr int WIDE = decltype(wide)::value, PER = 512 / WIDE, LANES = 64 / PER;
-#pragma unroll
-    for (int q = 0; q < decltype(count)::value; ++q) {
-      const int kr = (q * WAVES + w) * PER + lane / LANES;     // reduction row in the step
-      const int c = ((lane % LANES) ^ (2 * (kr & 3))) * 8;     // first column
-      const int64_t x = row_of(k + kr);
-      if (x >= 0)
-        to_lds(base + (c < limit ? c : 0) * 2 + x * ld * 2, 0, lds + (q * WAVES + w) * 512);
-      else
-        zero_lds(lds + (q * WAVES + w) * 512, lane);
-    }
-  };
+
+  // Loads the operands of the reduction values [k, k + 32).
   auto load = [&](uint16_t* A, uint16_t* B, int64_t k) {
-    if constexpr (AROW)
-      load_row(abase, aoff, AE, A, k, std::integral_constant<int, AE>{});
-    else
-      load_red(abase, g.dys, (int)(end - row0), A, k, std::integral_constant<int, AE>{},
-               std::integral_constant<int, BM>{},
-               [&](int64_t p) { return p < r1 ? p : (int64_t)-1; });
-    if constexpr (BROW)
-      load_row(bbase, boff, BE, B, k, std::integral_constant<int, BE>{});
-    else if constexpr (KIND == kInput)
-      load_red(reinterpret_cast<const char*>(W + n0), g.K, cols - n0, B, k,
-               std::integral_constant<int, BE>{}, std::integral_constant<int, BN>{},
-               [&](int64_t n) { return n < r1 ? n : (int64_t)-1; });
-    else
-      load_red(reinterpret_cast<const char*>(static_cast<const uint16_t*>(g.X) + n0), g.xs,
-               cols - n0, B, k, std::integral_constant<int, BE>{},
-               std::integral_constant<int, BN>{},
-               [&](int64_t p) { return p < r1 ? x_row(g, p) : (int64_t)-1; });
+    const bool whole = k + kStep <= r1;
+#pragma unroll
+    for (int q = 0; q < AL; ++q) {
+      uint32_t off = aoff[q];
+      if (!whole) {
+        const int at = AROW ? piece : (q * WAVES + w) * APER + lane / ALANES;
+        off = k + at < r1 ? off : kNowhere;
+      }
+      to_lds(abase, off, A + (q * WAVES + w) * 512);
+    }
+    abase += astep;
+#pragma unroll
+    for (int q = 0; q < BL; ++q) {
+      uint32_t off = boff[q];
+      if (KIND == kWeight && order) {
+        const int64_t x = token_of(g, slot[q]);
+        off = x >= 0 && off != kNowhere ? off + (uint32_t)(x * g.xs) * 2 : kNowhere;
+      }
+      if (!whole) {
+        const int at = BROW ? piece : (q * WAVES + w) * BPER + lane / BLANES;
+        off = k + at < r1 ? off : kNowhere;
+      }
+      to_lds(bbase, off, B + (q * WAVES + w) * 512);
+    }
+    bbase += bstep;
+    if (KIND == kWeight && order) fetch_slots(k + kStep);
   };
 
   f32x16 acc[TI][TJ];
@@ -541,68 +600,74 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
   auto frag = [&](const uint16_t* L, int row, int s, auto byrow, auto wide) -> s16x8 {
     if constexpr (decltype(byrow)::value) {
       const int r = row + rl;
-      return *reinterpret_cast<const s16x8*>(L + r * kStep + (((2 * s + kg) ^ (r & 7)) * 8));
+      return *reinterpret_cast<const s16x8*>(L + r * kStep + (((2 * s + kg) ^ (r >> 2 & 3)) * 8));
     } else {
       constexpr int WIDE = decltype(wide)::value;
       // the 16 lanes of a group: reduction row + (lane & 15) / 4, columns 4 (lane & 3) ..
       const int kr = 16 * s + 8 * kg + ((lane & 15) >> 2);
       const int c = row + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-      const int at = ((c >> 3) ^ (2 * (kr & 3))) * 8 + (c & 7);
+      const int at = ((c >> 3) ^ (4 * (kr & 3))) * 8 + (c & 7);
       typedef __attribute__((address_space(3))) s16x4* P;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + kr * WIDE + at));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + (kr + 4) * WIDE + at));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   };
-  // fragments of the next 16 reduction values are read while this 16's products run
-  auto multiply = [&](const uint16_t* A, const uint16_t* B) {
+
+  const int steps = (int)((r1 - r0 + kStep - 1) / kStep);
+  // Step t on buffers A and B; An and Bn are those of step t + 3, last read in step t - 1.
+  auto step = [&](const uint16_t* A, const uint16_t* B, uint16_t* An, uint16_t* Bn, int t) {
     s16x8 a[2][TI], b[2][TJ];
-    auto read = [&](int s) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
-        b[s & 1][j] = frag(B, WN * wn + 32 * j, s, std::integral_constant<bool, BROW>{},
-                           std::integral_constant<int, BN>{});
+        b[s][j] = frag(B, WN * wn + 32 * j, s, std::integral_constant<bool, BROW>{},
+                       std::integral_constant<int, BN>{});
 #pragma unroll
       for (int i = 0; i < TI; ++i)
-        a[s & 1][i] = frag(A, WM * wm + 32 * i, s, std::integral_constant<bool, AROW>{},
-                           std::integral_constant<int, BM>{});
-    };
-    read(0);
-#pragma unroll
-    for (int s = 0; s < kStep / 16; ++s) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (s + 1 < kStep / 16) read(s + 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = mma<TY>(b[s & 1][j], a[s & 1][i], acc[i][j]);
+        a[s][i] = frag(A, WM * wm + 32 * i, s, std::integral_constant<bool, AROW>{},
+                       std::integral_constant<int, BM>{});
     }
-    __builtin_amdgcn_sched_barrier(0);
+    // the loads of step t + 1 have landed when at most those of t + 2 and t + 3 are in flight
+    if (t + 3 < steps) {
+      load(An, Bn, r0 + (int64_t)(t + 3) * kStep);
+      arrive<2 * LOADS>();
+    } else if (t + 2 < steps) {
+      arrive<LOADS>();
+    } else {
+      arrive<0>();
+    }
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = mma<TY>(b[s][j], a[s][i], acc[i][j]);
+    __builtin_amdgcn_s_setprio(0);
+    if constexpr (PAIRED) arrive_only();
   };
 
-  // two steps a round; an odd one goes first
-  int64_t k = r0;
-  const int steps = (int)((r1 - r0 + kStep - 1) / kStep);
-  if (steps & 1) {
-    load(A1, B1, k);
-    __syncthreads();
-    k += kStep;
-    if (k < r1) load(A0, B0, k);
-    multiply(A1, B1);
-    __syncthreads();
-  } else {
-    if (k < r1) load(A0, B0, k);
-    __syncthreads();
-  }
-  for (int t = steps >> 1; t > 0; --t) {
-    load(A1, B1, k + kStep);
-    multiply(A0, B0);
-    __syncthreads();
-    k += 2 * kStep;
-    if (t > 1) load(A0, B0, k);
-    multiply(A1, B1);
-    __syncthreads();
+  if (steps > 0) {
+    if (KIND == kWeight && order) fetch_slots(r0);
+    load(A0, B0, r0);
+    if (steps > 1) load(A1, B1, r0 + kStep);
+    if (steps > 2) load(A2, B2, r0 + 2 * kStep);
+    if (steps > 2) arrive<2 * LOADS>();
+    else arrive<0>();
+    if (PAIRED && w >= WAVES / 2) arrive_only();
+    int t = 0;
+    for (; t + 4 <= steps; t += 4) {
+      step(A0, B0, A3, B3, t);
+      step(A1, B1, A0, B0, t + 1);
+      step(A2, B2, A1, B1, t + 2);
+      step(A3, B3, A2, B2, t + 3);
+    }
+    if (t < steps) step(A0, B0, A3, B3, t);
+    if (t + 1 < steps) step(A1, B1, A0, B0, t + 1);
+    if (t + 2 < steps) step(A2, B2, A1, B1, t + 2);
+    if (PAIRED && w < WAVES / 2) arrive_only();
   }
 
   // acc[i][j][v]: row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part
@@ -623,16 +688,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
         }
     }
   } else {
-    // through LDS, 32 rows at a time, so that a store is whole 16-byte pieces of rows
-    constexpr int PITCH = WN + 8;
-    uint16_t* out = (w % 2 ? A1 : A0) + (w / 2) * 32 * PITCH;
-    static_assert(32 * PITCH * ((WAVES + 1) / 2) <= BM * kStep, "the waves' parts fit");
+    // through LDS, 32 rows at a time, so that a store is whole 16-byte pieces of rows; every
+    // wave is past its last read of the tiles here
+    constexpr int PITCH = WN + 8, EACH = BM * kStep / (32 * PITCH);   // waves an array holds
+    static_assert(EACH * 4 >= WAVES, "the waves' parts fit");
+    uint16_t* const arr = w / EACH == 0 ? A0 : w / EACH == 1 ? A1 : w / EACH == 2 ? A2 : A3;
+    uint16_t* out = arr + (w % EACH) * 32 * PITCH;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int64_t rw = row0 + WM * wm + 32 * i;             // the first of 32 rows
-      float live = 1.f;
-      if constexpr (KIND == kForward)
-        if (g.order && rw + rl < end && e < g.E && x_row(g, rw + rl) < 0) live = 0.f;
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
 #pragma unroll
@@ -642,7 +706,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
 #pragma unroll
           for (int v = 0; v < 4; ++v) x[v] = acc[i][j][4 * q + v];
           if constexpr (KIND == kForward) {
-            if (live == 0.f) x[0] = x[1] = x[2] = x[3] = 0.f;
             const int n = n0 + WN * wn + c;
             if (g.b && e < g.E && n < cols) {
               const float* b = g.b + (int64_t)e * g.N + n;
@@ -752,7 +815,13 @@ static experts::Product expert_product(const void* X, int64_t xs, int64_t x_rows
                                        const int32_t* order, int k, const int32_t* offsets,
                                        int64_t n, int E, int K, const void* W, int N) {
   experts::Product g{};
-  g.X = X; g.xs = xs; g.x_rows = x_rows; g.order = order; g.k = k;
+  g.X = X; g.xs = xs; g.x_rows = x_rows; g.order = order;
+  // with 2^b >= k: kmul = floor(2^(31 + b) / k) + 1 exceeds the quotient by at most 1, which
+  // moves i * kmul / 2^(31 + b) by less than 2^-b <= 1 / k: never past the next integer
+  int bits = 0;
+  while (((int64_t)1 << bits) < k) ++bits;
+  g.kshift = 31 + bits;
+  g.kmul = (((uint64_t)1 << g.kshift) / (uint64_t)(k > 0 ? k : 1)) + 1;
   g.offsets = offsets; g.n = n; g.E = E; g.K = K; g.N = N; g.W = W;
   return g;
 }
@@ -765,11 +834,11 @@ static int64_t most_tiles(int64_t n, int E, int BM) { return n / BM + E + 1; }
 static bool wide_ok(const experts::Product& g, int dtype) {
   auto ok = [](const void* p, int64_t stride) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % 8 == 0 &&
-           stride < ((int64_t)1 << 22);
+           stride < ((int64_t)1 << 22);          // 256 rows: 2^31 bytes
   };
   if (dtype == kEltF32 || g.K % 8 || g.N % 8) return false;
   if (!ok(g.X, g.xs) || !ok(g.W, g.K) || !ok(g.Y, g.ys) || !ok(g.dY, g.dys)) return false;
-  return !g.order || g.x_rows * g.xs < ((int64_t)1 << 31);
+  return !g.order || g.x_rows * g.xs < ((int64_t)1 << 31) - ((int64_t)1 << 20);
 }
 
 template <int TY, int KIND, int BM, int BN, int WM, int WN>
