@@ -249,6 +249,13 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product g) {
   }
 }
 
+// A value that is the same in the whole wave, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Row tiles that the experts (and the positions of none) need.
 template <int BM>
 __device__ __forceinline__ int64_t count_tiles(const Product& g) {
@@ -261,19 +268,6 @@ __device__ __forceinline__ int64_t count_tiles(const Product& g) {
   }
   for (int d = 1; d < 64; d <<= 1) tiles += __shfl_xor(tiles, d);
   return tiles;
-}
-
-// The block's tile among rows * inner tiles, inner first: blocks go to the 8 XCDs in turn, and
-// each XCD, which has an L2 of its own, gets a run of neighbouring tiles that share operands.
-// The split is over the tiles that there are, not over the grid, which has more.
-__device__ __forceinline__ bool place_tile(const Product& g, int64_t rows, int inner,
-                                           int64_t* row, int* in) {
-  const uint32_t total = (uint32_t)(rows * inner), b = blockIdx.x, per = total / kXcds;
-  if (b >= total) return false;
-  const uint32_t t = b < per * kXcds ? (b % kXcds) * per + b / kXcds : b;
-  *row = t / (uint32_t)inner;
-  *in = (int)(t % (uint32_t)inner);
-  return true;
 }
 
 // The weight gradient's reduction is cut into slices of g.slice positions, so that an expert
@@ -333,6 +327,78 @@ __device__ __forceinline__ bool find_slice(const Product& g, int64_t unit, int e
   return false;
 }
 
+// What a tile costs beside its rounds of 64 (its first loads, its stores), in rounds.
+constexpr int64_t kTileCost = 10;
+// The first of the weight gradient's tiles (units in order, `tiles` each) that belongs to the
+// last (8 - x) eighths of their cost.
+__device__ __forceinline__ int64_t first_by_cost(const Product& g, int tiles, int x) {
+  const int lane = threadIdx.x & 63;
+  const int64_t full = g.slice / 64 + kTileCost;               // of a whole slice's tile
+  auto cost = [&](int64_t rows, int c) {
+    return c > 0 ? (c - 1) * full + (rows - (c - 1) * g.slice + 63) / 64 + kTileCost : 0;
+  };
+  int64_t total = 0;
+  for (int e = lane; e < g.E; e += 64) {
+    int64_t lo, hi;
+    const int c = slices_of(g, e, &lo, &hi);
+    total += cost(hi - lo, c);
+  }
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  const int64_t target = total * tiles * x / kXcds;
+  int64_t run = 0, units = 0;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    int64_t lo = 0, hi = 0;
+    const int c = e0 + lane < g.E ? slices_of(g, e0 + lane, &lo, &hi) : 0;
+    const int64_t mine = cost(hi - lo, c) * tiles;
+    int64_t upto = mine;
+    int cupto = c;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t v = __shfl_up(upto, d);
+      const int y = __shfl_up(cupto, d);
+      if (lane >= d) {
+        upto += v;
+        cupto += y;
+      }
+    }
+    const uint64_t past = __ballot(run + upto > target);
+    if (past) {
+      const int at = __ffsll((unsigned long long)past) - 1;
+      int64_t left = target - run - __shfl(upto - mine, at);
+      const int64_t rows = __shfl(hi - lo, at);
+      const int count = __shfl(c, at);
+      int64_t i = left / (full * tiles);
+      i = i < count - 1 ? i : count - 1;
+      left -= i * full * tiles;
+      const int64_t each = i < count - 1 ? full : cost(rows - i * g.slice, 1);
+      int64_t t = (left + each - 1) / each;
+      t = t < tiles ? t : tiles;
+      return (units + __shfl(cupto - c, at) + i) * tiles + t;
+    }
+    run += __shfl(upto, 63);
+    units += __shfl(cupto, 63);
+  }
+  return units * tiles;
+}
+
+// The block's first tile and the end of its XCD's part of all tiles: blocks go to the 8 XCDs in
+// turn, and each XCD, which has an L2 of its own, has a run of neighbouring tiles that share
+// operands.
+template <int KIND, int BM>
+__device__ __forceinline__ void part_of(const Product& g, int64_t* first, int64_t* last) {
+  const int x = blockIdx.x % kXcds;
+  if constexpr (KIND == kWeight) {
+    const int tiles = g.row_tiles * g.col_tiles;
+    *first = first_by_cost(g, tiles, x);
+    *last = x + 1 < (int)kXcds ? first_by_cost(g, tiles, x + 1) : count_slices(g) * tiles;
+  } else {
+    const int64_t total = count_tiles<BM>(g) * g.col_tiles;
+    *first = total * x / kXcds;
+    *last = total * (x + 1) / kXcds;
+  }
+  *first = uniform(*first) + blockIdx.x / kXcds;
+  *last = uniform(*last);
+}
+
 // dW of the experts with several slices: their partial sums added in order.  A block has
 // kJoin elements of one expert.
 constexpr int kJoin = 8192;
@@ -365,22 +431,24 @@ __device__ __forceinline__ uint32_t keep_positive(uint32_t h, uint32_t m) {
 // ------------------------------------------------------------------ 16-bit operands, staged
 // The products of 16-bit operands in 16-byte pieces (widths and strides multiples of 8,
 // 16-byte aligned arrays).  A block has a BM x BN output tile and a wave a WM x WN part of it
-// in 32 x 32 matrix-core tiles; the reduction advances 32 at a time through a ring of four LDS
-// buffers.  Tiles go from memory to LDS directly (one 16-byte load a lane, 1 KB a wave, no
-// registers in between), three steps ahead of their use; the loads' own bounds check gives
-// zeros for rows and reduction values that are not there.
+// in 32 x 32 matrix-core tiles.  The reduction advances in rounds of 64 values, so that a row
+// is read 128 bytes at a time (half of that costs the first-level cache twice the requests,
+// and the forward product 729 us instead of ... at 65536 x 2208 x 2048).  Tiles go from
+// memory to LDS directly (one 16-byte load a lane, 1 KB a wave, no registers in between); the
+// loads' own bounds check gives zeros for rows and reduction values that are not there.
 //
-// A step of a wave is a part that moves data (its fragments of the step from LDS to
-// registers, its share of the loads of the step three on) and a part that computes (16
-// matrix-core instructions in 256 x 256 tiles).  With eight waves, two on each SIMD, the
-// second four run half a step behind the first: while one of a SIMD's waves computes the
-// other moves data, and the matrix cores never wait for both.  Barriers end both parts.  With
-// four waves there are two blocks a compute unit, which interleave by themselves, and one
-// barrier a step.
+// LDS is a ring of five slots of one operand's round, in the order A0 B0 A1 B1 ...: while
+// round j is read, B of round j + 1 and A of round j + 2 are on their way.  A round has two
+// half steps, and a half step two parts: one that moves data (the wave's fragments from LDS
+// to registers, its share of the loads of one operand) and one that computes (16 matrix-core
+// instructions a wave in 256 x 256 tiles).  With eight waves, two on each SIMD, the second
+// four run one part behind the first: while one of a SIMD's waves computes the other moves
+// data.  Barriers end both parts.  With four waves there are two blocks a compute unit, which
+// interleave by themselves, and one barrier a half step.
 //
 // An operand lies in LDS in one of two forms; the banks serve 256 bytes at a time:
-//   by rows (32 reduction values of one row, 64 bytes): a fragment is one 16-byte read of 32
-//     rows.  The 16-byte piece c of row r is at c ^ (r / 4 & 3), so that sixteen lanes that
+//   by rows (64 reduction values of one row, 128 bytes): a fragment is one 16-byte read of 32
+//     rows.  The 16-byte piece c of row r is at c ^ (r / 2 & 7), so that sixteen lanes that
 //     read piece c of sixteen rows touch all banks.
 //   by reduction (BM or BN values of one reduction index): a fragment is two transposing
 //     reads, each giving a lane four reduction values of its row.  32 lanes read 64 bytes of
@@ -388,10 +456,14 @@ __device__ __forceinline__ uint32_t keep_positive(uint32_t h, uint32_t m) {
 //     the four over the banks.
 // The matrix cores take the columns as their rows: a lane then holds four neighbouring
 // columns of one output row, stored together.
+//
+// Blocks stay: each takes tiles of its XCD's part until there are none.  The parts have equal
+// cost, which for the weight gradient, whose tiles are as long as their expert has rows, is
+// not equal numbers.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kStep = 32;                      // reduction values a step
+constexpr int kRound = 64, kHalf = 32;         // reduction values
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;     // an offset past every buffer: reads zeros
 
 template <int TY>
@@ -413,11 +485,14 @@ __device__ __forceinline__ void to_lds(const void* base, uint32_t off, uint16_t*
 }
 
 // Ends a part: the wave's LDS reads are done and at most LOADS of its loads are in flight, in
-// every wave.
+// every wave (LOADS < 0: any number).
 template <int LOADS>
 __device__ __forceinline__ void arrive() {
   __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+  if constexpr (LOADS < 0)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 __device__ __forceinline__ void arrive_only() {
@@ -426,38 +501,33 @@ __device__ __forceinline__ void arrive_only() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// A value that is the same in the whole wave, in scalar registers.
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 template <int TY, int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Product g) {
   constexpr int WAVES = (BM / WM) * (BN / WN), WN_WAVES = BN / WN;
   constexpr bool AROW = KIND != kWeight, BROW = KIND == kForward, PAIRED = WAVES == 8;
   constexpr int TI = WM / 32, TJ = WN / 32;
-  constexpr int AL = BM * kStep / 512 / WAVES, BL = BN * kStep / 512 / WAVES, LOADS = AL + BL;
-  __shared__ __attribute__((aligned(16))) uint16_t A0[BM * kStep], A1[BM * kStep], A2[BM * kStep],
-      A3[BM * kStep];
-  __shared__ __attribute__((aligned(16))) uint16_t B0[BN * kStep], B1[BN * kStep], B2[BN * kStep],
-      B3[BN * kStep];
+  constexpr int AL = BM * kRound / 512 / WAVES, BL = BN * kRound / 512 / WAVES;
+  static_assert(BM == BN, "a ring slot holds either operand");
+  __shared__ __attribute__((aligned(16))) uint16_t R0[BM * kRound], R1[BM * kRound],
+      R2[BM * kRound], R3[BM * kRound], R4[BM * kRound];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / WN_WAVES, wn = w % WN_WAVES;
+  const int rl = lane & 31, kg = lane >> 5;
+  const int cols = KIND == kForward ? g.N : g.K;
 
+  int64_t at, last;
+  const int64_t stride = gridDim.x / kXcds;
+  part_of<KIND, BM>(g, &at, &last);
+  for (; at < last; at += stride) {
   // which tile
-  int e;
+  int e, n0;
   int64_t row0, end, r0 = 0, r1;
-  int n0;
   float* dW = g.dW;
   if constexpr (KIND == kWeight) {
+    const int tiles = g.row_tiles * g.col_tiles, tile = (int)(at % tiles);
     Slice u;
-    int64_t unit;
-    int tile;
-    if (!place_tile(g, count_slices(g), g.row_tiles * g.col_tiles, &unit, &tile)) return;
-    if (!find_slice(g, unit, -1, &u)) return;
+    if (!find_slice(g, at / tiles, -1, &u)) break;
     e = u.expert;
     r0 = u.lo;
     r1 = u.hi;
@@ -467,10 +537,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     n0 = tile % g.col_tiles * BN;
     end = g.N;
   } else {
-    int64_t mt;
-    if (!place_tile(g, count_tiles<BM>(g), g.col_tiles, &mt, &n0)) return;
-    n0 *= BN;
-    if (!find_tile<BM>(g, mt, &e, &row0, &end)) return;
+    n0 = (int)(at % g.col_tiles) * BN;
+    if (!find_tile<BM>(g, at / g.col_tiles, &e, &row0, &end)) break;
     r1 = e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
   }
   e = __builtin_amdgcn_readfirstlane(e);
@@ -479,35 +547,36 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
   end = uniform(end);
   r0 = uniform(r0);
   r1 = uniform(r1);
-  const int cols = KIND == kForward ? g.N : g.K;
   const uint16_t* W = static_cast<const uint16_t*>(g.W) + (int64_t)(e < g.E ? e : 0) * g.N * g.K;
 
-  // Where a lane's loads are, in bytes from the operand's base at the step's first reduction
-  // value.  By rows: lane i of piece q has row 16 q + i / 4 and its 16 bytes
-  // (i % 4) ^ (i / 16).  By reduction: 512 / WIDE reduction rows a piece.
-  const int piece = ((lane & 3) ^ (lane >> 4)) * 8;            // first reduction value
+  // Where a lane's loads are, in bytes from the operand's base at the round's first reduction
+  // value.  By rows: lane i of piece q has row 8 q + i / 8 and its 16 bytes
+  // (i % 8) ^ (row / 2 & 7).  By reduction: 512 / WIDE reduction rows a piece.
   const uint16_t* abase;
   const uint16_t* bbase;
-  int64_t astep, bstep;                                        // elements from step to step
+  int64_t astep, bstep;                                        // elements from round to round
   uint32_t aoff[AL], boff[BL];
   constexpr int APER = 512 / BM, BPER = 512 / BN;              // by reduction: rows a piece
   constexpr int ALANES = 64 / APER, BLANES = 64 / BPER;
+  auto piece = [&](int q) {                                    // first reduction value
+    return ((lane & 7) ^ ((4 * (q * WAVES + w) + (lane >> 4)) & 7)) * 8;
+  };
   if constexpr (AROW) {
     abase = static_cast<const uint16_t*>(KIND == kForward ? g.X : g.dY);
     const int64_t ld = KIND == kForward ? g.xs : g.dys;
     const bool gather = KIND == kForward && g.order;
     if (!gather) abase += row0 * ld;
-    astep = kStep;
+    astep = kRound;
 #pragma unroll
     for (int q = 0; q < AL; ++q) {
-      const int64_t r = row0 + 16 * (q * WAVES + w) + (lane >> 2);
+      const int64_t r = row0 + 8 * (q * WAVES + w) + (lane >> 3);
       int64_t x = r < end ? r - row0 : -1;
       if (gather && x >= 0) x = x_row(g, r);
-      aoff[q] = x >= 0 ? (uint32_t)(x * ld + piece) * 2 : kNowhere;
+      aoff[q] = x >= 0 ? (uint32_t)(x * ld + piece(q)) * 2 : kNowhere;
     }
   } else {
     abase = static_cast<const uint16_t*>(g.dY) + r0 * g.dys + row0;
-    astep = kStep * g.dys;
+    astep = kRound * g.dys;
 #pragma unroll
     for (int q = 0; q < AL; ++q) {
       const int kr = (q * WAVES + w) * APER + lane / ALANES;
@@ -518,16 +587,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
   const bool order = KIND == kWeight && g.order;
   if constexpr (BROW) {
     bbase = W + (int64_t)n0 * g.K;
-    bstep = kStep;
+    bstep = kRound;
 #pragma unroll
     for (int q = 0; q < BL; ++q) {
-      const int r = 16 * (q * WAVES + w) + (lane >> 2);
-      boff[q] = n0 + r < cols ? (uint32_t)((int64_t)r * g.K + piece) * 2 : kNowhere;
+      const int r = 8 * (q * WAVES + w) + (lane >> 3);
+      boff[q] = n0 + r < cols ? (uint32_t)((int64_t)r * g.K + piece(q)) * 2 : kNowhere;
     }
   } else {
     const int64_t ld = KIND == kInput ? g.K : g.xs;
     bbase = (KIND == kInput ? W : static_cast<const uint16_t*>(g.X)) + n0;
-    bstep = kStep * ld;
+    bstep = kRound * ld;
     if (order) bstep = 0;
     else bbase += r0 * ld;
 #pragma unroll
@@ -537,7 +606,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
       boff[q] = n0 + c < cols ? (uint32_t)((order ? 0 : kr * ld) + c) * 2 : kNowhere;
     }
   }
-  // with `order`: the slots of the step after the last loaded one, ahead of their use
+  // with `order`: the slots of the round after the last loaded one, ahead of their use
   // (scalar loads, which do not stand in line with the operands' loads)
   int32_t slot[BL];
   auto fetch_slots = [&](int64_t k) {
@@ -549,27 +618,30 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
 #pragma unroll
         for (int j = 0; j < BPER; ++j) {
           const int64_t p = k + (q * WAVES + w) * BPER + j;
-          const int32_t at = o[p < r1 ? p : r1 - 1];
-          i = lane / BLANES == j ? at : i;
+          const int32_t v = o[p < r1 ? p : r1 - 1];
+          i = lane / BLANES == j ? v : i;
         }
         slot[q] = i;
       }
     }
   };
 
-  // Loads the operands of the reduction values [k, k + 32).
-  auto load = [&](uint16_t* A, uint16_t* B, int64_t k) {
-    const bool whole = k + kStep <= r1;
+  // Load the next round of an operand, reduction values [k, k + 64).
+  auto load_a = [&](uint16_t* A, int64_t k) {
+    const bool whole = k + kRound <= r1;
 #pragma unroll
     for (int q = 0; q < AL; ++q) {
       uint32_t off = aoff[q];
       if (!whole) {
-        const int at = AROW ? piece : (q * WAVES + w) * APER + lane / ALANES;
-        off = k + at < r1 ? off : kNowhere;
+        const int i = AROW ? piece(q) : (q * WAVES + w) * APER + lane / ALANES;
+        off = k + i < r1 ? off : kNowhere;
       }
       to_lds(abase, off, A + (q * WAVES + w) * 512);
     }
     abase += astep;
+  };
+  auto load_b = [&](uint16_t* B, int64_t k) {
+    const bool whole = k + kRound <= r1;
 #pragma unroll
     for (int q = 0; q < BL; ++q) {
       uint32_t off = boff[q];
@@ -578,13 +650,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
         off = x >= 0 && off != kNowhere ? off + (uint32_t)(x * g.xs) * 2 : kNowhere;
       }
       if (!whole) {
-        const int at = BROW ? piece : (q * WAVES + w) * BPER + lane / BLANES;
-        off = k + at < r1 ? off : kNowhere;
+        const int i = BROW ? piece(q) : (q * WAVES + w) * BPER + lane / BLANES;
+        off = k + i < r1 ? off : kNowhere;
       }
       to_lds(bbase, off, B + (q * WAVES + w) * 512);
     }
     bbase += bstep;
-    if (KIND == kWeight && order) fetch_slots(k + kStep);
+    if (KIND == kWeight && order) fetch_slots(k + kRound);
   };
 
   f32x16 acc[TI][TJ];
@@ -595,49 +667,51 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-  const int rl = lane & 31, kg = lane >> 5;
-  // fragment of 32 rows from `row`, reduction values 16 s + 8 kg .. + 8
-  auto frag = [&](const uint16_t* L, int row, int s, auto byrow, auto wide) -> s16x8 {
+  // Where a lane's fragments are in a slot, in bytes: those of the operand's 32-row tile i and
+  // the reduction values 16 s + 8 kg .. + 8 are at `at` with a few bits flipped, plus a constant.
+  // (By reduction: the 16 lanes of a group have reduction row + (lane & 15) / 4 and columns
+  // 4 (lane & 3) ..)
+  auto frag_at = [&](int row, bool byrow, int wide) -> uint32_t {
+    if (byrow) return (row + rl) * kRound * 2 + ((kg ^ (rl >> 1 & 7)) * 16);
+    const int kr = 8 * kg + ((lane & 15) >> 2);
+    const int c = row + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    return kr * wide * 2 + ((c >> 3) ^ (4 * (kr & 3))) * 16 + (c & 7) * 2;
+  };
+  const uint32_t afrag = frag_at(WM * wm, AROW, BM), bfrag = frag_at(WN * wn, BROW, BN);
+  auto frag = [&](const uint16_t* L, uint32_t at, int i, int s, auto byrow, auto wide) -> s16x8 {
+    const char* p = reinterpret_cast<const char*>(L);
     if constexpr (decltype(byrow)::value) {
-      const int r = row + rl;
-      return *reinterpret_cast<const s16x8*>(L + r * kStep + (((2 * s + kg) ^ (r >> 2 & 3)) * 8));
+      return *reinterpret_cast<const s16x8*>(p + (at ^ (32 * s)) + 32 * i * kRound * 2);
     } else {
       constexpr int WIDE = decltype(wide)::value;
-      // the 16 lanes of a group: reduction row + (lane & 15) / 4, columns 4 (lane & 3) ..
-      const int kr = 16 * s + 8 * kg + ((lane & 15) >> 2);
-      const int c = row + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-      const int at = ((c >> 3) ^ (4 * (kr & 3))) * 8 + (c & 7);
       typedef __attribute__((address_space(3))) s16x4* P;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + kr * WIDE + at));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + (kr + 4) * WIDE + at));
+      p += (at ^ (64 * i)) + 16 * s * WIDE * 2;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 4 * WIDE * 2));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   };
 
-  const int steps = (int)((r1 - r0 + kStep - 1) / kStep);
-  // Step t on buffers A and B; An and Bn are those of step t + 3, last read in step t - 1.
-  auto step = [&](const uint16_t* A, const uint16_t* B, uint16_t* An, uint16_t* Bn, int t) {
+  const int halves = (int)((r1 - r0 + kHalf - 1) / kHalf), rounds = (halves + 1) >> 1;
+  // Half step h of a round: `ahead` issues its loads and arrives.
+  auto half = [&](const uint16_t* A, const uint16_t* B, auto h, auto ahead) {
     s16x8 a[2][TI], b[2][TJ];
+    // the addresses are made here each time: kept for all slots they would take the registers
+    // that the accumulators need
+    uint32_t aat = afrag, bat = bfrag;
+    asm volatile("" : "+v"(aat), "+v"(bat));
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
-        b[s][j] = frag(B, WN * wn + 32 * j, s, std::integral_constant<bool, BROW>{},
-                       std::integral_constant<int, BN>{});
+        b[s][j] = frag(B, bat, j, 2 * decltype(h)::value + s,
+                       std::integral_constant<bool, BROW>{}, std::integral_constant<int, BN>{});
 #pragma unroll
       for (int i = 0; i < TI; ++i)
-        a[s][i] = frag(A, WM * wm + 32 * i, s, std::integral_constant<bool, AROW>{},
-                       std::integral_constant<int, BM>{});
+        a[s][i] = frag(A, aat, i, 2 * decltype(h)::value + s,
+                       std::integral_constant<bool, AROW>{}, std::integral_constant<int, BM>{});
     }
-    // the loads of step t + 1 have landed when at most those of t + 2 and t + 3 are in flight
-    if (t + 3 < steps) {
-      load(An, Bn, r0 + (int64_t)(t + 3) * kStep);
-      arrive<2 * LOADS>();
-    } else if (t + 2 < steps) {
-      arrive<LOADS>();
-    } else {
-      arrive<0>();
-    }
+    ahead();
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -648,25 +722,43 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     __builtin_amdgcn_s_setprio(0);
     if constexpr (PAIRED) arrive_only();
   };
+  // Round j on A and B; Bn takes B of round j + 1 (its slot held A of round j - 1), An takes A
+  // of round j + 2 (its slot held B of round j - 1).
+  auto round = [&](const uint16_t* A, const uint16_t* B, uint16_t* Bn, uint16_t* An, int j) {
+    half(A, B, std::integral_constant<int, 0>{}, [&] {
+      if (j + 1 < rounds) load_b(Bn, r0 + (int64_t)(j + 1) * kRound);
+      arrive<-1>();
+    });
+    if (2 * j + 1 < halves)
+      half(A, B, std::integral_constant<int, 1>{}, [&] {
+        // round j + 1 has landed when at most A of round j + 2 is in flight
+        if (j + 2 < rounds) {
+          load_a(An, r0 + (int64_t)(j + 2) * kRound);
+          arrive<AL>();
+        } else {
+          arrive<0>();
+        }
+      });
+  };
 
-  if (steps > 0) {
+  if (halves > 0) {
     if (KIND == kWeight && order) fetch_slots(r0);
-    load(A0, B0, r0);
-    if (steps > 1) load(A1, B1, r0 + kStep);
-    if (steps > 2) load(A2, B2, r0 + 2 * kStep);
-    if (steps > 2) arrive<2 * LOADS>();
-    else arrive<0>();
-    if (PAIRED && w >= WAVES / 2) arrive_only();
-    int t = 0;
-    for (; t + 4 <= steps; t += 4) {
-      step(A0, B0, A3, B3, t);
-      step(A1, B1, A0, B0, t + 1);
-      step(A2, B2, A1, B1, t + 2);
-      step(A3, B3, A2, B2, t + 3);
+    load_a(R0, r0);
+    load_b(R1, r0);
+    if (rounds > 1) {
+      load_a(R2, r0 + kRound);
+      arrive<AL>();
+    } else {
+      arrive<0>();
     }
-    if (t < steps) step(A0, B0, A3, B3, t);
-    if (t + 1 < steps) step(A1, B1, A0, B0, t + 1);
-    if (t + 2 < steps) step(A2, B2, A1, B1, t + 2);
+    if (PAIRED && w >= WAVES / 2) arrive_only();
+    for (int j = 0; j < rounds; j += 5) {
+      round(R0, R1, R3, R4, j);
+      if (j + 1 < rounds) round(R2, R3, R0, R1, j + 1);
+      if (j + 2 < rounds) round(R4, R0, R2, R3, j + 2);
+      if (j + 3 < rounds) round(R1, R2, R4, R0, j + 3);
+      if (j + 4 < rounds) round(R3, R4, R1, R2, j + 4);
+    }
     if (PAIRED && w < WAVES / 2) arrive_only();
   }
 
@@ -690,10 +782,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
   } else {
     // through LDS, 32 rows at a time, so that a store is whole 16-byte pieces of rows; every
     // wave is past its last read of the tiles here
-    constexpr int PITCH = WN + 8, EACH = BM * kStep / (32 * PITCH);   // waves an array holds
-    static_assert(EACH * 4 >= WAVES, "the waves' parts fit");
-    uint16_t* const arr = w / EACH == 0 ? A0 : w / EACH == 1 ? A1 : w / EACH == 2 ? A2 : A3;
-    uint16_t* out = arr + (w % EACH) * 32 * PITCH;
+    constexpr int PITCH = WN + 8, EACH = BM * kRound / (32 * PITCH);   // waves an array holds
+    static_assert(EACH * 3 >= WAVES, "the waves' parts fit");
+    uint16_t* out = (w / EACH == 0 ? R0 : w / EACH == 1 ? R1 : R2) + (w % EACH) * 32 * PITCH;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int64_t rw = row0 + WM * wm + 32 * i;             // the first of 32 rows
@@ -747,6 +838,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
       }
       __builtin_amdgcn_wave_barrier();
     }
+  }
+  __syncthreads();                             // the next tile's loads overwrite the ring
   }
 }
 
@@ -849,8 +942,11 @@ static hipError_t launch_wide(experts::Product g, hipStream_t s) {
   const int64_t blocks = KIND == experts::kWeight
                              ? (g.n / g.slice + g.E) * (int64_t)g.row_tiles * g.col_tiles
                              : most_tiles(g.n, g.E, BM) * g.col_tiles;
+  // as many blocks as run at once, or the tiles there can be
+  const int64_t most = 256 * (BM == 256 ? 1 : 2);
+  const int64_t grid = (blocks < most ? blocks : most) + kXcds - 1;
   experts::wide_kernel<TY, KIND, BM, BN, WM, WN>
-      <<<(unsigned)blocks, (BM / WM) * (BN / WN) * 64, 0, s>>>(g);
+      <<<(unsigned)(grid / kXcds * kXcds), (BM / WM) * (BN / WN) * 64, 0, s>>>(g);
   return hipGetLastError();
 }
 
