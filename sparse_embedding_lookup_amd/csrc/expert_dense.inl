@@ -11,10 +11,12 @@
 // rows in E pieces can need, and a block finds its expert by a scan over the offsets.
 // Positions from offsets[E] on belong to no expert; their rows of Y and dX are zero.
 // Products are exact in the matrix cores (binary32 operands: rounded once), sums are fp32.
+#include <cstdlib>
 namespace ctr {
 namespace experts {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 
@@ -22,7 +24,7 @@ struct Product {
   const void* X;
   int64_t xs, x_rows;
   const int32_t* order;         // nullable: positions are X's rows
-  uint64_t kmul;                // i / k = i * kmul >> kshift for 0 <= i < 2^31
+  uint32_t kmul;                // i / k = 2 i * kmul >> 32 + kshift for 0 <= i < 2^31
   int kshift;
   const int32_t* offsets;
   int64_t n;
@@ -81,9 +83,9 @@ __device__ __forceinline__ bool find_tile(const Product& g, int64_t mt, int* exp
 }
 
 // Row of X of slot i (its token, i / k), or -1 (a slot outside X: its row reads as zeros).
-__device__ __forceinline__ int64_t token_of(const Product& g, int32_t i) {
-  const int64_t r = (int64_t)(((uint64_t)(uint32_t)i * g.kmul) >> g.kshift);
-  return i >= 0 && r < g.x_rows ? r : -1;
+__device__ __forceinline__ int32_t token_of(const Product& g, int32_t i) {
+  const int32_t r = (int32_t)(__umulhi(2u * (uint32_t)i, g.kmul) >> g.kshift);
+  return i >= 0 && r < (int32_t)g.x_rows ? r : -1;
 }
 // Row of X that position p reads, or -1.
 __device__ __forceinline__ int64_t x_row(const Product& g, int64_t p) {
@@ -464,7 +466,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRound = 64, kHalf = 32;         // reduction values
-constexpr uint32_t kNowhere = 0xFFFFFFF0u;     // an offset past every buffer: reads zeros
+// An offset past every buffer: reads zeros, writes nothing.  Offsets are below 2^31, and so is
+// what is added to them for all lanes, so that the sum never wraps; gathered rows, to which
+// nothing is added, reach further.
+constexpr uint32_t kNowhere = 0x80000000u, kFar = 0xFFFFFFF0u;
 
 template <int TY>
 __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
@@ -476,12 +481,33 @@ __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// 16 bytes a lane from base + off to lds + 16 * lane (base and lds the same in the whole wave).
-__device__ __forceinline__ void to_lds(const void* base, uint32_t off, uint16_t* lds) {
+// 16 bytes a lane from base + off + more to lds + 16 * lane (base, more and lds the same in the
+// whole wave).
+template <uint32_t END = kNowhere>
+__device__ __forceinline__ void to_lds(const void* base, uint32_t off, uint32_t more,
+                                       uint16_t* lds) {
   const __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)kNowhere, 0x00020000);
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)END, 0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                           (int)off, 0, 0, 0);
+                                           (int)off, (int)more, 0, 0);
+}
+
+// 16 bytes a lane from base + off (base the same in the whole wave).
+__device__ __forceinline__ uint4 load16(const void* base, uint32_t off) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<void*>(base), (short)0, (int)kFar, 0x00020000);
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// 16 bytes a lane to base + off (base the same in the whole wave).  No part of the address is
+// in the instruction's scalar offset: with one the compiler lets the next instruction write the
+// registers that are stored, and the store has been seen to take what that writes.
+__device__ __forceinline__ void store16(void* base, uint32_t off, uint4 x) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)kNowhere, 0x00020000);
+  const u32x4 v = {x.x, x.y, x.z, x.w};
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 0);
 }
 
 // Ends a part: the wave's LDS reads are done and at most LOADS of its loads are in flight, in
@@ -501,171 +527,178 @@ __device__ __forceinline__ void arrive_only() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int TY, int KIND, int BM, int BN, int WM, int WN>
+// ORDER: the weight gradient reads X's rows through g.order.
+template <int TY, int KIND, int BM, int BN, int WM, int WN, bool ORDER>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Product g) {
   constexpr int WAVES = (BM / WM) * (BN / WN), WN_WAVES = BN / WN;
   constexpr bool AROW = KIND != kWeight, BROW = KIND == kForward, PAIRED = WAVES == 8;
   constexpr int TI = WM / 32, TJ = WN / 32;
   constexpr int AL = BM * kRound / 512 / WAVES, BL = BN * kRound / 512 / WAVES;
-  static_assert(BM == BN, "a ring slot holds either operand");
-  __shared__ __attribute__((aligned(16))) uint16_t R0[BM * kRound], R1[BM * kRound],
-      R2[BM * kRound], R3[BM * kRound], R4[BM * kRound];
+  constexpr int STORES = TI * (KIND == kWeight ? WN / 8 : WN / 16);
+  constexpr int SLOT = (BM > BN ? BM : BN) * kRound;           // a ring slot holds either operand
+  __shared__ __attribute__((aligned(16))) uint16_t R0[SLOT], R1[SLOT], R2[SLOT], R3[SLOT], R4[SLOT];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / WN_WAVES, wn = w % WN_WAVES;
   const int rl = lane & 31, kg = lane >> 5;
   const int cols = KIND == kForward ? g.N : g.K;
 
-  int64_t at, last;
-  const int64_t stride = gridDim.x / kXcds;
-  part_of<KIND, BM>(g, &at, &last);
-  for (; at < last; at += stride) {
-  // which tile
-  int e, n0;
-  int64_t row0, end, r0 = 0, r1;
-  float* dW = g.dW;
-  if constexpr (KIND == kWeight) {
-    const int tiles = g.row_tiles * g.col_tiles, tile = (int)(at % tiles);
-    Slice u;
-    if (!find_slice(g, at / tiles, -1, &u)) break;
-    e = u.expert;
-    r0 = u.lo;
-    r1 = u.hi;
-    dW = u.partial >= 0 ? g.part + uniform(u.partial) * g.N * g.K
-                        : dW + uniform(e) * g.N * g.K;
-    row0 = (int64_t)(tile / g.col_tiles) * BM;
-    n0 = tile % g.col_tiles * BN;
-    end = g.N;
-  } else {
-    n0 = (int)(at % g.col_tiles) * BN;
-    if (!find_tile<BM>(g, at / g.col_tiles, &e, &row0, &end)) break;
-    r1 = e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
-  }
-  e = __builtin_amdgcn_readfirstlane(e);
-  n0 = __builtin_amdgcn_readfirstlane(n0);
-  row0 = uniform(row0);
-  end = uniform(end);
-  r0 = uniform(r0);
-  r1 = uniform(r1);
-  const uint16_t* W = static_cast<const uint16_t*>(g.W) + (int64_t)(e < g.E ? e : 0) * g.N * g.K;
+  // A tile: the first of its rows and columns, the end of the rows, the reduction's range.
+  struct Tile {
+    int e, n0;
+    int64_t row0, end, r0, r1;
+    float* dW;
+  };
+  auto find = [&](int64_t at) {
+    Tile n;
+    n.r0 = 0;
+    n.dW = g.dW;
+    if constexpr (KIND == kWeight) {
+      const uint32_t tiles = g.row_tiles * g.col_tiles, tile = (uint32_t)at % tiles;
+      Slice u;
+      u.expert = 0; u.lo = u.hi = 0; u.partial = -1;
+      find_slice(g, (uint32_t)at / tiles, -1, &u);
+      n.e = u.expert;
+      n.r0 = u.lo;
+      n.r1 = u.hi;
+      const int64_t part = uniform(u.partial);
+      n.dW = part >= 0 ? g.part + part * g.N * g.K : g.dW + uniform(n.e) * g.N * g.K;
+      n.row0 = (int64_t)(tile / (uint32_t)g.col_tiles) * BM;
+      n.n0 = (int)(tile % (uint32_t)g.col_tiles) * BN;
+      n.end = g.N;
+    } else {
+      n.n0 = (int)((uint32_t)at % (uint32_t)g.col_tiles) * BN;
+      n.e = g.E; n.row0 = n.end = g.n;
+      find_tile<BM>(g, (uint32_t)at / (uint32_t)g.col_tiles, &n.e, &n.row0, &n.end);
+      n.r1 = n.e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
+    }
+    n.e = __builtin_amdgcn_readfirstlane(n.e);
+    n.n0 = __builtin_amdgcn_readfirstlane(n.n0);
+    n.row0 = uniform(n.row0);
+    n.end = uniform(n.end);
+    n.r0 = uniform(n.r0);
+    n.r1 = uniform(n.r1);
+    return n;
+  };
 
-  // Where a lane's loads are, in bytes from the operand's base at the round's first reduction
-  // value.  By rows: lane i of piece q has row 8 q + i / 8 and its 16 bytes
-  // (i % 8) ^ (row / 2 & 7).  By reduction: 512 / WIDE reduction rows a piece.
+  // A load takes 8 rows (by rows) or 512 / WIDE reduction rows (by reduction); load q of wave w
+  // is number q * WAVES + w.  Where a lane's 16 bytes are: at `base` of the round, plus the
+  // lane's offset, plus a number of rows that is the same in the wave.  By rows lane i has row
+  // i / 8 and its piece (i % 8) ^ (row / 2 & 7).
   const uint16_t* abase;
   const uint16_t* bbase;
   int64_t astep, bstep;                                        // elements from round to round
-  uint32_t aoff[AL], boff[BL];
-  constexpr int APER = 512 / BM, BPER = 512 / BN;              // by reduction: rows a piece
+  uint32_t aoff, boff, rowoff[AL];                             // bytes
+  int arows, brows;                                            // rows that there are
+  constexpr int APER = 512 / BM, BPER = 512 / BN;
   constexpr int ALANES = 64 / APER, BLANES = 64 / BPER;
-  auto piece = [&](int q) {                                    // first reduction value
-    return ((lane & 7) ^ ((4 * (q * WAVES + w) + (lane >> 4)) & 7)) * 8;
+  const int piece = ((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) * 8;   // first reduction value
+  const int64_t ald = KIND == kForward ? g.xs : g.dys, bld = KIND == kWeight ? g.xs : g.K;
+  auto aim = [&](const Tile& n) {
+    const uint16_t* W =
+        static_cast<const uint16_t*>(g.W) + (int64_t)(n.e < g.E ? n.e : 0) * g.N * g.K;
+    arows = (int)(n.end - n.row0 < BM ? n.end - n.row0 : BM);
+    brows = cols - n.n0 < BN ? cols - n.n0 : BN;
+    if constexpr (KIND == kForward) {
+      abase = static_cast<const uint16_t*>(g.X) + (g.order ? 0 : n.row0 * ald);
+      astep = kRound;
+#pragma unroll
+      for (int q = 0; q < AL; ++q) {
+        const int r = 8 * (q * WAVES + w) + (lane >> 3);
+        int64_t x = r < arows ? r : -1;
+        if (g.order && x >= 0) x = x_row(g, n.row0 + r);
+        rowoff[q] = x >= 0 ? (uint32_t)(x * ald + piece) * 2 : kFar;
+      }
+    } else if constexpr (KIND == kInput) {
+      abase = static_cast<const uint16_t*>(g.dY) + n.row0 * ald;
+      astep = kRound;
+      aoff = (uint32_t)((lane >> 3) * ald + piece) * 2;
+    } else {
+      abase = static_cast<const uint16_t*>(g.dY) + n.r0 * ald + n.row0;
+      astep = kRound * ald;
+      const int kr = w * APER + lane / ALANES, c = ((lane % ALANES) ^ (4 * (kr & 3))) * 8;
+      aoff = c < arows ? (uint32_t)((lane / ALANES) * ald + c) * 2 : kNowhere;
+    }
+    if constexpr (BROW) {
+      bbase = W + (int64_t)n.n0 * bld;
+      bstep = kRound;
+      boff = (uint32_t)((lane >> 3) * bld + piece) * 2;
+    } else {
+      bbase = (KIND == kInput ? W : static_cast<const uint16_t*>(g.X)) + n.n0;
+      bstep = ORDER ? 0 : kRound * bld;
+      if (!ORDER) bbase += n.r0 * bld;
+      const int kr = w * BPER + lane / BLANES, c = ((lane % BLANES) ^ (4 * (kr & 3))) * 8;
+      boff = c < brows ? (uint32_t)((ORDER ? 0 : (lane / BLANES) * bld) + c) * 2 : kNowhere;
+    }
   };
-  if constexpr (AROW) {
-    abase = static_cast<const uint16_t*>(KIND == kForward ? g.X : g.dY);
-    const int64_t ld = KIND == kForward ? g.xs : g.dys;
-    const bool gather = KIND == kForward && g.order;
-    if (!gather) abase += row0 * ld;
-    astep = kRound;
-#pragma unroll
-    for (int q = 0; q < AL; ++q) {
-      const int64_t r = row0 + 8 * (q * WAVES + w) + (lane >> 3);
-      int64_t x = r < end ? r - row0 : -1;
-      if (gather && x >= 0) x = x_row(g, r);
-      aoff[q] = x >= 0 ? (uint32_t)(x * ld + piece(q)) * 2 : kNowhere;
-    }
-  } else {
-    abase = static_cast<const uint16_t*>(g.dY) + r0 * g.dys + row0;
-    astep = kRound * g.dys;
-#pragma unroll
-    for (int q = 0; q < AL; ++q) {
-      const int kr = (q * WAVES + w) * APER + lane / ALANES;
-      const int c = ((lane % ALANES) ^ (4 * (kr & 3))) * 8;
-      aoff[q] = row0 + c < end ? (uint32_t)(kr * g.dys + c) * 2 : kNowhere;
-    }
-  }
-  const bool order = KIND == kWeight && g.order;
-  if constexpr (BROW) {
-    bbase = W + (int64_t)n0 * g.K;
-    bstep = kRound;
-#pragma unroll
-    for (int q = 0; q < BL; ++q) {
-      const int r = 8 * (q * WAVES + w) + (lane >> 3);
-      boff[q] = n0 + r < cols ? (uint32_t)((int64_t)r * g.K + piece(q)) * 2 : kNowhere;
-    }
-  } else {
-    const int64_t ld = KIND == kInput ? g.K : g.xs;
-    bbase = (KIND == kInput ? W : static_cast<const uint16_t*>(g.X)) + n0;
-    bstep = kRound * ld;
-    if (order) bstep = 0;
-    else bbase += r0 * ld;
-#pragma unroll
-    for (int q = 0; q < BL; ++q) {
-      const int kr = (q * WAVES + w) * BPER + lane / BLANES;
-      const int c = ((lane % BLANES) ^ (4 * (kr & 3))) * 8;
-      boff[q] = n0 + c < cols ? (uint32_t)((order ? 0 : kr * ld) + c) * 2 : kNowhere;
-    }
-  }
-  // with `order`: the slots of the round after the last loaded one, ahead of their use
+  // with ORDER: the slots of the round after the last loaded one, ahead of their use
   // (scalar loads, which do not stand in line with the operands' loads)
   int32_t slot[BL];
   auto fetch_slots = [&](int64_t k) {
-    if constexpr (KIND == kWeight) {
+    if constexpr (ORDER) {
       const auto* o = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)g.order;
+      const int n1 = (int)g.n - 1;
 #pragma unroll
       for (int q = 0; q < BL; ++q) {
-        int32_t i = 0;
+        const int p = (int)k + (q * WAVES + w) * BPER;         // past the end: any slot, unused
+        int32_t v[BPER], i = 0;
 #pragma unroll
-        for (int j = 0; j < BPER; ++j) {
-          const int64_t p = k + (q * WAVES + w) * BPER + j;
-          const int32_t v = o[p < r1 ? p : r1 - 1];
-          i = lane / BLANES == j ? v : i;
-        }
+        for (int j = 0; j < BPER; ++j) v[j] = o[p + j < n1 ? p + j : n1];
+#pragma unroll
+        for (int j = 0; j < BPER; ++j) i = lane / BLANES == j ? v[j] : i;
         slot[q] = i;
       }
     }
   };
 
   // Load the next round of an operand, reduction values [k, k + 64).
-  auto load_a = [&](uint16_t* A, int64_t k) {
-    const bool whole = k + kRound <= r1;
+  auto load_a = [&](uint16_t* A, int64_t k, int64_t r1) {
+    const int left = (int)(r1 - k < kRound ? r1 - k : kRound);
 #pragma unroll
     for (int q = 0; q < AL; ++q) {
-      uint32_t off = aoff[q];
-      if (!whole) {
-        const int i = AROW ? piece(q) : (q * WAVES + w) * APER + lane / ALANES;
-        off = k + i < r1 ? off : kNowhere;
+      const int i = q * WAVES + w;
+      if constexpr (KIND == kForward) {
+        to_lds<kFar>(abase, piece < left ? rowoff[q] : kFar, 0, A + i * 512);
+      } else if constexpr (KIND == kInput) {
+        const bool in = piece < left && (lane >> 3) < arows - 8 * i;
+        to_lds(abase, in ? aoff : kNowhere, (uint32_t)(8 * i * ald) * 2, A + i * 512);
+      } else {
+        const bool in = lane / ALANES < left - i * APER;
+        to_lds(abase, in ? aoff : kNowhere, (uint32_t)(i * APER * ald) * 2, A + i * 512);
       }
-      to_lds(abase, off, A + (q * WAVES + w) * 512);
     }
     abase += astep;
   };
-  auto load_b = [&](uint16_t* B, int64_t k) {
-    const bool whole = k + kRound <= r1;
+  auto load_b = [&](uint16_t* B, int64_t k, int64_t r1) {
+    const int left = (int)(r1 - k < kRound ? r1 - k : kRound);
 #pragma unroll
     for (int q = 0; q < BL; ++q) {
-      uint32_t off = boff[q];
-      if (KIND == kWeight && order) {
-        const int64_t x = token_of(g, slot[q]);
-        off = x >= 0 && off != kNowhere ? off + (uint32_t)(x * g.xs) * 2 : kNowhere;
+      const int i = q * WAVES + w;
+      if constexpr (BROW) {
+        const bool in = piece < left && (lane >> 3) < brows - 8 * i;
+        to_lds(bbase, in ? boff : kNowhere, (uint32_t)(8 * i * bld) * 2, B + i * 512);
+      } else {
+        bool in = lane / BLANES < left - i * BPER;
+        if constexpr (ORDER) {
+          const int32_t x = token_of(g, slot[q]);
+          in = in && x >= 0 && boff != kNowhere;
+          to_lds<kFar>(bbase, in ? boff + (uint32_t)x * (uint32_t)bld * 2 : kFar, 0, B + i * 512);
+        } else {
+          to_lds(bbase, in ? boff : kNowhere, (uint32_t)(i * BPER * bld) * 2, B + i * 512);
+        }
       }
-      if (!whole) {
-        const int i = BROW ? piece(q) : (q * WAVES + w) * BPER + lane / BLANES;
-        off = k + i < r1 ? off : kNowhere;
-      }
-      to_lds(bbase, off, B + (q * WAVES + w) * 512);
     }
     bbase += bstep;
-    if (KIND == kWeight && order) fetch_slots(k + kRound);
+    fetch_slots(k + kRound);
   };
-
-  f32x16 acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  // The first loads of a tile: A0, B0 and A1.
+  auto start = [&](const Tile& n) {
+    if (n.r1 <= n.r0) return;
+    fetch_slots(n.r0);
+    load_a(R0, n.r0, n.r1);
+    load_b(R1, n.r0, n.r1);
+    load_a(R2, n.r0 + kRound, n.r1);
+  };
 
   // Where a lane's fragments are in a slot, in bytes: those of the operand's 32-row tile i and
   // the reduction values 16 s + 8 kg .. + 8 are at `at` with a few bits flipped, plus a constant.
@@ -692,7 +725,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     }
   };
 
-  const int halves = (int)((r1 - r0 + kHalf - 1) / kHalf), rounds = (halves + 1) >> 1;
+  f32x16 acc[TI][TJ];
   // Half step h of a round: `ahead` issues its loads and arrives.
   auto half = [&](const uint16_t* A, const uint16_t* B, auto h, auto ahead) {
     s16x8 a[2][TI], b[2][TJ];
@@ -722,35 +755,41 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     __builtin_amdgcn_s_setprio(0);
     if constexpr (PAIRED) arrive_only();
   };
-  // Round j on A and B; Bn takes B of round j + 1 (its slot held A of round j - 1), An takes A
-  // of round j + 2 (its slot held B of round j - 1).
-  auto round = [&](const uint16_t* A, const uint16_t* B, uint16_t* Bn, uint16_t* An, int j) {
-    half(A, B, std::integral_constant<int, 0>{}, [&] {
-      if (j + 1 < rounds) load_b(Bn, r0 + (int64_t)(j + 1) * kRound);
-      arrive<-1>();
-    });
-    if (2 * j + 1 < halves)
-      half(A, B, std::integral_constant<int, 1>{}, [&] {
-        // round j + 1 has landed when at most A of round j + 2 is in flight
-        if (j + 2 < rounds) {
-          load_a(An, r0 + (int64_t)(j + 2) * kRound);
-          arrive<AL>();
-        } else {
-          arrive<0>();
-        }
-      });
-  };
 
-  if (halves > 0) {
-    if (KIND == kWeight && order) fetch_slots(r0);
-    load_a(R0, r0);
-    load_b(R1, r0);
-    if (rounds > 1) {
-      load_a(R2, r0 + kRound);
-      arrive<AL>();
-    } else {
-      arrive<0>();
-    }
+  // The tile whose first loads are on their way: its sums into acc.  `stores`: of the tile
+  // before, issued after the loads.
+  auto multiply = [&](const Tile& n, bool stores) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    const int64_t r0 = n.r0, r1 = n.r1;
+    const int halves = (int)((r1 - r0 + kHalf - 1) / kHalf), rounds = (halves + 1) >> 1;
+    if (halves <= 0) return;
+    // (Loads past the last round read nowhere: the counts of loads in flight stay the same, and
+  // all have ended when the last half step does.)
+  // Round j on A and B; Bn takes B of round j + 1 (its slot held A of round j - 1), An takes A
+    // of round j + 2 (its slot held B of round j - 1).
+    auto round = [&](const uint16_t* A, const uint16_t* B, uint16_t* Bn, uint16_t* An, int j) {
+      half(A, B, std::integral_constant<int, 0>{}, [&] {
+        load_b(Bn, r0 + (int64_t)(j + 1) * kRound, r1);
+        if (2 * j + 1 < halves) arrive<-1>();
+        else arrive<0>();
+      });
+      if (2 * j + 1 < halves)
+        half(A, B, std::integral_constant<int, 1>{}, [&] {
+          // round j + 1 has landed when at most A of round j + 2 is in flight
+          load_a(An, r0 + (int64_t)(j + 2) * kRound, r1);
+          if (j + 1 < rounds) arrive<AL>();
+          else arrive<0>();
+        });
+    };
+
+    // A0 and B0 have landed when at most A1 and the stores after it are in flight
+    if (stores) arrive<AL + STORES>();
+    else arrive<AL>();
     if (PAIRED && w >= WAVES / 2) arrive_only();
     for (int j = 0; j < rounds; j += 5) {
       round(R0, R1, R3, R4, j);
@@ -760,34 +799,35 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
       if (j + 4 < rounds) round(R3, R4, R1, R2, j + 4);
     }
     if (PAIRED && w < WAVES / 2) arrive_only();
-  }
+  };
 
-  // acc[i][j][v]: row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part
-  if constexpr (KIND == kWeight) {
+  // acc[i][j][v] is row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part.
+  // 32 rows at a time go through 8 KB of LDS a wave (of the two slots that `start` leaves
+  // free), so that a store is whole 16-byte pieces along rows.  Every store is issued, those
+  // outside the tile to nowhere: `multiply` counts them.
+  constexpr int EACH = SLOT * 2 / 8192;                        // waves a slot holds
+  static_assert(2 * EACH >= WAVES, "the waves' parts fit");
+  char* const out = reinterpret_cast<char*>(w < EACH ? R3 : R4) + (w % EACH) * 8192;
+  auto finish = [&](const Tile& n, const f32x4 (&bias)[TJ][4]) {
+    constexpr int SIZE = KIND == kWeight ? 4 : 2, PIECE = 16 / SIZE, LR = WN / PIECE;
+    const int64_t ld = KIND == kWeight ? g.K : g.ys;
+    const int64_t rw = n.row0 + WM * wm;                       // the wave's first row
+    const int cw = n.n0 + WN * wn;                             // and column
+    char* base = KIND == kWeight ? reinterpret_cast<char*>(n.dW) : static_cast<char*>(g.Y);
+    base += (rw * ld + cw) * SIZE;
+    // this lane's row and column in the 64 / LR rows of a store (from a lane number that the
+    // compiler does not know: what it made of it would stay in registers over the products)
+    int me = lane;
+    asm volatile("" : "+v"(me));
+    const int l = me % LR, rr = me / LR, rl = me & 31, kg = me >> 5;
+    const bool in = cw + l * PIECE < cols;
+    const int rows = (int)(n.end - rw < WM ? n.end - rw : WM);
+    const uint32_t off = (uint32_t)(rr * ld + l * PIECE) * SIZE;
+    // with x_relu: the input's values at the same places
+    const bool masked = KIND == kInput && g.relu && n.e < g.E;
+    const uint16_t* xbase = static_cast<const uint16_t*>(g.X) + cw + (g.order ? 0 : rw * g.xs);
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-      const int64_t r = row0 + WM * wm + 32 * i + rl;
-      if (r >= end) continue;
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = n0 + WN * wn + 32 * j + 8 * q + 4 * kg;
-          if (c < cols)
-            *reinterpret_cast<float4*>(dW + r * g.K + c) =
-                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                            acc[i][j][4 * q + 3]);
-        }
-    }
-  } else {
-    // through LDS, 32 rows at a time, so that a store is whole 16-byte pieces of rows; every
-    // wave is past its last read of the tiles here
-    constexpr int PITCH = WN + 8, EACH = BM * kRound / (32 * PITCH);   // waves an array holds
-    static_assert(EACH * 3 >= WAVES, "the waves' parts fit");
-    uint16_t* out = (w / EACH == 0 ? R0 : w / EACH == 1 ? R1 : R2) + (w % EACH) * 32 * PITCH;
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int64_t rw = row0 + WM * wm + 32 * i;             // the first of 32 rows
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
 #pragma unroll
@@ -795,51 +835,85 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
           const int c = 32 * j + 8 * q + 4 * kg;
           float x[4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) x[v] = acc[i][j][4 * q + v];
-          if constexpr (KIND == kForward) {
-            const int n = n0 + WN * wn + c;
-            if (g.b && e < g.E && n < cols) {
-              const float* b = g.b + (int64_t)e * g.N + n;
-#pragma unroll
-              for (int v = 0; v < 4; ++v) x[v] += b[v];
+          for (int v = 0; v < 4; ++v) {
+            x[v] = acc[i][j][4 * q + v];
+            if constexpr (KIND == kForward) {
+              x[v] += bias[j][q][v];
+              if (g.relu) x[v] = x[v] > 0.f ? x[v] : 0.f;
             }
-            if (g.relu)
-#pragma unroll
-              for (int v = 0; v < 4; ++v) x[v] = x[v] > 0.f ? x[v] : 0.f;
           }
-          uint2 h;
-          h.x = to_half<TY, false>(x[0], 0u) | (to_half<TY, false>(x[1], 0u) << 16);
-          h.y = to_half<TY, false>(x[2], 0u) | (to_half<TY, false>(x[3], 0u) << 16);
-          *reinterpret_cast<uint2*>(out + rl * PITCH + c) = h;
+          if constexpr (KIND == kWeight) {
+            *reinterpret_cast<float4*>(out + rl * WN * 4 + ((c >> 2) ^ (rl & 15)) * 16) =
+                make_float4(x[0], x[1], x[2], x[3]);
+          } else {
+            uint2 h;
+            h.x = to_half<TY, false>(x[0], 0u) | (to_half<TY, false>(x[1], 0u) << 16);
+            h.y = to_half<TY, false>(x[2], 0u) | (to_half<TY, false>(x[3], 0u) << 16);
+            *reinterpret_cast<uint2*>(out + rl * (WN + 8) * 2 + c * 2) = h;
+          }
         }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      constexpr int LR = WN / 8;                              // lanes a row
 #pragma unroll
       for (int t = 0; t < 32 * LR / 64; ++t) {
-        const int rr = t * (64 / LR) + lane / LR, c = (lane % LR) * 8;
-        const int64_t r = rw + rr;
-        const int n = n0 + WN * wn + c;
-        uint4 h = *reinterpret_cast<const uint4*>(out + rr * PITCH + c);
-        if (r >= end || n >= cols) continue;
+        const int r = t * (64 / LR) + rr;                      // of the 32 staged rows
+        const bool here = in && 32 * i + r < rows;
+        uint4 h;
+        if constexpr (KIND == kWeight)
+          h = *reinterpret_cast<const uint4*>(out + r * WN * 4 + (l ^ (r & 15)) * 16);
+        else
+          h = *reinterpret_cast<const uint4*>(out + r * (WN + 8) * 2 + l * 16);
         if constexpr (KIND == kInput) {
-          if (g.relu && e < g.E) {
-            const int64_t xr = x_row(g, r);
-            uint4 m = make_uint4(0, 0, 0, 0);
-            if (xr >= 0)
-              m = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.X) + xr * g.xs + n);
+          if (masked) {
+            int32_t x = 32 * i + r;
+            if (g.order) x = here ? token_of(g, g.order[rw + x]) : -1;
+            const uint32_t from = ((uint32_t)x * (uint32_t)g.xs + l * PIECE) * 2;
+            const uint4 m = load16(xbase, here && x >= 0 ? from : kFar);
             h.x = keep_positive<TY>(h.x, m.x);
             h.y = keep_positive<TY>(h.y, m.y);
             h.z = keep_positive<TY>(h.z, m.z);
             h.w = keep_positive<TY>(h.w, m.w);
           }
         }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.Y) + r * g.ys + n) = h;
+        const uint32_t more = (uint32_t)((32 * i + t * (64 / LR)) * ld) * SIZE;
+        store16(base, here ? off + more : kNowhere, h);
       }
       __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_sched_barrier(0);
     }
-  }
-  __syncthreads();                             // the next tile's loads overwrite the ring
+  };
+
+  // The next tile's first loads are issued before this tile's results are stored.
+  int64_t at, last;
+  const int64_t stride = gridDim.x / kXcds;
+  part_of<KIND, BM>(g, &at, &last);
+  if (at >= last) return;
+  Tile n = find(at);
+  aim(n);
+  start(n);
+  for (bool stores = false;; stores = true) {
+    multiply(n, stores);
+    f32x4 bias[TJ][4];
+    if constexpr (KIND == kForward) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = n.n0 + WN * wn + 32 * j + 8 * q + 4 * kg;
+          const bool in = g.b && n.e < g.E && c < cols;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) bias[j][q][v] = in ? g.b[(int64_t)n.e * g.N + c + v] : 0.f;
+        }
+    }
+    const Tile done = n;
+    at += stride;
+    if (at < last) {
+      n = find(at);
+      aim(n);
+      start(n);
+    }
+    finish(done, bias);
+    if (at >= last) break;
   }
 }
 
@@ -911,10 +985,8 @@ static experts::Product expert_product(const void* X, int64_t xs, int64_t x_rows
   g.X = X; g.xs = xs; g.x_rows = x_rows; g.order = order;
   // with 2^b >= k: kmul = floor(2^(31 + b) / k) + 1 exceeds the quotient by at most 1, which
   // moves i * kmul / 2^(31 + b) by less than 2^-b <= 1 / k: never past the next integer
-  int bits = 0;
-  while (((int64_t)1 << bits) < k) ++bits;
-  g.kshift = 31 + bits;
-  g.kmul = (((uint64_t)1 << g.kshift) / (uint64_t)(k > 0 ? k : 1)) + 1;
+  while (((int64_t)1 << g.kshift) < k) ++g.kshift;
+  g.kmul = (uint32_t)((((uint64_t)1 << (31 + g.kshift)) / (uint64_t)(k > 0 ? k : 1)) + 1);
   g.offsets = offsets; g.n = n; g.E = E; g.K = K; g.N = N; g.W = W;
   return g;
 }
@@ -927,7 +999,7 @@ static int64_t most_tiles(int64_t n, int E, int BM) { return n / BM + E + 1; }
 static bool wide_ok(const experts::Product& g, int dtype) {
   auto ok = [](const void* p, int64_t stride) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % 8 == 0 &&
-           stride < ((int64_t)1 << 22);          // 256 rows: 2^31 bytes
+           stride < ((int64_t)1 << 21);          // 256 rows: 2^30 bytes
   };
   if (dtype == kEltF32 || g.K % 8 || g.N % 8) return false;
   if (!ok(g.X, g.xs) || !ok(g.W, g.K) || !ok(g.Y, g.ys) || !ok(g.dY, g.dys)) return false;
@@ -943,10 +1015,15 @@ static hipError_t launch_wide(experts::Product g, hipStream_t s) {
                              ? (g.n / g.slice + g.E) * (int64_t)g.row_tiles * g.col_tiles
                              : most_tiles(g.n, g.E, BM) * g.col_tiles;
   // as many blocks as run at once, or the tiles there can be
-  const int64_t most = 256 * (BM == 256 ? 1 : 2);
+  int64_t most = 256 * (BM == 256 ? 1 : 2);
+  if (getenv("CTR_NOSTAY") && KIND != experts::kWeight) most = 1 << 30;
   const int64_t grid = (blocks < most ? blocks : most) + kXcds - 1;
-  experts::wide_kernel<TY, KIND, BM, BN, WM, WN>
-      <<<(unsigned)(grid / kXcds * kXcds), (BM / WM) * (BN / WN) * 64, 0, s>>>(g);
+  const unsigned whole = (unsigned)(grid / kXcds * kXcds), threads = (BM / WM) * (BN / WN) * 64;
+  if (KIND == experts::kWeight && g.order)
+    experts::wide_kernel<TY, KIND, BM, BN, WM, WN, KIND == experts::kWeight>
+        <<<whole, threads, 0, s>>>(g);
+  else
+    experts::wide_kernel<TY, KIND, BM, BN, WM, WN, false><<<whole, threads, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -959,9 +1036,9 @@ template <int TY, int KIND>
 static hipError_t launch_product(experts::Product g, bool wide, hipStream_t s) {
   if constexpr (TY != kEltF32) {
     if (wide) {
-      const int cols = KIND == experts::kForward ? g.N : g.K;
-      if (KIND == experts::kWeight ? g.slice_big : big_tiles(g.n / 256 + g.E / 2, cols))
-        return launch_wide<TY, KIND, 256, 256, 128, 64>(g, s);
+      const int v = getenv("CTR_TILE") ? atoi(getenv("CTR_TILE")) : 0;
+      if (v == 0) return launch_wide<TY, KIND, 256, 256, 128, 64>(g, s);
+      if (v == 1) return launch_wide<TY, KIND, 256, 128, 64, 64>(g, s);
       return launch_wide<TY, KIND, 128, 128, 64, 64>(g, s);
     }
   }
@@ -984,6 +1061,7 @@ static void set_slices(experts::Product& g) {
   const int64_t tiles = g.slice_big ? big : small;
   int64_t slice = (g.n * tiles + 1023) / 1024;
   slice = slice < 512 ? 512 : slice;
+  if (getenv("CTR_SLICE")) slice = atoi(getenv("CTR_SLICE"));
   g.slice = (slice + 63) / 64 * 64;
 }
 
