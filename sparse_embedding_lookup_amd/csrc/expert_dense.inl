@@ -11,7 +11,6 @@
 // rows in E pieces can need, and a block finds its expert by a scan over the offsets.
 // Positions from offsets[E] on belong to no expert; their rows of Y and dX are zero.
 // Products are exact in the matrix cores (binary32 operands: rounded once), sums are fp32.
-#include <cstdlib>
 namespace ctr {
 namespace experts {
 
@@ -39,7 +38,7 @@ struct Product {
   float* dW;
   float* part;                  // partial sums of dW
   int64_t slice;                // positions a slice of dW's reduction
-  bool slice_big;               //   in 256 x 256 tiles
+  bool big;                     // dW in 256 x 256 tiles
   int col_tiles, row_tiles;
 };
 
@@ -93,163 +92,7 @@ __device__ __forceinline__ int64_t x_row(const Product& g, int64_t p) {
   return token_of(g, g.order[p]);
 }
 
-template <int TY>
-using Lds = typename std::conditional<TY == kEltF32, float, uint16_t>::type;
-
-// Eight elements of one operand row, as stored, from base[off ..]; those at or past `left`
-// are zero.
-template <int TY>
-struct Eight {
-  Lds<TY> v[8];
-  __device__ __forceinline__ void load(const void* base, int64_t off, int64_t left, bool vec) {
-    const Lds<TY>* p = static_cast<const Lds<TY>*>(base) + off;
-    if (vec && left >= 8) {
-      if constexpr (TY == kEltF32) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(p);
-        v[0] = (uint16_t)a.x; v[1] = (uint16_t)(a.x >> 16);
-        v[2] = (uint16_t)a.y; v[3] = (uint16_t)(a.y >> 16);
-        v[4] = (uint16_t)a.z; v[5] = (uint16_t)(a.z >> 16);
-        v[6] = (uint16_t)a.w; v[7] = (uint16_t)(a.w >> 16);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : Lds<TY>(0);
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = Lds<TY>(0);
-  }
-};
-
 enum Kind { kForward = 0, kInput = 1, kWeight = 2 };
-
-// The product for any type, width, stride and alignment: a block has a 64 x 64 tile, each of
-// its four waves a 32 x 32 matrix-core tile; the reduction advances 32 at a time through LDS.
-template <int TY, int KIND>
-__global__ __launch_bounds__(kThreads) void product_kernel(Product g) {
-  using LT = Lds<TY>;
-  constexpr int BM = 64, KT = 32, PITCH = TY == kEltF32 ? KT + 4 : KT + 8;
-  __shared__ __attribute__((aligned(16))) LT As[BM * PITCH], Bs[BM * PITCH];
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const int wm = w >> 1, wn = w & 1, rl = lane & 31, kg = lane >> 5;
-  const int n0 = (int)(blockIdx.x % g.col_tiles) * 64;
-  const int64_t mt = blockIdx.x / g.col_tiles;
-  const int cols = KIND == kForward ? g.N : g.K;
-  int e;
-  int64_t row0, end, r0 = 0, r1 = 0;       // output rows; reduction range
-  if constexpr (KIND == kWeight) {
-    e = (int)(mt / g.row_tiles);
-    row0 = (mt % g.row_tiles) * BM;
-    end = g.N;
-    bounds_of(g, e, &r0, &r1);
-  } else {
-    if (!find_tile<BM>(g, mt, &e, &row0, &end)) return;
-    r1 = e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
-  }
-  const int elem = TY == kEltF32 ? 4 : 2;
-  const int64_t we = (int64_t)e * g.N * g.K;           // e == E: not read
-  const char* W = static_cast<const char*>(g.W) + we * elem;
-  auto vec_ok = [&](const void* p, int64_t stride) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * elem % 16 == 0;
-  };
-  const bool xv = vec_ok(g.X, g.xs), wv = vec_ok(W, g.K), yv = vec_ok(g.dY, g.dys);
-
-  f32x16 acc;
-#pragma unroll
-  for (int v = 0; v < 16; ++v) acc[v] = 0.f;
-
-  for (int64_t k0 = r0; k0 < r1; k0 += KT) {
-    Eight<TY> a, b;
-    // operands whose rows run along the reduction: row t / 4, elements 8 (t % 4) ..
-    const int kr = t >> 2, kk = 8 * (t & 3);
-    // operands whose rows are the reduction: row t / 8, elements 8 (t % 8) ..
-    const int rr = t >> 3, rc = 8 * (t & 7);
-    if constexpr (KIND == kForward) {
-      const int64_t x = row0 + kr < end ? x_row(g, row0 + kr) : -1;
-      if (x >= 0) a.load(g.X, x * g.xs + k0 + kk, r1 - k0 - kk, xv);
-      else a.zero();
-    } else if constexpr (KIND == kInput) {
-      if (row0 + kr < end) a.load(g.dY, (row0 + kr) * g.dys + k0 + kk, r1 - k0 - kk, yv);
-      else a.zero();
-    } else {
-      if (k0 + rr < r1) a.load(g.dY, (k0 + rr) * g.dys + row0 + rc, end - row0 - rc, yv);
-      else a.zero();
-    }
-    if constexpr (KIND == kForward) {
-      if (n0 + kr < cols) b.load(W, (int64_t)(n0 + kr) * g.K + k0 + kk, r1 - k0 - kk, wv);
-      else b.zero();
-    } else if constexpr (KIND == kInput) {
-      if (k0 + rr < r1) b.load(W, (k0 + rr) * g.K + n0 + rc, cols - n0 - rc, wv);
-      else b.zero();
-    } else {
-      const int64_t x = k0 + rr < r1 ? x_row(g, k0 + rr) : -1;
-      if (x >= 0) b.load(g.X, x * g.xs + n0 + rc, cols - n0 - rc, xv);
-      else b.zero();
-    }
-    __syncthreads();                         // the last round's fragments are read
-    if constexpr (KIND == kWeight) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) As[(rc + i) * PITCH + rr] = a.v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) As[kr * PITCH + kk + i] = a.v[i];
-    }
-    if constexpr (KIND == kForward) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) Bs[kr * PITCH + kk + i] = b.v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) Bs[(rc + i) * PITCH + rr] = b.v[i];
-    }
-    __syncthreads();
-    const LT* Ar = As + (32 * wm + rl) * PITCH;
-    const LT* Br = Bs + (32 * wn + rl) * PITCH;
-    if constexpr (TY == kEltF32) {
-#pragma unroll
-      for (int s = 0; s < KT / 2; ++s)
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(Ar[2 * s + kg], Br[2 * s + kg], acc, 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int s = 0; s < KT / 16; ++s) {
-        if constexpr (TY == kEltBF16)
-          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              *reinterpret_cast<const bf16x8*>(Ar + 16 * s + 8 * kg),
-              *reinterpret_cast<const bf16x8*>(Br + 16 * s + 8 * kg), acc, 0, 0, 0);
-        else
-          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              *reinterpret_cast<const f16x8*>(Ar + 16 * s + 8 * kg),
-              *reinterpret_cast<const f16x8*>(Br + 16 * s + 8 * kg), acc, 0, 0, 0);
-      }
-    }
-  }
-
-  const int c = n0 + 32 * wn + rl;
-  if (c >= cols) return;
-  const float bias = KIND == kForward && g.b && e < g.E ? g.b[(int64_t)e * g.N + c] : 0.f;
-#pragma unroll
-  for (int v = 0; v < 16; ++v) {
-    const int64_t r = row0 + 32 * wm + 8 * (v >> 2) + 4 * kg + (v & 3);
-    if (r >= end) continue;
-    float x = acc[v];
-    if constexpr (KIND == kWeight) {
-      g.dW[we + r * g.K + c] = x;
-    } else {
-      if constexpr (KIND == kForward) {
-        x += bias;
-        if (g.relu) x = x > 0.f ? x : 0.f;
-      } else if (g.relu && e < g.E) {
-        const int64_t xr = x_row(g, r);
-        if (!(xr >= 0 && rows::load1<TY>(g.X, xr * g.xs + c) > 0.f)) x = 0.f;
-      }
-      rows::store1<TY>(g.Y, r * g.ys + c, x);
-    }
-  }
-}
 
 // A value that is the same in the whole wave, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t x) {
@@ -401,9 +244,17 @@ __device__ __forceinline__ void part_of(const Product& g, int64_t* first, int64_
   *last = uniform(*last);
 }
 
+// Four floats, aligned to one.
+__device__ __forceinline__ f32x4 load4(const float* p) {
+  f32x4 x;
+  __builtin_memcpy(&x, p, 16);
+  return x;
+}
+__device__ __forceinline__ void store4(float* p, f32x4 x) { __builtin_memcpy(p, &x, 16); }
+
 // dW of the experts with several slices: their partial sums added in order.  A block has
 // kJoin elements of one expert.
-constexpr int kJoin = 8192;
+constexpr int kJoin = 16 * kThreads;
 __global__ __launch_bounds__(kThreads) void join_kernel(Product g) {
   const int64_t count = (int64_t)g.N * g.K;
   const int64_t each = (count + kJoin - 1) / kJoin;
@@ -412,15 +263,20 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Product g) {
   if (!find_slice(g, 0, e, &u) || u.count < 2) return;
   const float* part = g.part + u.partial * count;
   float* out = g.dW + e * count;
-  const int64_t begin = (blockIdx.x % each) * kJoin;
-  const int64_t end = count < begin + kJoin ? count : begin + kJoin;
-  for (int64_t i = begin + threadIdx.x * 4; i < end; i += kThreads * 4) {   // count % 4 == 0
-    float4 s = *reinterpret_cast<const float4*>(part + i);
-    for (int z = 1; z < u.count; ++z) {
-      const float4 x = *reinterpret_cast<const float4*>(part + z * count + i);
-      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  int64_t i = (blockIdx.x % each) * kJoin + threadIdx.x * 4;
+#pragma unroll
+  for (int q = 0; q < kJoin / (4 * kThreads); ++q, i += 4 * kThreads) {
+    if (i + 4 <= count) {
+      f32x4 s = load4(part + i);
+      for (int z = 1; z < u.count; ++z) s += load4(part + z * count + i);
+      store4(out + i, s);
+    } else {
+      for (int64_t j = i; j < count; ++j) {
+        float s = part[j];
+        for (int z = 1; z < u.count; ++z) s += part[z * count + j];
+        out[j] = s;
+      }
     }
-    *reinterpret_cast<float4*>(out + i) = s;
   }
 }
 
@@ -917,6 +773,347 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
   }
 }
 
+// ---------------------------------------------------- any type, width, stride and alignment
+// What the staged kernel does not take: binary32, and 16-bit arrays in no whole 16-byte
+// pieces.  A block of four waves has a BM x BM tile, a wave a quarter of it; operands go
+// through registers, where what is past the end is cleared, into one of two LDS buffers, loaded
+// two rounds ahead.  A round is 128 bytes of a row: 64
+// reduction values of 16 bits or 32 of binary32.  LDS holds them as above.  The binary32
+// matrix instruction takes two reduction values a lane pair: lanes 0 to 31 have values
+// 8 c + e and lanes 32 to 63 values 8 c + 4 + e of both operands, so that by rows a lane's
+// next four values are one 16-byte read.
+// 64 x 64 tiles where 128 x 128 would leave compute units without a tile.
+template <int TY, int KIND, int BM>
+__global__ __launch_bounds__(kThreads) void loose_kernel(Product g) {
+  using T = typename std::conditional<TY == kEltF32, float, uint16_t>::type;
+  constexpr int SIZE = sizeof(T), PE = 16 / SIZE;              // elements a piece
+  constexpr int ROUND = 128 / SIZE, PIECES = BM * 8 / kThreads; // pieces a thread and operand
+  constexpr bool AROW = KIND != kWeight, BROW = KIND == kForward;
+  constexpr int ACROSS = BM / PE;                              // pieces of a reduction row
+  constexpr int TW = BM / 64;                                  // a wave's tiles each way
+  __shared__ __attribute__((aligned(16))) char lds[2][2][BM * 128];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, wm = w >> 1, wn = w & 1;
+  const int rl = lane & 31, kg = lane >> 5;
+  const int cols = KIND == kForward ? g.N : g.K;
+
+  // which tile: neighbours to one XCD
+  const int64_t rows_of = KIND == kWeight ? count_slices(g) * g.row_tiles : count_tiles<BM>(g);
+  const uint32_t total = (uint32_t)(rows_of * g.col_tiles), per = total / kXcds;
+  if (blockIdx.x >= total) return;
+  const uint32_t at = blockIdx.x < per * kXcds
+                          ? blockIdx.x % kXcds * per + blockIdx.x / kXcds : blockIdx.x;
+  const int n0 = (int)(at % (uint32_t)g.col_tiles) * BM;
+  const uint32_t mt = at / (uint32_t)g.col_tiles;
+  int e;
+  int64_t row0, end, r0 = 0, r1;
+  float* dW = g.dW;
+  if constexpr (KIND == kWeight) {
+    Slice u;
+    if (!find_slice(g, mt / (uint32_t)g.row_tiles, -1, &u)) return;
+    e = u.expert;
+    row0 = (int64_t)(mt % (uint32_t)g.row_tiles) * BM;
+    end = g.N;
+    r0 = u.lo;
+    r1 = u.hi;
+    dW = u.partial >= 0 ? g.part + u.partial * g.N * g.K : dW + (int64_t)e * g.N * g.K;
+  } else {
+    if (!find_tile<BM>(g, mt, &e, &row0, &end)) return;
+    r1 = e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
+  }
+  const T* X = static_cast<const T*>(g.X);
+  const T* dY = static_cast<const T*>(g.dY);
+  const T* W = static_cast<const T*>(g.W) + (int64_t)(e < g.E ? e : 0) * g.N * g.K;
+
+  // A thread's pieces: by rows row t / 8 + 32 q and piece t % 8; by reduction number
+  // kThreads q + t of ACROSS to a reduction row.
+  typedef T Piece __attribute__((ext_vector_type(PE)));
+  struct Set {
+    Piece a[PIECES], b[PIECES];
+  };
+  auto get = [&](const T* p, int64_t there) {                  // `there` elements of a piece
+    Piece x;
+    if (there >= PE) {
+      __builtin_memcpy(&x, p, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PE; ++i) x[i] = i < there ? p[i] : T(0);
+    }
+    return x;
+  };
+  int64_t xrow[PIECES];                                        // X's rows of the pieces
+  auto look = [&](int64_t k) {                                 // the weight gradient's next
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int64_t p = k + (q * kThreads + t) / ACROSS;
+      xrow[q] = p < r1 ? x_row(g, p) : -1;
+    }
+  };
+  if constexpr (KIND == kForward) {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int64_t r = row0 + q * 32 + (t >> 3);
+      xrow[q] = r < end ? x_row(g, r) : -1;
+    }
+  } else if constexpr (KIND == kWeight) {
+    look(r0);
+  }
+  auto load = [&](Set& x, int64_t k) {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int r = q * 32 + (t >> 3), kp = (t & 7) * PE;      // by rows
+      const int kr = (q * kThreads + t) / ACROSS, c = (q * kThreads + t) % ACROSS * PE;
+      if constexpr (KIND == kForward) {
+        x.a[q] = get(X + xrow[q] * g.xs + k + kp, xrow[q] >= 0 ? r1 - k - kp : 0);
+        x.b[q] = get(W + (int64_t)(n0 + r) * g.K + k + kp, n0 + r < cols ? r1 - k - kp : 0);
+      } else if constexpr (KIND == kInput) {
+        x.a[q] = get(dY + (row0 + r) * g.dys + k + kp, row0 + r < end ? r1 - k - kp : 0);
+        x.b[q] = get(W + (k + kr) * g.K + n0 + c, k + kr < r1 ? cols - n0 - c : 0);
+      } else {
+        x.a[q] = get(dY + (k + kr) * g.dys + row0 + c, k + kr < r1 ? end - row0 - c : 0);
+        x.b[q] = get(X + xrow[q] * g.xs + n0 + c, xrow[q] >= 0 ? cols - n0 - c : 0);
+      }
+    }
+    if constexpr (KIND == kWeight) look(k + ROUND);
+  };
+  // Bytes from a buffer's start of piece c of row r, and of piece c of reduction row q.
+  auto by_row = [](int r, int c) { return r * 128 + (c ^ (r >> 1 & 7)) * 16; };
+  auto by_red = [](int q, int c) {
+    if constexpr (TY == kEltF32) return q * BM * 4 + (c ^ (q & 4 ? 8 : 0)) * 16;
+    else if constexpr (BM == 64) return q * 128 + (c ^ (q & 2 ? 4 : 0)) * 16;
+    else return q * BM * 2 + (c ^ (4 * (q & 3))) * 16;
+  };
+  auto put = [&](int buf, const Set& x) {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int r = q * 32 + (t >> 3), c = t & 7;
+      const int kr = (q * kThreads + t) / ACROSS, cc = (q * kThreads + t) % ACROSS;
+      *reinterpret_cast<Piece*>(lds[buf][0] + (AROW ? by_row(r, c) : by_red(kr, cc))) = x.a[q];
+      *reinterpret_cast<Piece*>(lds[buf][1] + (BROW ? by_row(r, c) : by_red(kr, cc))) = x.b[q];
+    }
+  };
+
+  f32x16 acc[TW][TW];
+#pragma unroll
+  for (int i = 0; i < TW; ++i)
+#pragma unroll
+    for (int j = 0; j < TW; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+
+  // 16 bits: 8 reduction values of 32 rows; binary32: four (the e of above)
+  auto frag = [&](const char* L, int row, int s, auto byrow) {
+    if constexpr (decltype(byrow)::value) {
+      return *reinterpret_cast<const Piece*>(L + by_row(row + rl, 2 * s + kg));
+    } else if constexpr (TY == kEltF32) {
+      const int c = row + rl;
+      Piece x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = *reinterpret_cast<const float*>(L + by_red(8 * s + 4 * kg + i, c >> 2) + (c & 3) * 4);
+      return x;
+    } else {
+      const int kr = 16 * s + 8 * kg + ((lane & 15) >> 2);
+      const int c = row + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+      typedef __attribute__((address_space(3))) s16x4* P;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + by_red(kr, c >> 3) + (c & 7) * 2));
+      const s16x4 hi =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(L + by_red(kr + 4, c >> 3) + (c & 7) * 2));
+      return __builtin_bit_cast(Piece, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
+  auto multiply = [&](int buf) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      Piece x[TW], y[TW];
+#pragma unroll
+      for (int i = 0; i < TW; ++i) {
+        x[i] = frag(lds[buf][0], BM / 2 * wm + 32 * i, s, std::integral_constant<bool, AROW>{});
+        y[i] = frag(lds[buf][1], BM / 2 * wn + 32 * i, s, std::integral_constant<bool, BROW>{});
+      }
+#pragma unroll
+      for (int i = 0; i < TW; ++i)
+#pragma unroll
+        for (int j = 0; j < TW; ++j) {
+          if constexpr (TY == kEltF32) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(y[j][v], x[i][v], acc[i][j], 0, 0, 0);
+          } else {
+            acc[i][j] = mma<TY>(__builtin_bit_cast(s16x8, y[j]), __builtin_bit_cast(s16x8, x[i]),
+                                acc[i][j]);
+          }
+        }
+    }
+  };
+  if (r0 < r1) {
+    // loads two rounds ahead; past the end they clear and read nothing
+    Set even, odd;
+    load(even, r0);
+    load(odd, r0 + ROUND);
+    put(0, even);
+    __syncthreads();
+    for (int64_t k = r0; k < r1; k += 2 * ROUND) {
+      load(even, k + 2 * ROUND);
+      multiply(0);
+      put(1, odd);
+      __syncthreads();
+      if (k + ROUND >= r1) break;
+      load(odd, k + 3 * ROUND);
+      multiply(1);
+      put(0, even);
+      __syncthreads();
+    }
+  }
+
+  // acc[i][j][v]: row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part
+#pragma unroll
+  for (int i = 0; i < TW; ++i) {
+    const int64_t r = row0 + BM / 2 * wm + 32 * i + rl;
+    if (r >= end) continue;
+    const bool masked = KIND == kInput && g.relu && e < g.E;
+    const int64_t xr = masked ? x_row(g, r) : 0;
+#pragma unroll
+    for (int j = 0; j < TW; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = n0 + BM / 2 * wn + 32 * j + 8 * q + 4 * kg;
+        if (c >= cols) continue;
+        float x[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          x[v] = acc[i][j][4 * q + v];
+          if (c + v >= cols) continue;
+          if constexpr (KIND == kForward) {
+            if (g.b && e < g.E) x[v] += g.b[(int64_t)e * g.N + c + v];
+            if (g.relu) x[v] = x[v] > 0.f ? x[v] : 0.f;
+          } else if constexpr (KIND == kInput) {
+            if (masked && !(xr >= 0 && rows::load1<TY>(g.X, xr * g.xs + c + v) > 0.f)) x[v] = 0.f;
+          }
+        }
+        if constexpr (KIND == kWeight || TY == kEltF32) {
+          float* out = KIND == kWeight ? dW + r * g.K + c : static_cast<float*>(g.Y) + r * g.ys + c;
+          if (c + 4 <= cols) {
+            store4(out, f32x4{x[0], x[1], x[2], x[3]});
+          } else {
+            for (int v = 0; v < cols - c; ++v) out[v] = x[v];
+          }
+        } else {
+          uint16_t* out = static_cast<uint16_t*>(g.Y) + r * g.ys + c;
+          uint16_t h[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) h[v] = (uint16_t)to_half<TY, false>(x[v], 0u);
+          if (c + 4 <= cols) {
+            __builtin_memcpy(out, h, 8);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 3; ++v)
+              if (c + v < cols) out[v] = h[v];
+          }
+        }
+      }
+  }
+}
+
+// ------------------------------------------------------------------------ few rows an expert
+// The forward product of a small request: its time is that of reading the weights of the
+// experts that have rows.  A block of four waves has 16 columns of one expert, a wave every
+// fourth 32 reduction values of them; weights and inputs go from memory to registers in the
+// form that the 16 x 16 matrix instruction takes (a lane 16 bytes of one row), eight loads of
+// weights in flight a wave, up to 64 rows of the expert against them.  The waves' sums are
+// added in order through LDS.
+constexpr int kFewRows = 64;
+template <int TY>
+__device__ __forceinline__ f32x4 mma16(s16x8 a, s16x8 b, f32x4 c) {
+  if constexpr (TY == kEltBF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <int TY, int RT>                                      // RT tiles of 16 rows
+__device__ __forceinline__ void few_rows(const Product& g, int e, int n0, int64_t row0,
+                                         int64_t end, f32x4 (*red)[4][64]) {
+  constexpr int DEEP = 8;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l = lane & 15, kg = lane >> 4;
+  const uint16_t* W = static_cast<const uint16_t*>(g.W) + (int64_t)e * g.N * g.K;
+  const uint16_t* wrow = W + (int64_t)(n0 + l < g.N ? n0 + l : g.N - 1) * g.K + 8 * kg;
+  const uint16_t* xrow[RT];
+  bool there[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int64_t r = row0 + 16 * i + l, x = r < end ? x_row(g, r) : -1;
+    there[i] = x >= 0;
+    xrow[i] = static_cast<const uint16_t*>(g.X) + (x >= 0 ? x : 0) * g.xs + 8 * kg;
+  }
+  f32x4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const s16x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int k0 = 32 * w; k0 < g.K; k0 += 4 * 32 * DEEP) {
+    s16x8 a[DEEP], b[DEEP][RT];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      const int k = k0 + 128 * d;
+      const bool in = k + 8 * kg < g.K;                        // K is a multiple of 8
+      a[d] = in ? *reinterpret_cast<const s16x8*>(wrow + k) : zero;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        b[d][i] = in && there[i] ? *reinterpret_cast<const s16x8*>(xrow[i] + k) : zero;
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) acc[i] = mma16<TY>(a[d], b[d][i], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) red[w][i][lane] = acc[i];
+  __syncthreads();
+  // a lane has columns 4 kg .. + 4 of row l; wave w finishes tile w
+  if (w < RT) {
+    const f32x4 s = ((red[0][w][lane] + red[1][w][lane]) + red[2][w][lane]) + red[3][w][lane];
+    const int64_t r = row0 + 16 * w + l;
+    const int c = n0 + 4 * kg;
+    if (r < end && c < g.N) {
+      uint32_t h[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float x = s[v];
+        if (g.b) x += g.b[(int64_t)e * g.N + c + v];
+        if (g.relu) x = x > 0.f ? x : 0.f;
+        h[v] = to_half<TY, false>(x, 0u);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.Y) + r * g.ys + c) =
+          make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    }
+  }
+  __syncthreads();
+}
+
+template <int TY>
+__global__ __launch_bounds__(kThreads) void few_kernel(Product g) {
+  __shared__ f32x4 red[4][4][64];
+  const int e = (int)(blockIdx.x / (uint32_t)g.col_tiles);
+  const int n0 = (int)(blockIdx.x % (uint32_t)g.col_tiles) * 16;
+  int64_t lo, hi;
+  bounds_of(g, e, &lo, &hi);
+  lo = uniform(lo);
+  hi = uniform(hi);
+  if (e == g.E) {                                              // positions of no expert
+    const int64_t c = n0 + (threadIdx.x & 1) * 8;
+    if (c < g.N)
+      for (int64_t r = lo + threadIdx.x / 2; r < hi; r += kThreads / 2)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.Y) + r * g.ys + c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  for (; lo < hi; lo += kFewRows) {
+    if (hi - lo <= 16) few_rows<TY, 1>(g, e, n0, lo, hi, red);
+    else if (hi - lo <= 32) few_rows<TY, 2>(g, e, n0, lo, hi, red);
+    else few_rows<TY, 4>(g, e, n0, lo, hi, red);
+  }
+}
+
 // db[e, c] = sum of dY over the expert's rows.  Like the weight gradient's reduction it is cut
 // into slices (of g.slice rows here), which write db itself or, where an expert has several,
 // partial sums [unit, N] that bias_join_kernel adds in order.  A block has one slice and
@@ -991,6 +1188,11 @@ static experts::Product expert_product(const void* X, int64_t xs, int64_t x_rows
   return g;
 }
 
+// Rows up to which the few-rows kernel takes the forward product: 16 an expert, and 64 (16
+// experts of 1024 x 1024: 96 rows 10 and 16 us with 128 x 128 tiles, 256 rows 14 and 16 us, 512
+// rows 18 and 16 us; one expert: 64 rows 8 and 16 us, 256 rows 25 and 16 us).
+static int64_t few_most(int E) { return 16 * (int64_t)E + 64; }
+
 // Row tiles that n rows in E + 1 pieces can need.
 static int64_t most_tiles(int64_t n, int E, int BM) { return n / BM + E + 1; }
 
@@ -1015,8 +1217,7 @@ static hipError_t launch_wide(experts::Product g, hipStream_t s) {
                              ? (g.n / g.slice + g.E) * (int64_t)g.row_tiles * g.col_tiles
                              : most_tiles(g.n, g.E, BM) * g.col_tiles;
   // as many blocks as run at once, or the tiles there can be
-  int64_t most = 256 * (BM == 256 ? 1 : 2);
-  if (getenv("CTR_NOSTAY") && KIND != experts::kWeight) most = 1 << 30;
+  const int64_t most = 256 * (BM == 256 ? 1 : 2);
   const int64_t grid = (blocks < most ? blocks : most) + kXcds - 1;
   const unsigned whole = (unsigned)(grid / kXcds * kXcds), threads = (BM / WM) * (BN / WN) * 64;
   if (KIND == experts::kWeight && g.order)
@@ -1027,41 +1228,58 @@ static hipError_t launch_wide(experts::Product g, hipStream_t s) {
   return hipGetLastError();
 }
 
-// 256 x 256 tiles, or 128 x 128 where the larger ones are too few to fill the chip.
-static bool big_tiles(int64_t row_tiles, int cols) {
-  return row_tiles * ((cols + 255) / 256) >= 512;
+// 256 x 256 tiles, or 128 x 128 ones, two blocks of which share a compute unit.  A round of
+// 256 large tiles takes 1 / 0.7 of a round of 512 small ones (1024 x 1024, 16 experts: 25 and
+// 16 us), so the choice is by rounds: 8192 rows 29 and 35 us (1 round and 2), 4096 rows 26 and
+// 20 us (1 and 1), 65536 rows 162 and 214 us (5 and 9).
+static bool big_tiles(int64_t n, int E, int cols) {
+  const int64_t big = (n / 256 + E / 2 + 1) * ((cols + 255) / 256);
+  const int64_t small = (n / 128 + E / 2 + 1) * ((cols + 127) / 128);
+  return (big + 255) / 256 * 10 <= (small + 511) / 512 * 7;
 }
 
 template <int TY, int KIND>
 static hipError_t launch_product(experts::Product g, bool wide, hipStream_t s) {
+  const int cols = KIND == experts::kForward ? g.N : g.K;
   if constexpr (TY != kEltF32) {
+    if constexpr (KIND == experts::kForward) {
+      if (wide && g.n <= few_most(g.E)) {
+        g.col_tiles = (g.N + 15) / 16;
+        experts::few_kernel<TY><<<(unsigned)((g.E + 1) * g.col_tiles), experts::kThreads, 0, s>>>(g);
+        return hipGetLastError();
+      }
+    }
     if (wide) {
-      const int v = getenv("CTR_TILE") ? atoi(getenv("CTR_TILE")) : 0;
-      if (v == 0) return launch_wide<TY, KIND, 256, 256, 128, 64>(g, s);
-      if (v == 1) return launch_wide<TY, KIND, 256, 128, 64, 64>(g, s);
+      if (KIND == experts::kWeight ? g.big : big_tiles(g.n, g.E, cols))
+        return launch_wide<TY, KIND, 256, 256, 128, 64>(g, s);
       return launch_wide<TY, KIND, 128, 128, 64, 64>(g, s);
     }
   }
-  const int cols = KIND == experts::kForward ? g.N : g.K;
-  g.col_tiles = (cols + 63) / 64;
-  g.row_tiles = (g.N + 63) / 64;
-  const int64_t rows = KIND == experts::kWeight ? (int64_t)g.E * g.row_tiles
-                                                : most_tiles(g.n, g.E, 64);
-  experts::product_kernel<TY, KIND>
-      <<<(unsigned)(rows * g.col_tiles), experts::kThreads, 0, s>>>(g);
+  auto tiles = [&](int BM) {
+    g.col_tiles = (cols + BM - 1) / BM;
+    g.row_tiles = (g.N + BM - 1) / BM;
+    const int64_t units = KIND == experts::kWeight ? (g.n / g.slice + g.E) * g.row_tiles
+                                                   : most_tiles(g.n, g.E, BM);
+    return units * g.col_tiles;
+  };
+  if (tiles(128) >= 512) {
+    experts::loose_kernel<TY, KIND, 128><<<(unsigned)tiles(128), experts::kThreads, 0, s>>>(g);
+  } else {
+    experts::loose_kernel<TY, KIND, 64><<<(unsigned)tiles(64), experts::kThreads, 0, s>>>(g);
+  }
   return hipGetLastError();
 }
 
-// Positions a slice of the weight gradient's reduction: about four blocks a compute unit in
-// all, at least 512.
-static void set_slices(experts::Product& g) {
-  const int64_t big = (int64_t)((g.N + 255) / 256) * ((g.K + 255) / 256);
-  const int64_t small = (int64_t)((g.N + 127) / 128) * ((g.K + 127) / 128);
-  g.slice_big = big * g.E >= 512;
-  const int64_t tiles = g.slice_big ? big : small;
-  int64_t slice = (g.n * tiles + 1023) / 1024;
+// Positions a slice of the weight gradient's reduction.  Where every expert once around gives
+// the compute units a tile each, only experts of more than twice the mean rows are cut: a
+// slice more costs writing and reading N K sums (16384 rows, 16 experts of 1024 x 1024: 116 us
+// with slices of 1024, 111 us with 2048).  Else as many slices as fill the chip.
+static void set_slices(experts::Product& g, bool wide) {
+  auto across = [&](int64_t t) { return (g.N + t - 1) / t * ((g.K + t - 1) / t); };
+  g.big = across(256) * g.E >= 256;
+  const int64_t tiles = across(wide ? (g.big ? 256 : 128) : 64);
+  int64_t slice = tiles * g.E >= 256 ? 2 * g.n / g.E : g.n * tiles / 512;
   slice = slice < 512 ? 512 : slice;
-  if (getenv("CTR_SLICE")) slice = atoi(getenv("CTR_SLICE"));
   g.slice = (slice + 63) / 64 * 64;
 }
 
@@ -1091,10 +1309,13 @@ static int64_t bias_slice(int64_t n) {
 
 size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtype) {
   experts::Product g = expert_product(nullptr, K, n, nullptr, 1, nullptr, n, E, K, nullptr, N);
-  int64_t need = 0;
+  // arrays that are not in whole 16-byte pieces may take the other kernel, and its slices
+  set_slices(g, false);
+  int64_t need = most_partials(g) * N * K;
   if (dtype != kEltF32 && K % 8 == 0 && N % 8 == 0) {
-    set_slices(g);
-    need = most_partials(g) * N * K;
+    set_slices(g, true);
+    const int64_t wide = most_partials(g) * N * K;
+    need = wide > need ? wide : need;
   }
   // the bias gradient's sums come after the weight gradient's are joined
   g.slice = bias_slice(n);
@@ -1125,10 +1346,10 @@ hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t
       h.W = nullptr;
       h.dW = dW;
       h.part = static_cast<float*>(workspace);
-      set_slices(h);
       const bool wide = wide_ok(h, dtype) && (reinterpret_cast<uintptr_t>(dW) & 15u) == 0;
+      set_slices(h, wide);
       e = launch_product<TY, experts::kWeight>(h, wide, s);
-      if (e == hipSuccess && wide && n > h.slice) {
+      if (e == hipSuccess && n > h.slice) {
         const int64_t each = ((int64_t)N * K + experts::kJoin - 1) / experts::kJoin;
         experts::join_kernel<<<(unsigned)(E * each), experts::kThreads, 0, s>>>(h);
         e = hipGetLastError();
