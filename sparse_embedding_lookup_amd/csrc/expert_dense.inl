@@ -776,15 +776,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
 // ---------------------------------------------------- any type, width, stride and alignment
 // What the staged kernel does not take: binary32, and 16-bit arrays in no whole 16-byte
 // pieces.  A block of four waves has a BM x BM tile, a wave a quarter of it; operands go
-// through registers, where what is past the end is cleared, into one of two LDS buffers, loaded
-// two rounds ahead.  A round is 128 bytes of a row: 64
+// through registers, where what is past the end is cleared, into one of two LDS buffers, those
+// of the next round while this round's products run.  A round is 128 bytes of a row: 64
 // reduction values of 16 bits or 32 of binary32.  LDS holds them as above.  The binary32
 // matrix instruction takes two reduction values a lane pair: lanes 0 to 31 have values
 // 8 c + e and lanes 32 to 63 values 8 c + 4 + e of both operands, so that by rows a lane's
 // next four values are one 16-byte read.
 // 64 x 64 tiles where 128 x 128 would leave compute units without a tile.
 template <int TY, int KIND, int BM>
-__global__ __launch_bounds__(kThreads) void loose_kernel(Product g) {
+__global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
   using T = typename std::conditional<TY == kEltF32, float, uint16_t>::type;
   constexpr int SIZE = sizeof(T), PE = 16 / SIZE;              // elements a piece
   constexpr int ROUND = 128 / SIZE, PIECES = BM * 8 / kThreads; // pieces a thread and operand
@@ -815,36 +815,69 @@ __global__ __launch_bounds__(kThreads) void loose_kernel(Product g) {
     end = g.N;
     r0 = u.lo;
     r1 = u.hi;
-    dW = u.partial >= 0 ? g.part + u.partial * g.N * g.K : dW + (int64_t)e * g.N * g.K;
+    const int64_t part = uniform(u.partial);
+    dW = part >= 0 ? g.part + part * g.N * g.K : dW + uniform(e) * g.N * g.K;
   } else {
     if (!find_tile<BM>(g, mt, &e, &row0, &end)) return;
     r1 = e < g.E ? (KIND == kForward ? g.K : g.N) : 0;
   }
+  e = __builtin_amdgcn_readfirstlane(e);
+  row0 = uniform(row0);
+  end = uniform(end);
+  r0 = uniform(r0);
+  r1 = uniform(r1);
   const T* X = static_cast<const T*>(g.X);
   const T* dY = static_cast<const T*>(g.dY);
   const T* W = static_cast<const T*>(g.W) + (int64_t)(e < g.E ? e : 0) * g.N * g.K;
 
   // A thread's pieces: by rows row t / 8 + 32 q and piece t % 8; by reduction number
-  // kThreads q + t of ACROSS to a reduction row.
+  // kThreads q + t of ACROSS to a reduction row, so always the same piece t % ACROSS.
   typedef T Piece __attribute__((ext_vector_type(PE)));
-  struct Set {
-    Piece a[PIECES], b[PIECES];
+  Piece a[PIECES], b[PIECES];
+  const int kp = (t & 7) * PE, kr = t / ACROSS, c = t % ACROSS * PE;
+  constexpr int STEP = kThreads / ACROSS;                      // reduction rows from q to q + 1
+  // A whole round reads whole pieces.  Rows and columns past the tile's last are not stored,
+  // so any in their place will do: rows the tile's first, and a column piece that is partly
+  // there the row's last whole one, moved down (by `down` elements) to where it belongs.
+  const int64_t atop = AROW ? end - row0 : end, btop = cols;
+  auto column = [&](int64_t first, int64_t top, int* down) -> int64_t {
+    const int64_t at = first + c;
+    *down = at < top && at + PE > top ? (int)(at + PE - top) : 0;
+    return at < top ? at - *down : first;
   };
-  auto get = [&](const T* p, int64_t there) {                  // `there` elements of a piece
-    Piece x;
-    if (there >= PE) {
-      __builtin_memcpy(&x, p, 16);
+  int adown = 0, bdown = 0;
+  const int64_t acol = AROW ? 0 : column(row0, atop, &adown);
+  const int64_t bcol = BROW ? 0 : column(n0, btop, &bdown);
+  const bool aedge = !AROW && row0 + BM > atop, bedge = !BROW && n0 + BM > btop;
+  const bool narrow = (!AROW && atop < PE) || (!BROW && btop < PE);
+  auto moved = [](Piece x, int down) {
+    if constexpr (TY == kEltF32) {
+      if (down & 1) x = __builtin_shufflevector(x, x, 1, 2, 3, 3);
+      if (down & 2) x = __builtin_shufflevector(x, x, 2, 3, 3, 3);
     } else {
-#pragma unroll
-      for (int i = 0; i < PE; ++i) x[i] = i < there ? p[i] : T(0);
+      if (down & 1) x = __builtin_shufflevector(x, x, 1, 2, 3, 4, 5, 6, 7, 7);
+      if (down & 2) x = __builtin_shufflevector(x, x, 2, 3, 4, 5, 6, 7, 7, 7);
+      if (down & 4) x = __builtin_shufflevector(x, x, 4, 5, 6, 7, 7, 7, 7, 7);
     }
+    return x;
+  };
+  auto all = [](const T* p) {
+    Piece x;
+    __builtin_memcpy(&x, p, 16);
+    return x;
+  };
+  auto some = [&](const T* p, int64_t there) {                 // `there` elements, then zeros
+    if (there >= PE) return all(p);
+    Piece x;
+#pragma unroll
+    for (int i = 0; i < PE; ++i) x[i] = i < there ? p[i] : T(0);
     return x;
   };
   int64_t xrow[PIECES];                                        // X's rows of the pieces
   auto look = [&](int64_t k) {                                 // the weight gradient's next
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
-      const int64_t p = k + (q * kThreads + t) / ACROSS;
+      const int64_t p = k + kr + q * STEP;
       xrow[q] = p < r1 ? x_row(g, p) : -1;
     }
   };
@@ -857,20 +890,44 @@ __global__ __launch_bounds__(kThreads) void loose_kernel(Product g) {
   } else if constexpr (KIND == kWeight) {
     look(r0);
   }
-  auto load = [&](Set& x, int64_t k) {
+  const Piece zero = {};
+  auto load = [&](int64_t k) {
+    if (k + ROUND <= r1 && !narrow) {
 #pragma unroll
-    for (int q = 0; q < PIECES; ++q) {
-      const int r = q * 32 + (t >> 3), kp = (t & 7) * PE;      // by rows
-      const int kr = (q * kThreads + t) / ACROSS, c = (q * kThreads + t) % ACROSS * PE;
-      if constexpr (KIND == kForward) {
-        x.a[q] = get(X + xrow[q] * g.xs + k + kp, xrow[q] >= 0 ? r1 - k - kp : 0);
-        x.b[q] = get(W + (int64_t)(n0 + r) * g.K + k + kp, n0 + r < cols ? r1 - k - kp : 0);
-      } else if constexpr (KIND == kInput) {
-        x.a[q] = get(dY + (row0 + r) * g.dys + k + kp, row0 + r < end ? r1 - k - kp : 0);
-        x.b[q] = get(W + (k + kr) * g.K + n0 + c, k + kr < r1 ? cols - n0 - c : 0);
-      } else {
-        x.a[q] = get(dY + (k + kr) * g.dys + row0 + c, k + kr < r1 ? end - row0 - c : 0);
-        x.b[q] = get(X + xrow[q] * g.xs + n0 + c, xrow[q] >= 0 ? cols - n0 - c : 0);
+      for (int q = 0; q < PIECES; ++q) {
+        const int r = q * 32 + (t >> 3);
+        const int64_t ar = row0 + (r < atop ? r : 0), br = n0 + r < btop ? n0 + r : n0;
+        const int64_t kk = k + kr + q * STEP;
+        if constexpr (KIND == kForward) {
+          a[q] = all(X + (xrow[q] >= 0 ? xrow[q] : 0) * g.xs + k + kp);
+          if (xrow[q] < 0) a[q] = zero;
+          b[q] = all(W + br * g.K + k + kp);
+        } else if constexpr (KIND == kInput) {
+          a[q] = all(dY + ar * g.dys + k + kp);
+          b[q] = all(W + kk * g.K + bcol);
+        } else {
+          a[q] = all(dY + kk * g.dys + acol);
+          b[q] = all(X + (xrow[q] >= 0 ? xrow[q] : 0) * g.xs + bcol);
+          if (xrow[q] < 0) b[q] = zero;
+        }
+        if (aedge) a[q] = moved(a[q], adown);
+        if (bedge) b[q] = moved(b[q], bdown);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) {
+        const int r = q * 32 + (t >> 3);
+        const int64_t kk = k + kr + q * STEP;
+        if constexpr (KIND == kForward) {
+          a[q] = some(X + xrow[q] * g.xs + k + kp, xrow[q] >= 0 ? r1 - k - kp : 0);
+          b[q] = some(W + (int64_t)(n0 + r) * g.K + k + kp, n0 + r < cols ? r1 - k - kp : 0);
+        } else if constexpr (KIND == kInput) {
+          a[q] = some(dY + (row0 + r) * g.dys + k + kp, row0 + r < end ? r1 - k - kp : 0);
+          b[q] = some(W + kk * g.K + n0 + c, kk < r1 ? cols - n0 - c : 0);
+        } else {
+          a[q] = some(dY + kk * g.dys + row0 + c, kk < r1 ? end - row0 - c : 0);
+          b[q] = some(X + xrow[q] * g.xs + n0 + c, xrow[q] >= 0 ? cols - n0 - c : 0);
+        }
       }
     }
     if constexpr (KIND == kWeight) look(k + ROUND);
@@ -882,13 +939,12 @@ __global__ __launch_bounds__(kThreads) void loose_kernel(Product g) {
     else if constexpr (BM == 64) return q * 128 + (c ^ (q & 2 ? 4 : 0)) * 16;
     else return q * BM * 2 + (c ^ (4 * (q & 3))) * 16;
   };
-  auto put = [&](int buf, const Set& x) {
+  auto put = [&](int buf) {
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
-      const int r = q * 32 + (t >> 3), c = t & 7;
-      const int kr = (q * kThreads + t) / ACROSS, cc = (q * kThreads + t) % ACROSS;
-      *reinterpret_cast<Piece*>(lds[buf][0] + (AROW ? by_row(r, c) : by_red(kr, cc))) = x.a[q];
-      *reinterpret_cast<Piece*>(lds[buf][1] + (BROW ? by_row(r, c) : by_red(kr, cc))) = x.b[q];
+      const int r = by_row(q * 32 + (t >> 3), t & 7), red = by_red(kr + q * STEP, t % ACROSS);
+      *reinterpret_cast<Piece*>(lds[buf][0] + (AROW ? r : red)) = a[q];
+      *reinterpret_cast<Piece*>(lds[buf][1] + (BROW ? r : red)) = b[q];
     }
   };
 
@@ -946,23 +1002,19 @@ __global__ __launch_bounds__(kThreads) void loose_kernel(Product g) {
     }
   };
   if (r0 < r1) {
-    // loads two rounds ahead; past the end they clear and read nothing
-    Set even, odd;
-    load(even, r0);
-    load(odd, r0 + ROUND);
-    put(0, even);
+    // (Loads two rounds ahead give nothing: 64 x 64 tiles 29 us for 27 at 4096 x 479 x 257 in
+    // binary32.)
+    load(r0);
+    put(0);
     __syncthreads();
-    for (int64_t k = r0; k < r1; k += 2 * ROUND) {
-      load(even, k + 2 * ROUND);
-      multiply(0);
-      put(1, odd);
-      __syncthreads();
-      if (k + ROUND >= r1) break;
-      load(odd, k + 3 * ROUND);
-      multiply(1);
-      put(0, even);
+    int buf = 0;
+    for (int64_t k = r0 + ROUND; k < r1; k += ROUND, buf ^= 1) {
+      load(k);
+      multiply(buf);
+      put(buf ^ 1);
       __syncthreads();
     }
+    multiply(buf);
   }
 
   // acc[i][j][v]: row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part
