@@ -282,35 +282,45 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
 }
 
 // ------------------------------------------------------------------ rows there and back
-// G lanes (a power of two) have one token and walk its row in pieces of VW elements: one
-// 16-byte vector, or single elements where alignment, width or strides do not allow vectors.
-// These kernels are copies with little arithmetic, bound by the memory they touch.
+// G lanes (a power of two) have one token and walk its row in pieces of 16 bytes, U of them at
+// a time, so that the loads of U pieces of K slots' rows are in flight together; the last
+// elements, less than a piece, go one by one.  These kernels are copies with little arithmetic,
+// bound by the memory they touch.  A piece needs the alignment of its elements only (the memory
+// pipeline takes any), so odd widths and strides run at nearly the same rate.
 template <int TY, bool VEC>
 struct Piece {
   static constexpr int kElems = VEC ? Vec<TY>::kElems : 1;
   float v[kElems];
   __device__ __forceinline__ void load(const void* base, int64_t i) {
-    if constexpr (VEC) {
-      Vec<TY> x;
-      x.load(static_cast<const char*>(base) + i * (TY == kEltF32 ? 4 : 2));
-#pragma unroll
-      for (int e = 0; e < kElems; ++e) v[e] = x.v[e];
-    } else {
+    if constexpr (!VEC) {
       v[0] = load1<TY>(base, i);
+    } else {
+      uint32_t u[4];
+      __builtin_memcpy(u, static_cast<const char*>(base) + i * (TY == kEltF32 ? 4 : 2), 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (TY == kEltF32) {
+          v[e] = __uint_as_float(u[e]);
+        } else {
+          v[2 * e] = half_lo<TY>(u[e]);
+          v[2 * e + 1] = half_hi<TY>(u[e]);
+        }
+      }
     }
   }
   __device__ __forceinline__ void store(void* base, int64_t i) const {
     if constexpr (!VEC) {
       store1<TY>(base, i, v[0]);
-    } else if constexpr (TY == kEltF32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-      uint4 x;
-      x.x = to_half<TY, false>(v[0], 0u) | (to_half<TY, false>(v[1], 0u) << 16);
-      x.y = to_half<TY, false>(v[2], 0u) | (to_half<TY, false>(v[3], 0u) << 16);
-      x.z = to_half<TY, false>(v[4], 0u) | (to_half<TY, false>(v[5], 0u) << 16);
-      x.w = to_half<TY, false>(v[6], 0u) | (to_half<TY, false>(v[7], 0u) << 16);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) = x;
+      uint32_t u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (TY == kEltF32)
+          u[e] = __float_as_uint(v[e]);
+        else
+          u[e] = to_half<TY, false>(v[2 * e], 0u) | (to_half<TY, false>(v[2 * e + 1], 0u) << 16);
+      }
+      __builtin_memcpy(static_cast<char*>(base) + i * (TY == kEltF32 ? 4 : 2), u, 16);
     }
   }
 };
@@ -330,86 +340,185 @@ struct RowArgs {
   int64_t ys;
 };
 
-// The rows of positions that hold no slot are zero.
-template <int TY, bool VEC>
-__device__ __forceinline__ void zero_tail(const RowArgs& a, int64_t t, int l) {
-  int64_t p = a.offsets[a.E];
-  p = (p < 0 ? 0 : p) + t;
-  Piece<TY, VEC> z{};
-  for (; p < a.n; p += a.T)
-    for (int64_t c = (int64_t)l * z.kElems; c < a.D; c += (int64_t)a.G * z.kElems)
-      z.store(a.y, p * a.ys + c);
+// The lane's part of a row: whole(c, pieces) for its pieces c, c + G, .. U at a time, those below
+// `pieces`, then one(i) for its single elements.
+template <int U, int PE, typename Whole, typename One>
+__device__ __forceinline__ void walk_row(const RowArgs& a, int l, Whole whole, One one) {
+  const int pieces = a.D / PE;
+  for (int c = l; c < pieces; c += U * a.G) whole(c, pieces);
+  for (int i = pieces * PE + l; i < a.D; i += a.G) one(i);
 }
 
-template <int TY, bool VEC>
+// The rows of positions that hold no slot are zero.
+template <int TY>
+__device__ __forceinline__ void zero_tail(const RowArgs& a, int64_t t, int l) {
+  using P = Piece<TY, true>;
+  int64_t p = a.offsets[a.E];
+  p = (p < 0 ? 0 : p) + t;
+  for (; p < a.n; p += a.T)
+    walk_row<1, P::kElems>(
+        a, l, [&](int c, int) { P{}.store(a.y, p * a.ys + c * P::kElems); },
+        [&](int i) { store1<TY>(a.y, p * a.ys + i, 0.f); });
+}
+
+// The positions (-1: none) and weights of K of a token's slots, from slot j on.
+template <int K>
+struct Slots {
+  int64_t p[K];
+  float w[K];
+  __device__ __forceinline__ void load(const RowArgs& a, int64_t t, int j) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int64_t at = j + i < a.k ? a.slots[t * a.k + j + i] : -1;
+      p[i] = at >= 0 && at < a.n ? at : -1;
+      w[i] = a.weights && j + i < a.k ? a.weights[t * a.k + j + i] : 1.f;
+    }
+  }
+};
+
+template <int TY, int K>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(RowArgs a) {
   const int l = threadIdx.x & (a.G - 1);
   const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / a.G;
   if (t >= a.T) return;
-  using P = Piece<TY, VEC>;
-  for (int64_t c = (int64_t)l * P::kElems; c < a.D; c += (int64_t)a.G * P::kElems) {
-    P x;
-    x.load(a.x, t * a.xs + c);
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t p = a.slots[t * a.k + j];
-      if (p >= 0 && p < a.n) x.store(a.y, p * a.ys + c);
-    }
+  using P = Piece<TY, true>;
+  constexpr int PE = P::kElems, U = 4;
+  for (int j = 0; j < a.k; j += K) {
+    Slots<K> s;
+    s.load(a, t, j);
+    walk_row<U, PE>(
+        a, l,
+        [&](int c, int pieces) {
+          P x[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (c + u * a.G < pieces) x[u].load(a.x, t * a.xs + (c + u * a.G) * PE);
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0)
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                if (c + u * a.G < pieces) x[u].store(a.y, s.p[i] * a.ys + (c + u * a.G) * PE);
+        },
+        [&](int e) {
+          const float x = load1<TY>(a.x, t * a.xs + e);
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0) store1<TY>(a.y, s.p[i] * a.ys + e, x);
+        });
   }
-  zero_tail<TY, VEC>(a, t, l);
+  zero_tail<TY>(a, t, l);
 }
 
-template <int TY, bool VEC>
+template <int TY, int K>
 __global__ __launch_bounds__(kThreads) void combine_fwd_kernel(RowArgs a) {
   const int l = threadIdx.x & (a.G - 1);
   const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / a.G;
   if (t >= a.T) return;
-  using P = Piece<TY, VEC>;
-  for (int64_t c = (int64_t)l * P::kElems; c < a.D; c += (int64_t)a.G * P::kElems) {
-    P y{};
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t p = a.slots[t * a.k + j];
-      if (p < 0 || p >= a.n) continue;
-      const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
-      P x;
-      x.load(a.x, p * a.xs + c);
+  using P = Piece<TY, true>;
+  // one piece of each of the K rows: 9.5 us at 8192 x 1024 and 94 us at 32771 x 2208, with two
+  // pieces 10.4 and 92 us, with four 11.9 and 114 us (fewer waves at once)
+  constexpr int PE = P::kElems, U = 1;
+  Slots<K> s;
+  s.load(a, t, 0);
+  walk_row<U, PE>(
+      a, l,
+      [&](int c, int pieces) {
+        P y[U]{};
+        for (int j = 0; j < a.k; j += K) {
+          if (a.k > K) s.load(a, t, j);
+          P x[K][U];
 #pragma unroll
-      for (int e = 0; e < P::kElems; ++e) y.v[e] = __builtin_fmaf(w, x.v[e], y.v[e]);
-    }
-    y.store(a.y, t * a.ys + c);
-  }
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0)
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                if (c + u * a.G < pieces) x[i][u].load(a.x, s.p[i] * a.xs + (c + u * a.G) * PE);
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0)
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < PE; ++e)
+                  y[u].v[e] = __builtin_fmaf(s.w[i], x[i][u].v[e], y[u].v[e]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c + u * a.G < pieces) y[u].store(a.y, t * a.ys + (c + u * a.G) * PE);
+      },
+      [&](int e) {
+        float y = 0.f;
+        for (int j = 0; j < a.k; j += K) {
+          if (a.k > K) s.load(a, t, j);
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0) y = __builtin_fmaf(s.w[i], load1<TY>(a.x, s.p[i] * a.xs + e), y);
+        }
+        store1<TY>(a.y, t * a.ys + e, y);
+      });
 }
 
-template <int TY, bool VEC>
+template <int TY, int K>
 __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
   const int l = threadIdx.x & (a.G - 1);
   const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / a.G;
   if (t >= a.T) return;
-  using P = Piece<TY, VEC>;
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t p = a.slots[t * a.k + j];
-    const bool there = p >= 0 && p < a.n;
-    float dot = 0.f;
-    if (there) {
-      const float w = a.weights ? a.weights[t * a.k + j] : 1.f;
-      for (int64_t c = (int64_t)l * P::kElems; c < a.D; c += (int64_t)a.G * P::kElems) {
-        P g, q, d;
-        g.load(a.x, t * a.xs + c);
-        if (a.dweights) {
-          q.load(a.p, p * a.ps + c);
+  using P = Piece<TY, true>;
+  constexpr int PE = P::kElems, U = 2;
+  for (int j = 0; j < a.k; j += K) {
+    Slots<K> s;
+    s.load(a, t, j);
+    float dot[K];
 #pragma unroll
-          for (int e = 0; e < P::kElems; ++e) dot = __builtin_fmaf(g.v[e], q.v[e], dot);
-        }
+    for (int i = 0; i < K; ++i) dot[i] = 0.f;
+    walk_row<U, PE>(
+        a, l,
+        [&](int c, int pieces) {
+          P g[U], x[K][U];
 #pragma unroll
-        for (int e = 0; e < P::kElems; ++e) d.v[e] = w * g.v[e];
-        d.store(a.y, p * a.ys + c);
+          for (int u = 0; u < U; ++u)
+            if (c + u * a.G < pieces) g[u].load(a.x, t * a.xs + (c + u * a.G) * PE);
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0 && a.dweights)
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                if (c + u * a.G < pieces) x[i][u].load(a.p, s.p[i] * a.ps + (c + u * a.G) * PE);
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0)
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                if (c + u * a.G < pieces) {
+                  P d;
+#pragma unroll
+                  for (int e = 0; e < PE; ++e) {
+                    if (a.dweights) dot[i] = __builtin_fmaf(g[u].v[e], x[i][u].v[e], dot[i]);
+                    d.v[e] = s.w[i] * g[u].v[e];
+                  }
+                  d.store(a.y, s.p[i] * a.ys + (c + u * a.G) * PE);
+                }
+        },
+        [&](int e) {
+          const float g = load1<TY>(a.x, t * a.xs + e);
+#pragma unroll
+          for (int i = 0; i < K; ++i)
+            if (s.p[i] >= 0) {
+              if (a.dweights)
+                dot[i] = __builtin_fmaf(g, load1<TY>(a.p, s.p[i] * a.ps + e), dot[i]);
+              store1<TY>(a.y, s.p[i] * a.ys + e, s.w[i] * g);
+            }
+        });
+    if (a.dweights) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        for (int d = 1; d < a.G; d <<= 1) dot[i] += __shfl_xor(dot[i], d);
+        if (l == 0 && j + i < a.k) a.dweights[t * a.k + j + i] = dot[i];
       }
     }
-    if (a.dweights) {
-      for (int d = 1; d < a.G; d <<= 1) dot += __shfl_xor(dot, d);
-      if (l == 0) a.dweights[t * a.k + j] = dot;
-    }
   }
-  zero_tail<TY, VEC>(a, t, l);
+  zero_tail<TY>(a, t, l);
 }
 
 inline bool row_vec(const void* p, int64_t stride, int D, int elem) {
@@ -524,14 +633,13 @@ static int row_lanes(int64_t pieces) {
 template <typename F>
 static hipError_t launch_rows(rows::RowArgs& a, int dtype, F f) {
   if (a.T == 0) return hipSuccess;
-  const int elem = dtype == kEltF32 ? 4 : 2;
-  const bool vec = rows::row_vec(a.x, a.xs, a.D, elem) && rows::row_vec(a.p, a.ps, a.D, elem) &&
-                   rows::row_vec(a.y, a.ys, a.D, elem);
-  a.G = row_lanes(vec ? (int64_t)a.D * elem / 16 : a.D);
+  a.G = row_lanes(a.D / (dtype == kEltF32 ? 4 : 8));
   const unsigned blocks = (unsigned)((a.T * a.G + rows::kThreads - 1) / rows::kThreads);
   return by_type(dtype, [&](auto ty) {
-    if (vec) f(ty, std::true_type{}, blocks);
-    else f(ty, std::false_type{}, blocks);
+    // slots taken together: all there are up to two, else four at a time
+    if (a.k == 1) f(ty, std::integral_constant<int, 1>{}, blocks);
+    else if (a.k == 2) f(ty, std::integral_constant<int, 2>{}, blocks);
+    else f(ty, std::integral_constant<int, 4>{}, blocks);
     return hipGetLastError();
   });
 }
@@ -543,8 +651,8 @@ hipError_t launch_expert_dispatch(const void* X, int dtype, int64_t xs, int64_t 
   a.T = T; a.n = T * k; a.D = D; a.k = k; a.E = E;
   a.slots = slots; a.offsets = offsets;
   a.x = X; a.xs = xs; a.y = P; a.ys = ps;
-  return launch_rows(a, dtype, [&](auto ty, auto vec, unsigned blocks) {
-    rows::dispatch_kernel<decltype(ty)::value, decltype(vec)::value>
+  return launch_rows(a, dtype, [&](auto ty, auto k, unsigned blocks) {
+    rows::dispatch_kernel<decltype(ty)::value, decltype(k)::value>
         <<<blocks, rows::kThreads, 0, s>>>(a);
   });
 }
@@ -556,8 +664,8 @@ hipError_t launch_expert_combine_fwd(const void* P, int dtype, int64_t ps, int64
   a.T = T; a.n = T * k; a.D = D; a.k = k;
   a.slots = slots; a.weights = weights;
   a.x = P; a.xs = ps; a.y = Y; a.ys = ys;
-  return launch_rows(a, dtype, [&](auto ty, auto vec, unsigned blocks) {
-    rows::combine_fwd_kernel<decltype(ty)::value, decltype(vec)::value>
+  return launch_rows(a, dtype, [&](auto ty, auto k, unsigned blocks) {
+    rows::combine_fwd_kernel<decltype(ty)::value, decltype(k)::value>
         <<<blocks, rows::kThreads, 0, s>>>(a);
   });
 }
@@ -570,8 +678,8 @@ hipError_t launch_expert_combine_bwd(const void* dY, int dtype, int64_t dys, int
   a.T = T; a.n = T * k; a.D = D; a.k = k; a.E = E;
   a.slots = slots; a.offsets = offsets; a.weights = weights; a.dweights = dweights;
   a.x = dY; a.xs = dys; a.p = dweights ? P : nullptr; a.ps = ps; a.y = dP; a.ys = dps;
-  return launch_rows(a, dtype, [&](auto ty, auto vec, unsigned blocks) {
-    rows::combine_bwd_kernel<decltype(ty)::value, decltype(vec)::value>
+  return launch_rows(a, dtype, [&](auto ty, auto k, unsigned blocks) {
+    rows::combine_bwd_kernel<decltype(ty)::value, decltype(k)::value>
         <<<blocks, rows::kThreads, 0, s>>>(a);
   });
 }
