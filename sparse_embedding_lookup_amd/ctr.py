@@ -654,20 +654,48 @@ def _launch(name: str, device: torch.device, args: tuple, stream, prepare: bool,
 
 
 def _expert_arg(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
-                device: torch.device, rows: bool = False) -> int:
-    """The address of an argument of this shape, dtype and device; contiguous, or with `rows`
-    2-D with contiguous rows of any stride."""
+                device: torch.device) -> int:
+    """The address of a contiguous argument of this shape, dtype and device."""
     if t.dtype != dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
     if t.device != device:
         raise ValueError("%s is on %s, not %s" % (name, t.device, device))
-    if rows:
-        _row_stride(t, name)
-    elif not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
+
+
+def _rows_arg(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
+              device: torch.device) -> tuple:
+    """The address and row stride of a 2-D argument of this shape, dtype and device."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, not %s" % (name, t.device, device))
+    return t.data_ptr(), _row_stride(t, name)
+
+
+def _matrix(out: Optional[torch.Tensor], name: str, rows: int, width: int, dtype: torch.dtype,
+            device: torch.device) -> tuple:
+    """An output in rows: (tensor, address, row stride), checked, or made if it is None
+    (empty_strided takes 1.25 us where empty takes 1.6)."""
+    if out is None:
+        out = torch.empty_strided((rows, width), (width, 1), dtype=dtype, device=device)
+        return out, out.data_ptr(), width
+    return (out,) + _rows_arg(out, name, (rows, width), dtype, device)
+
+
+def _dense(out: Optional[torch.Tensor], name: str, shape: tuple, stride: tuple,
+           dtype: torch.dtype, device: torch.device) -> tuple:
+    """A contiguous output: (tensor, address), checked, or made if it is None."""
+    if out is None:
+        out = torch.empty_strided(shape, stride, dtype=dtype, device=device)
+        return out, out.data_ptr()
+    return out, _expert_arg(out, name, shape, dtype, device)
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -675,10 +703,11 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     overlap."""
     if t.dim() != 2:
         raise ValueError("%s must be 2-D" % name)
-    width, stride = t.shape[1], t.stride(0)
-    if width > 1 and t.stride(1) != 1:
+    rows, width = t.shape
+    stride, inner = t.stride()
+    if width > 1 and inner != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    if t.shape[0] <= 1:
+    if rows <= 1:
         return max(stride, width)
     if stride < width:
         raise ValueError("%s must have rows that do not overlap" % name)
@@ -702,13 +731,9 @@ def ctr_expert_route_fwd(logits: torch.Tensor, k: int, renormalize: bool = True,
     code, ls = _expert_type(logits, "logits"), _row_stride(logits, "logits")
     T, E = logits.shape
     dev = logits.device
-    if experts is None:
-        experts = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    args = (logits.data_ptr(), code, ls, T, E, k, int(bool(renormalize)),
-            _expert_arg(experts, "experts", (T, k), torch.int32, dev),
-            _expert_arg(weights, "weights", (T, k), torch.float32, dev))
+    experts, ep = _dense(experts, "experts", (T, k), (k, 1), torch.int32, dev)
+    weights, wp = _dense(weights, "weights", (T, k), (k, 1), torch.float32, dev)
+    args = (logits.data_ptr(), code, ls, T, E, k, int(bool(renormalize)), ep, wp)
     return _launch("ctr_expert_route_fwd", dev, args, stream, prepare, (experts, weights))
 
 
@@ -721,14 +746,11 @@ def ctr_expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, weights: t
     code, ls = _expert_type(logits, "logits"), _row_stride(logits, "logits")
     T, E = logits.shape
     dev, k = logits.device, experts.shape[-1]
-    if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    dlogits, dp, dls = _matrix(dlogits, "dlogits", T, E, logits.dtype, dev)
     args = (logits.data_ptr(), code, ls, T, E, k, int(bool(renormalize)),
             _expert_arg(experts, "experts", (T, k), torch.int32, dev),
             _expert_arg(weights, "weights", (T, k), torch.float32, dev),
-            _expert_arg(dweights, "dweights", (T, k), torch.float32, dev),
-            _expert_arg(dlogits, "dlogits", (T, E), logits.dtype, dev, rows=True),
-            _row_stride(dlogits, "dlogits"))
+            _expert_arg(dweights, "dweights", (T, k), torch.float32, dev), dp, dls)
     return _launch("ctr_expert_route_bwd", dev, args, stream, prepare, dlogits)
 
 
@@ -752,20 +774,14 @@ def ctr_expert_sort(experts: torch.Tensor, num_experts: int,
         raise ValueError("experts must be [T, k]")
     T, k = experts.shape
     dev = experts.device
-    if offsets is None:
-        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    if slots is None:
-        slots = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if order is None:
-        order = torch.empty(T * k, dtype=torch.int32, device=dev)
+    offsets, fp = _dense(offsets, "offsets", (num_experts + 1,), (1,), torch.int32, dev)
+    slots, sp = _dense(slots, "slots", (T, k), (k, 1), torch.int32, dev)
+    order, op = _dense(order, "order", (T * k,), (1,), torch.int32, dev)
     if workspace is None:
         workspace = _workspace(expert_sort_workspace_bytes(T, k, num_experts), dev)
     wsb = ctypes.c_size_t(workspace.numel())
-    args = (_expert_arg(experts, "experts", (T, k), torch.int32, dev), T, k, num_experts,
-            _expert_arg(offsets, "offsets", (num_experts + 1,), torch.int32, dev),
-            _expert_arg(slots, "slots", (T, k), torch.int32, dev),
-            _expert_arg(order, "order", (T * k,), torch.int32, dev), workspace.data_ptr(),
-            ctypes.byref(wsb))
+    args = (_expert_arg(experts, "experts", (T, k), torch.int32, dev), T, k, num_experts, fp, sp,
+            op, workspace.data_ptr(), ctypes.byref(wsb))
     return _launch("ctr_expert_sort", dev, args, stream, prepare, (offsets, slots, order),
                 workspace)
 
@@ -788,12 +804,11 @@ def ctr_expert_dispatch(X: torch.Tensor, slots: torch.Tensor, offsets: torch.Ten
     """The tokens' rows in the experts' order: P [T * k, D], P[slots[t, j]] = X[t]; positions of
     no slot are zero."""
     code, dev = _expert_type(X, "X"), X.device
-    xs, D = _row_stride(X, "X"), X.shape[1]
     T, k, sp, op, E = _slot_args(slots, offsets, dev)
-    if P is None:
-        P = torch.empty((T * k, D), dtype=X.dtype, device=dev)
-    args = (_expert_arg(X, "X", (T, D), X.dtype, dev, rows=True), code, xs, T, k, D, sp, op, E,
-            _expert_arg(P, "P", (T * k, D), X.dtype, dev, rows=True), _row_stride(P, "P"))
+    D = X.shape[-1]
+    xp, xs = _rows_arg(X, "X", (T, D), X.dtype, dev)
+    P, pp, ps = _matrix(P, "P", T * k, D, X.dtype, dev)
+    args = (xp, code, xs, T, k, D, sp, op, E, pp, ps)
     return _launch("ctr_expert_dispatch", dev, args, stream, prepare, P)
 
 
@@ -803,13 +818,12 @@ def ctr_expert_combine_fwd(P: torch.Tensor, slots: torch.Tensor,
     """Y[t] = sum_j weights[t, j] P[slots[t, j]] (weights None: 1, the gradient of
     ctr_expert_dispatch)."""
     code, dev = _expert_type(P, "P"), P.device
-    ps, D = _row_stride(P, "P"), P.shape[1]
     T, k, sp, _, _ = _slot_args(slots, None, dev)
-    if Y is None:
-        Y = torch.empty((T, D), dtype=P.dtype, device=dev)
+    D = P.shape[-1]
+    pp, ps = _rows_arg(P, "P", (T * k, D), P.dtype, dev)
+    Y, yp, ys = _matrix(Y, "Y", T, D, P.dtype, dev)
     wp = None if weights is None else _expert_arg(weights, "weights", (T, k), torch.float32, dev)
-    args = (_expert_arg(P, "P", (T * k, D), P.dtype, dev, rows=True), code, ps, T, k, D, sp, wp,
-            _expert_arg(Y, "Y", (T, D), P.dtype, dev, rows=True), _row_stride(Y, "Y"))
+    args = (pp, code, ps, T, k, D, sp, wp, yp, ys)
     return _launch("ctr_expert_combine_fwd", dev, args, stream, prepare, Y)
 
 
@@ -821,23 +835,18 @@ def ctr_expert_combine_bwd(dY: torch.Tensor, P: Optional[torch.Tensor], slots: t
     """(dP [T * k, D], dweights fp32 [T, k]) of ctr_expert_combine_fwd; P None: dP alone (then
     dweights is None)."""
     code, dev = _expert_type(dY, "dY"), dY.device
-    dys, D = _row_stride(dY, "dY"), dY.shape[1]
     T, k, sp, op, E = _slot_args(slots, offsets, dev)
-    if dP is None:
-        dP = torch.empty((T * k, D), dtype=dY.dtype, device=dev)
+    D = dY.shape[-1]
+    yp, dys = _rows_arg(dY, "dY", (T, D), dY.dtype, dev)
+    dP, dpp, dps = _matrix(dP, "dP", T * k, D, dY.dtype, dev)
     pp, ps, dwp = None, D, None
     if P is not None:
-        pp = _expert_arg(P, "P", (T * k, D), dY.dtype, dev, rows=True)
-        ps = _row_stride(P, "P")
-        if dweights is None:
-            dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        dwp = _expert_arg(dweights, "dweights", (T, k), torch.float32, dev)
+        pp, ps = _rows_arg(P, "P", (T * k, D), dY.dtype, dev)
+        dweights, dwp = _dense(dweights, "dweights", (T, k), (k, 1), torch.float32, dev)
     elif dweights is not None:
         raise ValueError("dweights needs P")
     wp = None if weights is None else _expert_arg(weights, "weights", (T, k), torch.float32, dev)
-    args = (_expert_arg(dY, "dY", (T, D), dY.dtype, dev, rows=True), code, dys, T, k, D, pp, ps,
-            sp, op, E, wp, _expert_arg(dP, "dP", (T * k, D), dY.dtype, dev, rows=True),
-            _row_stride(dP, "dP"), dwp)
+    args = (yp, code, dys, T, k, D, pp, ps, sp, op, E, wp, dpp, dps, dwp)
     return _launch("ctr_expert_combine_bwd", dev, args, stream, prepare, (dP, dweights))
 
 
@@ -872,11 +881,9 @@ def ctr_expert_dense_fwd(X: torch.Tensor, W: torch.Tensor, b: Optional[torch.Ten
     k) the token's row X [T, K]."""
     first, n, E, N, K = _product_args(X, W, offsets, order, k)
     dev = X.device
-    if Y is None:
-        Y = torch.empty((n, N), dtype=X.dtype, device=dev)
+    Y, yp, ys = _matrix(Y, "Y", n, N, X.dtype, dev)
     bp = None if b is None else _expert_arg(b, "b", (E, N), torch.float32, dev)
-    args = first + (bp, N, int(bool(relu)),
-                    _expert_arg(Y, "Y", (n, N), X.dtype, dev, rows=True), _row_stride(Y, "Y"))
+    args = first + (bp, N, int(bool(relu)), yp, ys)
     return _launch("ctr_expert_dense_fwd", dev, args, stream, prepare, Y)
 
 
@@ -903,23 +910,19 @@ def ctr_expert_dense_bwd(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor
     is not wanted (bias, want_dx, want_dw) is None."""
     first, n, E, N, K = _product_args(X, W, offsets, order, k)
     dev = X.device
-    if want_dx and dX is None:
-        dX = torch.empty((n, K), dtype=X.dtype, device=dev)
-    if want_dw and dW is None:
-        dW = torch.empty((E, N, K), dtype=torch.float32, device=dev)
-    if bias and db is None:
-        db = torch.empty((E, N), dtype=torch.float32, device=dev)
+    yp, dys = _rows_arg(dY, "dY", (n, N), X.dtype, dev)
+    xp, dxs, wp, bp = None, K, None, None
+    if want_dx:
+        dX, xp, dxs = _matrix(dX, "dX", n, K, X.dtype, dev)
+    if want_dw:
+        dW, wp = _dense(dW, "dW", (E, N, K), (N * K, K, 1), torch.float32, dev)
+    if bias:
+        db, bp = _dense(db, "db", (E, N), (N, 1), torch.float32, dev)
     if workspace is None:
         workspace = _workspace(expert_dense_bwd_workspace_bytes(n, E, K, N, first[1]), dev)
     wsb = ctypes.c_size_t(workspace.numel())
-    args = first + (
-        N, int(bool(x_relu)), _expert_arg(dY, "dY", (n, N), X.dtype, dev, rows=True),
-        _row_stride(dY, "dY"),
-        _expert_arg(dX, "dX", (n, K), X.dtype, dev, rows=True) if want_dx else None,
-        _row_stride(dX, "dX") if want_dx else K,
-        _expert_arg(dW, "dW", (E, N, K), torch.float32, dev) if want_dw else None,
-        _expert_arg(db, "db", (E, N), torch.float32, dev) if bias else None,
-        workspace.data_ptr(), ctypes.byref(wsb))
+    args = first + (N, int(bool(x_relu)), yp, dys, xp, dxs, wp, bp, workspace.data_ptr(),
+                    ctypes.byref(wsb))
     return _launch("ctr_expert_dense_bwd", dev, args, stream, prepare,
                 (dX if want_dx else None, dW if want_dw else None, db if bias else None),
                 workspace)
@@ -976,8 +979,8 @@ def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepar
         op = None if outs is None else _tensor_list(list(outs), out_name, dev, counts, codes)[0]
         return _launch(name, dev, head + (op,) + tail, stream, prepare, stats, workspace)
     pp, _, pcodes = _tensor_list(list(outs), out_name, dev, counts)
-    return _launch(name, dev, head + (pp, (ctypes.c_int32 * num)(*pcodes), float(lr)) + tail, stream,
-                prepare, stats, workspace)
+    return _launch(name, dev, head + (pp, (ctypes.c_int32 * num)(*pcodes), float(lr)) + tail,
+                   stream, prepare, stats, workspace)
 
 
 def ctr_grad_clip(grads: Sequence[torch.Tensor], max_norm: float,
