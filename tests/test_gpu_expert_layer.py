@@ -1,0 +1,199 @@
+"""ExpertLayer and ExpertClicks: every stage against its definition in 64 bits on the stage's own
+inputs (so the bounds are those of the single operators), graph replays against eager steps,
+training; and the products at sizes that take the largest tiles, with several tiles a block,
+cut reductions and odd widths."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_embedding_lookup_amd import ctr
+from sparse_embedding_lookup_amd.experts import ExpertClicks, ExpertLayer, synthetic_clicks
+from tests import experts_ref as ref
+from tests.experts_ref import U32, assert_near, stored
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+DEV = "cuda"
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def _fill(layer, seed):
+    g = torch.Generator().manual_seed(seed)
+    layer.X.copy_(torch.randn(layer.X.shape, generator=g))
+    layer.dY.copy_(torch.randn(layer.dY.shape, generator=g))
+    layer.b1.copy_(torch.randn(layer.b1.shape, generator=g) * 0.1)
+    layer.b2.copy_(torch.randn(layer.b2.shape, generator=g) * 0.1)
+
+
+# (tokens, dim, hidden, out, experts, k, renormalize, gather)
+LAYERS = [(1, 8, 16, 8, 4, 2, True, True), (37, 40, 24, 16, 8, 2, True, False),
+          (300, 61, 33, 7, 5, 3, False, True), (1200, 96, 136, 64, 4, 1, False, False),
+          (513, 128, 256, 1, 16, 2, True, True)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T,D,N1,N2,E,k,renorm,gather", LAYERS)
+def test_layer_stages(T, D, N1, N2, E, k, renorm, gather, dtype):
+    say("layer", T, D, N1, N2, E, k, renorm, gather, dtype)
+    L = ExpertLayer(T, D, N1, N2, E, k, dtype, renorm, gather)
+    _fill(L, T + D)
+    before = [p.cpu().clone() for p in L.params]
+    L.forward()
+    L.backward()
+    h = {n: getattr(L, n).cpu() for n in ("X", "logits", "experts", "weights", "offsets", "slots",
+                                          "order", "H", "Q", "Y", "dY", "dQ", "dweights", "dH",
+                                          "dP", "dlogits", "dXg", "dX", "P")}
+    n, m = T * k, int(h["offsets"][E])
+    Wg, W1, b1, W2, b2 = before
+    all_rows = torch.tensor([0, T])
+
+    def near(name, v, mag, terms):
+        assert_near(h[name], v, stored(v, (terms + 3) * U32 * mag, dtype), name)
+    near("logits", *ref.dense_fwd(h["X"], Wg, None, all_rows, False, None, 1, T), D)
+    we, ww = ref.route_fwd(h["logits"], k, renorm)
+    assert torch.equal(h["experts"], we)
+    assert_near(h["weights"], ww, (64 + E + 10) * 2 * U32 * ww + 1e-30, "weights")
+    for a, b in zip((h["offsets"], h["slots"], h["order"]), ref.sort(we, E)):
+        assert torch.equal(a, b)
+    order = h["order"] if gather else None
+    near("H", *ref.dense_fwd(h["P"], W1, b1, h["offsets"], True, order, k, n), D)
+    near("Q", *ref.dense_fwd(h["H"], W2, b2, h["offsets"], False, None, 1, n), N1)
+    near("Y", *ref.combine_fwd(h["Q"], h["slots"], h["weights"]), k)
+    dQ, dw, mag = ref.combine_bwd(h["dY"], h["Q"], h["slots"], h["weights"])
+    near("dQ", dQ, dQ.abs(), 0)
+    assert_near(h["dweights"], dw, (N2 + 2) * U32 * mag, "dweights")
+    second = ref.dense_bwd(h["H"], W2, h["offsets"], h["dQ"], None, 1, True)
+    near("dH", *second["dX"])
+    first = ref.dense_bwd(h["P"], W1, h["offsets"], h["dH"], order, k, False)
+    near("dP", *first["dX"])
+    want = ref.route_bwd(h["logits"], we, h["dweights"], renorm)
+    most = h["dweights"].abs().sum(1, keepdim=True).double()
+    assert_near(h["dlogits"], want, stored(want, (64 + E + k + 20) * 4 * U32 * most, dtype), "dlogits")
+    gate = ref.dense_bwd(h["X"], Wg, all_rows, h["dlogits"], None, 1, False)
+    near("dXg", *gate["dX"])
+    # the sum of the slots' rows, rounded, plus the gate's part, rounded
+    back, bmag = ref.combine_fwd(h["dP"], h["slots"], None)
+    half = stored(back, (k + 2) * U32 * bmag, dtype)
+    total = back + h["dXg"].double()
+    assert_near(h["dX"], total, stored(total, half, dtype), "dX")
+    grads = [g.cpu() for g in L.grads]
+    for g, (v, mag, terms), name in zip(grads, (gate["dW"], first["dW"], first["db"], second["dW"],
+                                                second["db"]), ("dWg", "dW1", "db1", "dW2", "db2")):
+        assert_near(g, v, (terms + 2) * U32 * mag, name)
+    norm = float(torch.sqrt(sum((g.double() ** 2).sum() for g in grads)))
+    lr, max_norm = 0.25, norm / 2
+    stats = L.update(lr, max_norm).cpu()
+    assert abs(float(stats[0]) - norm) <= 2 * U32 * norm
+    c = float(np.float32(lr)) * (float(np.float32(max_norm)) / norm)
+    for p, b, g in zip(L.params, before, grads):
+        move = c * g.double()
+        want = b.double() - move
+        assert_near(p, want, stored(want, U32 * want.abs() + 4 * U32 * move.abs(), p.dtype), "param")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_in_a_graph(dtype):
+    """Steps replayed from a graph leave the parameters that eager steps leave."""
+    say("layer graph", dtype)
+    pair = [ExpertLayer(700, 64, 128, 32, 6, 2, dtype) for _ in range(2)]
+    for L in pair:
+        _fill(L, 5)
+
+    def step(L):
+        L.forward()
+        L.backward()
+        L.update(0.1, 1.0)
+    for L in pair:
+        step(L)                                 # also marshals the update's call
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(pair[0])
+    for _ in range(4):
+        graph.replay()
+        step(pair[1])
+        torch.cuda.synchronize()
+        for a, b in zip(pair[0].params + [pair[0].dX, pair[0].Y],
+                        pair[1].params + [pair[1].dX, pair[1].Y]):
+            assert torch.equal(a, b)
+
+
+def test_clicks_learn():
+    """Training lowers the normalized entropy well below that of the click rate alone (1)."""
+    m = ExpertClicks(2048, 32, 64, 8)
+    last = []
+    for i in range(150):
+        x, y = synthetic_clicks(2048, 32, DEV, i)
+        m.layer.X.copy_(x)
+        m.labels.copy_(y)
+        m.step(1.0, 1.0)
+        if i >= 140:
+            last.append(float(m.ne[2]))
+    say("NE", last)
+    assert max(last) < 0.8 and all(np.isfinite(last))
+
+
+# (rows, experts, K, N, dtype): the largest tiles and more of them than blocks for Y, dX and dW;
+# odd widths at the same sizes
+LARGE = [(9000, 4, 96, 2048, BF16), (9000, 4, 2048, 96, F16), (600, 4, 2048, 2048, BF16),
+         (5000, 4, 2048, 2056, BF16), (9000, 5, 97, 2049, F32), (9000, 5, 2049, 97, BF16),
+         (3000, 3, 1031, 1027, F16), (40000, 3, 72, 64, BF16), (40000, 3, 33, 65, F32)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("n,E,K,N,dtype", LARGE)
+def test_large_products(n, E, K, N, dtype, gather):
+    say("large", n, E, K, N, dtype, gather)
+    g = torch.Generator().manual_seed(n + K)
+    share = torch.softmax(1.5 * torch.randn(E, generator=g), 0).cumsum(0)
+    offsets = torch.cat([torch.zeros(1), (share * n).floor()]).int()
+    offsets[E] = n - 13                         # a few positions of no expert
+    order = torch.randperm(n, generator=g).int() if gather else None
+    X = torch.randn((n, K), generator=g).to(dtype)
+    W = (torch.randn((E, N, K), generator=g) * K ** -0.5).to(dtype)
+    dY = torch.randn((n, N), generator=g).to(dtype)
+    at = None if order is None else order.to(DEV)
+    Xd, Wd, fd, dYd = X.to(DEV), W.to(DEV), offsets.to(DEV), dY.to(DEV)
+    Y = ctr.ctr_expert_dense_fwd(Xd, Wd, None, fd, False, at, 1)
+    dX, dW, db = ctr.ctr_expert_dense_bwd(Xd, Wd, fd, dYd, at, 1)
+    v, mag = ref.dense_fwd(X, W, None, offsets, False, order, 1, n)
+    assert_near(Y, v, stored(v, (K + 3) * U32 * mag, dtype), "Y")
+    want = ref.dense_bwd(X, W, offsets, dY, order, 1, False)
+    v, mag, terms = want["dX"]
+    assert_near(dX, v, stored(v, (terms + 2) * U32 * mag, dtype), "dX")
+    for got, name in ((dW, "dW"), (db, "db")):
+        v, mag, terms = want[name]
+        assert_near(got, v, (terms + 2) * U32 * mag, name)
+
+
+def test_memory_of_a_call_on_another_stream():
+    """What the binding allocates for a call on a given stream is not reused by the current
+    stream before that call has run."""
+    side = torch.cuda.Stream()
+    g = torch.Generator().manual_seed(3)
+    experts = torch.randint(0, 7, (60000, 2), generator=g, dtype=torch.int32)
+    want = ref.sort(experts, 7)
+    e = experts.to(DEV)
+    a = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(10):
+            a = a @ a * 1e-3                    # the sort waits behind these
+    got = ctr.ctr_expert_sort(e, 7, stream=side)
+    for _ in range(8):                          # the workspace's memory, were it free
+        torch.empty(200 * 7 * 4 + 512, dtype=torch.uint8, device=DEV).fill_(255)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x.cpu(), y)
+
+
+def test_gpu_tensors_are_required():
+    with pytest.raises(ValueError):
+        ctr.ctr_expert_route_fwd(torch.zeros(4, 8), 2)
+    with pytest.raises(ValueError):
+        ctr.ctr_grad_clip([torch.zeros(4)], 1.0)
