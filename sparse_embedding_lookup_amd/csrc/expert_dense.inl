@@ -37,6 +37,7 @@ struct Product {
   int64_t ys;
   float* dW;
   float* part;                  // partial sums of dW
+  const struct Plan* plan;      // who takes which tile of dW
   int64_t slice;                // positions a slice of dW's reduction
   bool big;                     // dW in 256 x 256 tiles
   int col_tiles, row_tiles;
@@ -172,76 +173,125 @@ __device__ __forceinline__ bool find_slice(const Product& g, int64_t unit, int e
   return false;
 }
 
-// What a tile costs beside its rounds of 64 (its first loads, its stores), in rounds.
-constexpr int64_t kTileCost = 10;
-// The first of the weight gradient's tiles (units in order, `tiles` each) that belongs to the
-// last (8 - x) eighths of their cost.
-__device__ __forceinline__ int64_t first_by_cost(const Product& g, int tiles, int x) {
-  const int lane = threadIdx.x & 63;
-  const int64_t full = g.slice / 64 + kTileCost;               // of a whole slice's tile
-  auto cost = [&](int64_t rows, int c) {
-    return c > 0 ? (c - 1) * full + (rows - (c - 1) * g.slice + 63) / 64 + kTileCost : 0;
+// The weight gradient's tiles are as long as their expert has rows, which differ widely.  One
+// block lays out who takes which before the product: a unit's tiles in entries of at most 32
+// neighbours, the entries sorted by the length of their tiles and dealt to the XCDs like cards,
+// largest first, back and forth.  An XCD's blocks walk its tiles in strides to and fro, so that
+// who begins with the longest tile ends with the shortest.  (Runs of tiles of equal cost an
+// XCD, unsorted: dW of 16384 rows in 16 uneven experts of 1024 x 1024 ... us for ... us.)
+struct Entry {
+  int32_t start;                // the entry's first tile in the XCD's order
+  int32_t expert, lo, hi, partial;
+  int32_t tile;                 // its first tile of the unit's
+  int32_t pad[2];
+};
+constexpr int kEntries = 2048, kPlanThreads = 1024;
+struct Plan {
+  int32_t tiles[8], count[8];   // of each XCD
+  Entry entry[8][kEntries / 8];
+};
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(Product g, Plan* plan) {
+  __shared__ int32_t units_to[kPlanThreads], partials_to[kPlanThreads];
+  __shared__ int32_t wave_sum[2][16], rounds[kEntries], many[8][kEntries / 8];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  int64_t lo, hi;
+  const int c = t < g.E ? slices_of(g, t, &lo, &hi) : 0, m = c > 1 ? c : 0;
+  int upto = c, mupto = m;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d), x = __shfl_up(mupto, d);
+    if (lane >= d) {
+      upto += v;
+      mupto += x;
+    }
+  }
+  if (lane == 63) {
+    wave_sum[0][w] = upto;
+    wave_sum[1][w] = mupto;
+  }
+  __syncthreads();
+  int units = 0;
+  for (int i = 0; i < 16; ++i) {
+    if (i < w) {
+      upto += wave_sum[0][i];
+      mupto += wave_sum[1][i];
+    }
+    units += wave_sum[0][i];
+  }
+  units_to[t] = upto;
+  partials_to[t] = mupto;
+  const int tiles = g.row_tiles * g.col_tiles;
+  int parts = (tiles + 31) / 32, least = (2 * (int)kXcds + units - 1) / units;
+  parts = parts > least ? parts : least;
+  parts = parts < tiles ? parts : tiles;
+  parts = parts < kEntries / units ? parts : kEntries / units;
+  const int entries = units * parts;           // set_slices keeps the units below kEntries
+  __syncthreads();
+  auto of = [&](int j, Entry* x) {             // entry j, units in order; its tiles' number
+    const int u = j / parts, p = j % parts;
+    int e = 0;
+    for (int d = kPlanThreads / 2; d > 0; d >>= 1)
+      if (units_to[e + d - 1] <= u) e += d;
+    int64_t elo, ehi;
+    const int n = slices_of(g, e, &elo, &ehi), i = u - (units_to[e] - n);
+    x->expert = e;
+    x->lo = (int32_t)(elo + i * g.slice);
+    x->hi = (int32_t)(ehi - x->lo < g.slice ? ehi : x->lo + g.slice);
+    x->partial = n > 1 ? partials_to[e] - n + i : -1;
+    x->tile = tiles * p / parts;
+    return tiles * (p + 1) / parts - x->tile;
   };
-  int64_t total = 0;
-  for (int e = lane; e < g.E; e += 64) {
-    int64_t lo, hi;
-    const int c = slices_of(g, e, &lo, &hi);
-    total += cost(hi - lo, c);
+  Entry x{};
+  for (int j = t; j < entries; j += kPlanThreads) {
+    of(j, &x);
+    rounds[j] = (x.hi - x.lo + 63) / 64;
   }
-  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-  const int64_t target = total * tiles * x / kXcds;
-  int64_t run = 0, units = 0;
-  for (int e0 = 0; e0 < g.E; e0 += 64) {
-    int64_t lo = 0, hi = 0;
-    const int c = e0 + lane < g.E ? slices_of(g, e0 + lane, &lo, &hi) : 0;
-    const int64_t mine = cost(hi - lo, c) * tiles;
-    int64_t upto = mine;
-    int cupto = c;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t v = __shfl_up(upto, d);
-      const int y = __shfl_up(cupto, d);
-      if (lane >= d) {
-        upto += v;
-        cupto += y;
+  __syncthreads();
+  for (int j = t; j < entries; j += kPlanThreads) {
+    const int mine = rounds[j];
+    int rank = 0;
+    for (int i = 0; i < entries; ++i) rank += rounds[i] > mine || (rounds[i] == mine && i < j);
+    const int at = rank / (int)kXcds, in = rank % (int)kXcds;
+    const int xcd = at & 1 ? (int)kXcds - 1 - in : in;
+    many[xcd][at] = of(j, &x);
+    plan->entry[xcd][at] = x;                  // without its start
+  }
+  __syncthreads();
+  if (w < (int)kXcds) {                        // wave w: the starts of XCD w's entries
+    const int full = entries / (int)kXcds, odd = entries % (int)kXcds;
+    const int count = full + ((full & 1 ? (int)kXcds - 1 - w : w) < odd);
+    int run = 0;
+    for (int i = 0; i < count; i += 64) {
+      const int n = i + lane < count ? many[w][i + lane] : 0;
+      int s = n;
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(s, d);
+        if (lane >= d) s += v;
       }
+      if (i + lane < count) plan->entry[w][i + lane].start = run + s - n;
+      run += __shfl(s, 63);
     }
-    const uint64_t past = __ballot(run + upto > target);
-    if (past) {
-      const int at = __ffsll((unsigned long long)past) - 1;
-      int64_t left = target - run - __shfl(upto - mine, at);
-      const int64_t rows = __shfl(hi - lo, at);
-      const int count = __shfl(c, at);
-      int64_t i = left / (full * tiles);
-      i = i < count - 1 ? i : count - 1;
-      left -= i * full * tiles;
-      const int64_t each = i < count - 1 ? full : cost(rows - i * g.slice, 1);
-      int64_t t = (left + each - 1) / each;
-      t = t < tiles ? t : tiles;
-      return (units + __shfl(cupto - c, at) + i) * tiles + t;
+    if (lane == 0) {
+      plan->tiles[w] = run;
+      plan->count[w] = count;
     }
-    run += __shfl(upto, 63);
-    units += __shfl(cupto, 63);
   }
-  return units * tiles;
 }
 
-// The block's first tile and the end of its XCD's part of all tiles: blocks go to the 8 XCDs in
-// turn, and each XCD, which has an L2 of its own, has a run of neighbouring tiles that share
-// operands.
-template <int KIND, int BM>
-__device__ __forceinline__ void part_of(const Product& g, int64_t* first, int64_t* last) {
-  const int x = blockIdx.x % kXcds;
-  if constexpr (KIND == kWeight) {
-    const int tiles = g.row_tiles * g.col_tiles;
-    *first = first_by_cost(g, tiles, x);
-    *last = x + 1 < (int)kXcds ? first_by_cost(g, tiles, x + 1) : count_slices(g) * tiles;
-  } else {
-    const int64_t total = count_tiles<BM>(g) * g.col_tiles;
-    *first = total * x / kXcds;
-    *last = total * (x + 1) / kXcds;
+// Tile i of XCD x's.
+__device__ __forceinline__ Entry find_entry(const Plan* plan, int x, int i) {
+  const int lane = threadIdx.x & 63, count = plan->count[x];
+  int at = -1;
+  for (int k = 0; k < count; k += 64) {
+    const uint64_t before = __ballot(k + lane < count && plan->entry[x][k + lane].start <= i);
+    at += __popcll(before);
+    if (before != ~0ull) break;
   }
-  *first = uniform(*first) + blockIdx.x / kXcds;
-  *last = uniform(*last);
+  const auto* p = (const __attribute__((address_space(4))) int32_t*)(uintptr_t)
+      &plan->entry[x][__builtin_amdgcn_readfirstlane(at < 0 ? 0 : at)];
+  Entry e;
+  e.start = p[0]; e.expert = p[1]; e.lo = p[2]; e.hi = p[3]; e.partial = p[4]; e.tile = p[5];
+  return e;
 }
 
 // Four floats, aligned to one.
@@ -315,9 +365,7 @@ __device__ __forceinline__ uint32_t keep_positive(uint32_t h, uint32_t m) {
 // The matrix cores take the columns as their rows: a lane then holds four neighbouring
 // columns of one output row, stored together.
 //
-// Blocks stay: each takes tiles of its XCD's part until there are none.  The parts have equal
-// cost, which for the weight gradient, whose tiles are as long as their expert has rows, is
-// not equal numbers.
+// Blocks stay: each takes tiles of its XCD's part until there are none.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -410,15 +458,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     n.r0 = 0;
     n.dW = g.dW;
     if constexpr (KIND == kWeight) {
-      const uint32_t tiles = g.row_tiles * g.col_tiles, tile = (uint32_t)at % tiles;
-      Slice u;
-      u.expert = 0; u.lo = u.hi = 0; u.partial = -1;
-      find_slice(g, (uint32_t)at / tiles, -1, &u);
+      const Entry u = find_entry(g.plan, blockIdx.x % kXcds, (int)at);
+      const uint32_t tile = (uint32_t)(u.tile + (int)at - u.start);
       n.e = u.expert;
       n.r0 = u.lo;
       n.r1 = u.hi;
-      const int64_t part = uniform(u.partial);
-      n.dW = part >= 0 ? g.part + part * g.N * g.K : g.dW + uniform(n.e) * g.N * g.K;
+      const int64_t part = u.partial;
+      n.dW = part >= 0 ? g.part + part * g.N * g.K : g.dW + (int64_t)n.e * g.N * g.K;
       n.row0 = (int64_t)(tile / (uint32_t)g.col_tiles) * BM;
       n.n0 = (int)(tile % (uint32_t)g.col_tiles) * BN;
       n.end = g.N;
@@ -739,10 +785,26 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
     }
   };
 
-  // The next tile's first loads are issued before this tile's results are stored.
+  // The next tile's first loads are issued before this tile's results are stored.  A block
+  // takes every stride-th tile of its XCD's: of neighbouring tiles, which share operands, each
+  // XCD, with an L2 of its own, has a run; blocks go to the 8 XCDs in turn.
+  const int x = blockIdx.x % kXcds;
+  const int64_t stride = gridDim.x / kXcds, mine = blockIdx.x / kXcds;
   int64_t at, last;
-  const int64_t stride = gridDim.x / kXcds;
-  part_of<KIND, BM>(g, &at, &last);
+  if constexpr (KIND == kWeight) {
+    at = mine;
+    last = g.plan->tiles[x];
+  } else {
+    const int64_t total = uniform(count_tiles<BM>(g)) * g.col_tiles;
+    at = total * x / kXcds + mine;
+    last = total * (x + 1) / kXcds;
+  }
+  bool fro = false;
+  auto next = [&](int64_t i) {
+    if (KIND != kWeight) return i + stride;
+    fro = !fro;                                // from mine in one stride to its mirror in the next
+    return fro ? i + 2 * (stride - mine) - 1 : i + 2 * mine + 1;
+  };
   if (at >= last) return;
   Tile n = find(at);
   aim(n);
@@ -762,7 +824,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
         }
     }
     const Tile done = n;
-    at += stride;
+    at = next(at);
     if (at < last) {
       n = find(at);
       aim(n);
@@ -1271,6 +1333,8 @@ static hipError_t launch_wide(experts::Product g, hipStream_t s) {
   // as many blocks as run at once, or the tiles there can be
   const int64_t most = 256 * (BM == 256 ? 1 : 2);
   const int64_t grid = (blocks < most ? blocks : most) + kXcds - 1;
+  if constexpr (KIND == experts::kWeight)
+    experts::plan_kernel<<<1, experts::kPlanThreads, 0, s>>>(g, const_cast<experts::Plan*>(g.plan));
   const unsigned whole = (unsigned)(grid / kXcds * kXcds), threads = (BM / WM) * (BN / WN) * 64;
   if (KIND == experts::kWeight && g.order)
     experts::wide_kernel<TY, KIND, BM, BN, WM, WN, KIND == experts::kWeight>
@@ -1359,14 +1423,17 @@ static int64_t bias_slice(int64_t n) {
   return s < 256 ? 256 : s;
 }
 
+// The plan of the weight gradient's tiles, at the workspace's start.
+constexpr int64_t kPlanFloats = (sizeof(experts::Plan) + 255) / 256 * 64;
+
 size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtype) {
   experts::Product g = expert_product(nullptr, K, n, nullptr, 1, nullptr, n, E, K, nullptr, N);
   // arrays that are not in whole 16-byte pieces may take the other kernel, and its slices
   set_slices(g, false);
-  int64_t need = most_partials(g) * N * K;
+  int64_t need = most_partials(g) * N * K + kPlanFloats;
   if (dtype != kEltF32 && K % 8 == 0 && N % 8 == 0) {
     set_slices(g, true);
-    const int64_t wide = most_partials(g) * N * K;
+    const int64_t wide = most_partials(g) * N * K + kPlanFloats;
     need = wide > need ? wide : need;
   }
   // the bias gradient's sums come after the weight gradient's are joined
@@ -1397,9 +1464,10 @@ hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t
       experts::Product h = g;
       h.W = nullptr;
       h.dW = dW;
-      h.part = static_cast<float*>(workspace);
       const bool wide = wide_ok(h, dtype) && (reinterpret_cast<uintptr_t>(dW) & 15u) == 0;
       set_slices(h, wide);
+      h.plan = static_cast<const experts::Plan*>(workspace);
+      h.part = static_cast<float*>(workspace) + kPlanFloats;
       e = launch_product<TY, experts::kWeight>(h, wide, s);
       if (e == hipSuccess && n > h.slice) {
         const int64_t each = ((int64_t)N * K + experts::kJoin - 1) / experts::kJoin;
