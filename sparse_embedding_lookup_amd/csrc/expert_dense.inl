@@ -174,28 +174,29 @@ __device__ __forceinline__ bool find_slice(const Product& g, int64_t unit, int e
 }
 
 // The weight gradient's tiles are as long as their expert has rows, which differ widely.  One
-// block lays out who takes which before the product: a unit's tiles in entries of at most 32
+// block lays out who takes which before the product: a unit's tiles in entries of about kNear
 // neighbours, the entries sorted by the length of their tiles and dealt to the XCDs like cards,
 // largest first, back and forth.  An XCD's blocks walk its tiles in strides to and fro, so that
 // who begins with the longest tile ends with the shortest.  (Runs of tiles of equal cost an
-// XCD, unsorted: dW of 16384 rows in 16 uneven experts of 1024 x 1024 ... us for ... us.)
+// XCD, unsorted: dW of 16384 rows in 8 uneven experts of 2048 x 2048 175 us for 142 us.)
 struct Entry {
   int32_t start;                // the entry's first tile in the XCD's order
   int32_t expert, lo, hi, partial;
   int32_t tile;                 // its first tile of the unit's
   int32_t pad[2];
 };
-constexpr int kEntries = 2048, kPlanThreads = 1024;
+constexpr int kEntries = 2048, kPlanThreads = 1024, kNear = 32;
 struct Plan {
   int32_t tiles[8], count[8];   // of each XCD
   Entry entry[8][kEntries / 8];
 };
 
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(Product g, Plan* plan) {
-  __shared__ int32_t units_to[kPlanThreads], partials_to[kPlanThreads];
-  __shared__ int32_t wave_sum[2][16], rounds[kEntries], many[8][kEntries / 8];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  int64_t lo, hi;
+  __shared__ int32_t units_to[kPlanThreads], partials_to[kPlanThreads];
+  __shared__ int32_t begin[kPlanThreads], stop[kPlanThreads];
+  __shared__ int32_t wave_sum[2][16], rounds[kEntries], many[8][kEntries / 8];
+  int64_t lo = 0, hi = 0;
   const int c = t < g.E ? slices_of(g, t, &lo, &hi) : 0, m = c > 1 ? c : 0;
   int upto = c, mupto = m;
   for (int d = 1; d < 64; d <<= 1) {
@@ -209,8 +210,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(Product g, Plan* pla
     wave_sum[0][w] = upto;
     wave_sum[1][w] = mupto;
   }
+  begin[t] = (int32_t)lo;
+  stop[t] = (int32_t)hi;
   __syncthreads();
   int units = 0;
+#pragma unroll
   for (int i = 0; i < 16; ++i) {
     if (i < w) {
       upto += wave_sum[0][i];
@@ -221,40 +225,47 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(Product g, Plan* pla
   units_to[t] = upto;
   partials_to[t] = mupto;
   const int tiles = g.row_tiles * g.col_tiles;
-  int parts = (tiles + 31) / 32, least = (2 * (int)kXcds + units - 1) / units;
+  int parts = (tiles + kNear - 1) / kNear, least = (2 * (int)kXcds + units - 1) / units;
   parts = parts > least ? parts : least;
   parts = parts < tiles ? parts : tiles;
   parts = parts < kEntries / units ? parts : kEntries / units;
   const int entries = units * parts;           // set_slices keeps the units below kEntries
+  int top = kPlanThreads;                      // the experts, to a power of two
+  while (top / 2 >= g.E) top >>= 1;
   __syncthreads();
-  auto of = [&](int j, Entry* x) {             // entry j, units in order; its tiles' number
+  Entry x[kEntries / kPlanThreads];            // entry t and, if there are so many, t + 1024
+  int size[kEntries / kPlanThreads];
+#pragma unroll
+  for (int i = 0; i < kEntries / kPlanThreads; ++i) {
+    const int j = t + i * kPlanThreads;
+    if (j >= entries) continue;
     const int u = j / parts, p = j % parts;
     int e = 0;
-    for (int d = kPlanThreads / 2; d > 0; d >>= 1)
+    for (int d = top / 2; d > 0; d >>= 1)
       if (units_to[e + d - 1] <= u) e += d;
-    int64_t elo, ehi;
-    const int n = slices_of(g, e, &elo, &ehi), i = u - (units_to[e] - n);
-    x->expert = e;
-    x->lo = (int32_t)(elo + i * g.slice);
-    x->hi = (int32_t)(ehi - x->lo < g.slice ? ehi : x->lo + g.slice);
-    x->partial = n > 1 ? partials_to[e] - n + i : -1;
-    x->tile = tiles * p / parts;
-    return tiles * (p + 1) / parts - x->tile;
-  };
-  Entry x{};
-  for (int j = t; j < entries; j += kPlanThreads) {
-    of(j, &x);
-    rounds[j] = (x.hi - x.lo + 63) / 64;
+    const int before = e > 0 ? units_to[e - 1] : 0, n = units_to[e] - before;
+    x[i].start = 0;
+    x[i].expert = e;
+    x[i].lo = (int32_t)(begin[e] + (u - before) * g.slice);
+    x[i].hi = stop[e] - x[i].lo < g.slice ? stop[e] : (int32_t)(x[i].lo + g.slice);
+    x[i].partial = n > 1 ? partials_to[e] - n + u - before : -1;
+    x[i].tile = tiles * p / parts;
+    size[i] = tiles * (p + 1) / parts - x[i].tile;
+    rounds[j] = (x[i].hi - x[i].lo + 63) / 64;
   }
   __syncthreads();
-  for (int j = t; j < entries; j += kPlanThreads) {
+#pragma unroll
+  for (int i = 0; i < kEntries / kPlanThreads; ++i) {
+    const int j = t + i * kPlanThreads;
+    if (j >= entries) continue;
     const int mine = rounds[j];
     int rank = 0;
-    for (int i = 0; i < entries; ++i) rank += rounds[i] > mine || (rounds[i] == mine && i < j);
+#pragma unroll 8
+    for (int o = 0; o < entries; ++o) rank += rounds[o] > mine || (rounds[o] == mine && o < j);
     const int at = rank / (int)kXcds, in = rank % (int)kXcds;
     const int xcd = at & 1 ? (int)kXcds - 1 - in : in;
-    many[xcd][at] = of(j, &x);
-    plan->entry[xcd][at] = x;                  // without its start
+    many[xcd][at] = size[i];
+    plan->entry[xcd][at] = x[i];               // without its start
   }
   __syncthreads();
   if (w < (int)kXcds) {                        // wave w: the starts of XCD w's entries
@@ -1387,14 +1398,17 @@ static hipError_t launch_product(experts::Product g, bool wide, hipStream_t s) {
 }
 
 // Positions a slice of the weight gradient's reduction.  Where every expert once around gives
-// the compute units a tile each, only experts of more than twice the mean rows are cut: a
-// slice more costs writing and reading N K sums (16384 rows, 16 experts of 1024 x 1024: 116 us
-// with slices of 1024, 111 us with 2048).  Else as many slices as fill the chip.
+// the compute units a tile each, only experts well above the mean rows are cut, for a slice
+// more costs writing and reading N K sums: above twice the mean, or, where there are fewer than
+// two tiles a compute unit, one and a half (product and join of 16384 rows in 16 uneven experts
+// of 1024 x 1024, 256 tiles: 96 us with twice, 81 us; 8 experts of 2048 x 2048, 512 tiles: 147
+// and 161 us).  Else as many slices as fill the chip.
 static void set_slices(experts::Product& g, bool wide) {
   auto across = [&](int64_t t) { return (g.N + t - 1) / t * ((g.K + t - 1) / t); };
   g.big = across(256) * g.E >= 256;
   const int64_t tiles = across(wide ? (g.big ? 256 : 128) : 64);
-  int64_t slice = tiles * g.E >= 256 ? 2 * g.n / g.E : g.n * tiles / 512;
+  int64_t slice = tiles * g.E >= 512 ? 2 * g.n / g.E
+                  : tiles * g.E >= 256 ? 3 * g.n / (2 * g.E) : g.n * tiles / 512;
   slice = slice < 512 ? 512 : slice;
   g.slice = (slice + 63) / 64 * 64;
 }
