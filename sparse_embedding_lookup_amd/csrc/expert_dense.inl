@@ -352,7 +352,7 @@ __device__ __forceinline__ uint32_t keep_positive(uint32_t h, uint32_t m) {
 // 16-byte aligned arrays).  A block has a BM x BN output tile and a wave a WM x WN part of it
 // in 32 x 32 matrix-core tiles.  The reduction advances in rounds of 64 values, so that a row
 // is read 128 bytes at a time (half of that costs the first-level cache twice the requests,
-// and the forward product 729 us instead of ... at 65536 x 2208 x 2048).  Tiles go from
+// and the forward product 729 us instead of 603 at 65536 x 2208 x 2048).  Tiles go from
 // memory to LDS directly (one 16-byte load a lane, 1 KB a wave, no registers in between); the
 // loads' own bounds check gives zeros for rows and reduction values that are not there.
 //

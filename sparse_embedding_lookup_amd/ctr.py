@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from array import array
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -203,6 +204,7 @@ class Call:
         self.args = args
         self.result = result
         self.keep = keep                  # a workspace that the binding allocated for the call
+                                          # (and host arrays that the library reads)
 
     def __call__(self, stream=None):
         st = self.fn(*self.args, _stream(stream))
@@ -647,8 +649,9 @@ def _launch(name: str, device: torch.device, args: tuple, stream, prepare: bool,
     if stream is not None and not prepare:
         # what the binding allocated belongs to the current stream: its memory is not reused
         # there before this stream's work is done
-        for t in (result if isinstance(result, tuple) else (result,)) + (keep,):
-            if t is not None:
+        for t in (result if isinstance(result, tuple) else (result,)) + (
+                keep if isinstance(keep, tuple) else (keep,)):
+            if isinstance(t, torch.Tensor):
                 t.record_stream(stream)
     return got
 
@@ -783,7 +786,7 @@ def ctr_expert_sort(experts: torch.Tensor, num_experts: int,
     args = (_expert_arg(experts, "experts", (T, k), torch.int32, dev), T, k, num_experts, fp, sp,
             op, workspace.data_ptr(), ctypes.byref(wsb))
     return _launch("ctr_expert_sort", dev, args, stream, prepare, (offsets, slots, order),
-                workspace)
+                   workspace)
 
 
 def _slot_args(slots: torch.Tensor, offsets: Optional[torch.Tensor], dev):
@@ -924,8 +927,8 @@ def ctr_expert_dense_bwd(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor
     args = first + (N, int(bool(x_relu)), yp, dys, xp, dxs, wp, bp, workspace.data_ptr(),
                     ctypes.byref(wsb))
     return _launch("ctr_expert_dense_bwd", dev, args, stream, prepare,
-                (dX if want_dx else None, dW if want_dw else None, db if bias else None),
-                workspace)
+                   (dX if want_dx else None, dW if want_dw else None, db if bias else None),
+                   workspace)
 
 
 # --------------------------------------------------------------------- gradient clipping
@@ -939,25 +942,25 @@ def grad_clip_workspace_bytes(num: int) -> int:
 
 
 def _tensor_list(ts, name: str, device: torch.device, sizes=None, dtypes=None):
-    """A host array of the addresses of contiguous tensors on one device, and their element
-    counts and types."""
+    """Addresses, element counts and types of contiguous tensors on one device."""
     at = -1 if device.type == "cpu" else device.index
     codes = [_DTYPE_CODES.get(t.dtype) for t in ts]
     if None in codes:
         i = codes.index(None)
         raise TypeError("%s[%d] must be float32, bfloat16 or float16, not %s"
                         % (name, i, ts[i].dtype))
-    for i, t in enumerate(ts):
-        if not t.is_contiguous():
-            raise ValueError("%s[%d] must be contiguous" % (name, i))
-        if t.get_device() != at:
-            raise ValueError("%s[%d] is on %s, not %s" % (name, i, t.device, device))
+    if not all([t.is_contiguous() and t.get_device() == at for t in ts]):
+        for i, t in enumerate(ts):
+            if not t.is_contiguous():
+                raise ValueError("%s[%d] must be contiguous" % (name, i))
+            if t.get_device() != at:
+                raise ValueError("%s[%d] is on %s, not %s" % (name, i, t.device, device))
     counts = [t.numel() for t in ts]
     if sizes is not None and counts != sizes:
         raise ValueError("%s and grads differ in number or sizes" % name)
     if dtypes is not None and codes != dtypes:
         raise TypeError("%s and grads differ in type" % name)
-    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts]), counts, codes
+    return [t.data_ptr() for t in ts], counts, codes
 
 
 def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepare, out_name):
@@ -965,22 +968,25 @@ def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepar
     if not grads:
         raise ValueError("no gradients")
     dev = grads[0].device
-    gp, counts, codes = _tensor_list(grads, "grads", dev)
+    ptrs, counts, codes = _tensor_list(grads, "grads", dev)
     num = len(grads)
-    if stats is None:
-        stats = torch.empty(2, dtype=torch.float32, device=dev)
-    sp = _expert_arg(stats, "stats", (2,), torch.float32, dev)
+    stats, sp = _dense(stats, "stats", (2,), (1,), torch.float32, dev)
     if workspace is None:
         workspace = _workspace(grad_clip_workspace_bytes(num), dev)
     wsb = ctypes.c_size_t(workspace.numel())
-    head = (num, gp, (ctypes.c_int64 * num)(*counts), (ctypes.c_int32 * num)(*codes))
-    tail = (float(max_norm), sp, workspace.data_ptr(), ctypes.byref(wsb))
-    if lr is None:
-        op = None if outs is None else _tensor_list(list(outs), out_name, dev, counts, codes)[0]
-        return _launch(name, dev, head + (op,) + tail, stream, prepare, stats, workspace)
-    pp, _, pcodes = _tensor_list(list(outs), out_name, dev, counts)
-    return _launch(name, dev, head + (pp, (ctypes.c_int32 * num)(*pcodes), float(lr)) + tail,
-                   stream, prepare, stats, workspace)
+    host = [array("Q", ptrs), array("q", counts), array("i", codes)]
+    if outs is not None:
+        optrs, _, ocodes = _tensor_list(list(outs), out_name, dev, counts,
+                                        codes if lr is None else None)
+        host.append(array("Q", optrs))
+        if lr is not None:
+            host += [array("i", ocodes)]
+    at = [h.buffer_info()[0] for h in host]
+    if outs is None:
+        at.append(None)
+    args = (num, *at) + (() if lr is None else (float(lr),)) + (
+        float(max_norm), sp, workspace.data_ptr(), ctypes.byref(wsb))
+    return _launch(name, dev, args, stream, prepare, stats, (workspace, host))
 
 
 def ctr_grad_clip(grads: Sequence[torch.Tensor], max_norm: float,
