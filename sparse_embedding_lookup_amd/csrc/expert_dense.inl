@@ -313,34 +313,6 @@ __device__ __forceinline__ f32x4 load4(const float* p) {
 }
 __device__ __forceinline__ void store4(float* p, f32x4 x) { __builtin_memcpy(p, &x, 16); }
 
-// dW of the experts with several slices: their partial sums added in order.  A block has
-// kJoin elements of one expert.
-constexpr int kJoin = 16 * kThreads;
-__global__ __launch_bounds__(kThreads) void join_kernel(Product g) {
-  const int64_t count = (int64_t)g.N * g.K;
-  const int64_t each = (count + kJoin - 1) / kJoin;
-  const int e = (int)(blockIdx.x / each);
-  Slice u;
-  if (!find_slice(g, 0, e, &u) || u.count < 2) return;
-  const float* part = g.part + u.partial * count;
-  float* out = g.dW + e * count;
-  int64_t i = (blockIdx.x % each) * kJoin + threadIdx.x * 4;
-#pragma unroll
-  for (int q = 0; q < kJoin / (4 * kThreads); ++q, i += 4 * kThreads) {
-    if (i + 4 <= count) {
-      f32x4 s = load4(part + i);
-      for (int z = 1; z < u.count; ++z) s += load4(part + z * count + i);
-      store4(out + i, s);
-    } else {
-      for (int64_t j = i; j < count; ++j) {
-        float s = part[j];
-        for (int z = 1; z < u.count; ++z) s += part[z * count + j];
-        out[j] = s;
-      }
-    }
-  }
-}
-
 // The 16-bit values of h where those of m are positive, else zero.
 template <int TY>
 __device__ __forceinline__ uint32_t keep_positive(uint32_t h, uint32_t m) {
@@ -1241,7 +1213,7 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Product g) {
 
 // db[e, c] = sum of dY over the expert's rows.  Like the weight gradient's reduction it is cut
 // into slices (of g.slice rows here), which write db itself or, where an expert has several,
-// partial sums [unit, N] that bias_join_kernel adds in order.  A block has one slice and
+// partial sums [unit, N] that join_kernel adds in order.  A block has one slice and
 // LR lanes along the columns, VW columns each, times 256 / LR rows, four of them in flight.  Bound by reading dY once.
 template <int TY, int VW>
 __global__ __launch_bounds__(kThreads) void bias_grad_kernel(Product g, int LR,
@@ -1287,15 +1259,52 @@ __global__ __launch_bounds__(kThreads) void bias_grad_kernel(Product g, int LR,
   for (int e = 0; e < VW; ++e) out[c + e] = red[t * VW + e];
 }
 
-__global__ __launch_bounds__(kThreads) void bias_join_kernel(Product g, float* __restrict__ db) {
-  const int e = (int)(blockIdx.x / g.col_tiles);
-  const int c = (int)(blockIdx.x % g.col_tiles) * kThreads + threadIdx.x;
+// The gradients of the experts with several slices: their partial sums added in order.  The
+// first dw_blocks blocks have kJoin elements of one expert's dW each, the others kThreads of one
+// expert's db, whose slices (those of h) are shorter.  Bound by reading the partial sums.
+constexpr int kJoin = 16 * kThreads;
+__global__ __launch_bounds__(kThreads) void join_kernel(Product g, Product h, int64_t dw_blocks,
+                                                        float* __restrict__ db) {
   Slice u;
-  if (!find_slice(g, 0, e, &u) || u.count < 2 || c >= g.N) return;
-  const float* part = g.part + u.partial * g.N + c;
-  float s = part[0];
-  for (int z = 1; z < u.count; ++z) s += part[(int64_t)z * g.N];
-  db[(int64_t)e * g.N + c] = s;
+  if (blockIdx.x >= dw_blocks) {
+    const int64_t at = blockIdx.x - dw_blocks;
+    const int e = (int)(at / h.col_tiles), c = (int)(at % h.col_tiles) * kThreads + threadIdx.x;
+    if (!find_slice(h, 0, e, &u) || u.count < 2 || c >= h.N) return;
+    const float* part = h.part + u.partial * h.N + c;
+    float s = 0.f;
+    int z = 0;
+    for (; z + 8 <= u.count; z += 8) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = part[(int64_t)(z + i) * h.N];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[i];
+    }
+    for (; z < u.count; ++z) s += part[(int64_t)z * h.N];
+    db[(int64_t)e * h.N + c] = s;
+    return;
+  }
+  const int64_t count = (int64_t)g.N * g.K;
+  const int64_t each = (count + kJoin - 1) / kJoin;
+  const int e = (int)(blockIdx.x / each);
+  if (!find_slice(g, 0, e, &u) || u.count < 2) return;
+  const float* part = g.part + u.partial * count;
+  float* out = g.dW + e * count;
+  int64_t i = (blockIdx.x % each) * kJoin + threadIdx.x * 4;
+#pragma unroll
+  for (int q = 0; q < kJoin / (4 * kThreads); ++q, i += 4 * kThreads) {
+    if (i + 4 <= count) {
+      f32x4 s = load4(part + i);
+      for (int z = 1; z < u.count; ++z) s += load4(part + z * count + i);
+      store4(out + i, s);
+    } else {
+      for (int64_t j = i; j < count; ++j) {
+        float s = part[j];
+        for (int z = 1; z < u.count; ++z) s += part[z * count + j];
+        out[j] = s;
+      }
+    }
+  }
 }
 
 }  // namespace experts
@@ -1450,10 +1459,8 @@ size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtyp
     const int64_t wide = most_partials(g) * N * K + kPlanFloats;
     need = wide > need ? wide : need;
   }
-  // the bias gradient's sums come after the weight gradient's are joined
   g.slice = bias_slice(n);
-  const int64_t bias = most_partials(g) * N;
-  return (size_t)(need > bias ? need : bias) * sizeof(float) + 256;
+  return (size_t)(need + most_partials(g) * N) * sizeof(float) + 256;
 }
 
 hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t x_rows,
@@ -1474,37 +1481,40 @@ hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t
       h.Y = dX; h.ys = dxs;
       e = launch_product<TY, experts::kInput>(h, wide_ok(h, dtype), s);
     }
+    // partial sums: the weight gradient's, then the bias gradient's
+    float* part = static_cast<float*>(workspace) + kPlanFloats;
+    experts::Product h = g, f = g;
+    int64_t dw_blocks = 0, db_blocks = 0;
     if (e == hipSuccess && dW) {
-      experts::Product h = g;
       h.W = nullptr;
       h.dW = dW;
       const bool wide = wide_ok(h, dtype) && (reinterpret_cast<uintptr_t>(dW) & 15u) == 0;
       set_slices(h, wide);
       h.plan = static_cast<const experts::Plan*>(workspace);
-      h.part = static_cast<float*>(workspace) + kPlanFloats;
+      h.part = part;
+      part += most_partials(h) * N * K;
       e = launch_product<TY, experts::kWeight>(h, wide, s);
-      if (e == hipSuccess && n > h.slice) {
-        const int64_t each = ((int64_t)N * K + experts::kJoin - 1) / experts::kJoin;
-        experts::join_kernel<<<(unsigned)(E * each), experts::kThreads, 0, s>>>(h);
-        e = hipGetLastError();
-      }
+      if (n > h.slice) dw_blocks = E * (((int64_t)N * K + experts::kJoin - 1) / experts::kJoin);
     }
     if (e == hipSuccess && db) {
-      g.slice = bias_slice(n);
-      g.part = static_cast<float*>(workspace);
+      f.slice = bias_slice(n);
+      f.part = part;
       const int VW = TY == kEltF32 ? 4 : 8;
       const bool vec = rows::row_vec(dY, dys, N, TY == kEltF32 ? 4 : 2);
       const int LR = row_lanes(vec ? N / VW : N), wide = LR * (vec ? VW : 1);
-      g.col_tiles = (N + wide - 1) / wide;
-      const unsigned blocks = (unsigned)((n / g.slice + E) * g.col_tiles);
+      f.col_tiles = (N + wide - 1) / wide;
+      const unsigned blocks = (unsigned)((n / f.slice + E) * f.col_tiles);
       if (vec)
-        experts::bias_grad_kernel<TY, VW><<<blocks, experts::kThreads, 0, s>>>(g, LR, db);
+        experts::bias_grad_kernel<TY, VW><<<blocks, experts::kThreads, 0, s>>>(f, LR, db);
       else
-        experts::bias_grad_kernel<TY, 1><<<blocks, experts::kThreads, 0, s>>>(g, LR, db);
-      if (n > g.slice) {
-        g.col_tiles = (N + experts::kThreads - 1) / experts::kThreads;
-        experts::bias_join_kernel<<<(unsigned)(E * g.col_tiles), experts::kThreads, 0, s>>>(g, db);
-      }
+        experts::bias_grad_kernel<TY, 1><<<blocks, experts::kThreads, 0, s>>>(f, LR, db);
+      e = hipGetLastError();
+      f.col_tiles = (N + experts::kThreads - 1) / experts::kThreads;
+      if (n > f.slice) db_blocks = (int64_t)E * f.col_tiles;
+    }
+    if (e == hipSuccess && dw_blocks + db_blocks > 0) {
+      experts::join_kernel<<<(unsigned)(dw_blocks + db_blocks), experts::kThreads, 0, s>>>(
+          h, f, dw_blocks, db);
       e = hipGetLastError();
     }
     return e;
