@@ -14,10 +14,13 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------------------- router
 // G lanes (a power of two, at least k and at most 64) hold one row of E logits, V a lane:
-// lane l holds experts l, l + G, ...  The k largest are taken one at a time: each lane's best
+// lane l holds experts V l .. V l + V - 1, which it reads and writes together.  The k largest are taken one at a time: each lane's best
 // of what it has left, joined over the lanes by a butterfly that prefers the larger value
 // and, among equals, the lower expert; lane j keeps the j-th.  The softmax is relative to the
 // first value taken, the row's largest.  A logit that is -inf or NaN closes its expert.
+// Bound by the k rounds of dependent exchanges (forward 8.3 us, backward, which has one exchange,
+// 6.1 us at 65536 x 64 bf16, 4 experts; with exchanges through LDS and one logit a load 10.7 and
+// 7.1 us; their bytes are 2 us each).
 template <int TY>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
   if constexpr (TY == kEltF32) return static_cast<const float*>(p)[i];
@@ -36,6 +39,71 @@ __device__ __forceinline__ float exp_below(float x, float m) {
   return x == m ? 1.f : expf(x - m);
 }
 
+// Calls f(get) for every step of a butterfly over G lanes, get(v) the other lane's v: within 16
+// lanes by the data-parallel moves (the mirrors of 8 and 16 lanes do as steps of 4 and 8 where
+// all lanes of a group already hold the same), which take no trip through LDS.
+template <int CTRL>
+__device__ __forceinline__ int moved(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
+}
+template <typename F>
+__device__ __forceinline__ void butterfly(int G, F f) {
+  if (G > 1) f([](int v) { return moved<0xB1>(v); });          // quads 1 0 3 2
+  if (G > 2) f([](int v) { return moved<0x4E>(v); });          // quads 2 3 0 1
+  if (G > 4) f([](int v) { return moved<0x141>(v); });         // half rows mirrored
+  if (G > 8) f([](int v) { return moved<0x140>(v); });         // rows mirrored
+  if (G > 16) f([](int v) { return __shfl_xor(v, 16); });
+  if (G > 32) f([](int v) { return __shfl_xor(v, 32); });
+}
+__device__ __forceinline__ float group_sum(int G, float v) {
+  butterfly(G, [&](auto get) { v += __int_as_float(get(__float_as_int(v))); });
+  return v;
+}
+
+// A lane's V logits, those from n on as `none`; V of them at a row's place `first`.
+template <int TY, int V>
+__device__ __forceinline__ void load_lane(const void* row, int first, int n, float none, float* x) {
+  constexpr int SIZE = TY == kEltF32 ? 4 : 2;
+  if constexpr (V * SIZE >= 4) {
+    if (first + V <= n) {
+      uint32_t u[V * SIZE / 4];
+      __builtin_memcpy(u, static_cast<const char*>(row) + (int64_t)first * SIZE, sizeof(u));
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (TY == kEltF32) x[i] = __uint_as_float(u[i]);
+        else x[i] = i & 1 ? half_hi<TY>(u[i >> 1]) : half_lo<TY>(u[i >> 1]);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = first + i < n ? load1<TY>(row, first + i) : none;
+}
+template <int TY, int V>
+__device__ __forceinline__ void store_lane(void* row, int first, int n, const float* x) {
+  constexpr int SIZE = TY == kEltF32 ? 4 : 2;
+  if constexpr (V * SIZE >= 4) {
+    if (first + V <= n) {
+      uint32_t u[V * SIZE / 4];
+#pragma unroll
+      for (int i = 0; i < V * SIZE / 4; ++i) {
+        if constexpr (TY == kEltF32) u[i] = __float_as_uint(x[i]);
+        else u[i] = to_half<TY, false>(x[2 * i], 0u) | (to_half<TY, false>(x[2 * i + 1], 0u) << 16);
+      }
+      __builtin_memcpy(static_cast<char*>(row) + (int64_t)first * SIZE, u, sizeof(u));
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (first + i < n) store1<TY>(row, first + i, x[i]);
+}
+// Row t of a matrix of element type TY and row stride s.
+template <int TY>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t t, int64_t s) {
+  return static_cast<const char*>(p) + t * s * (TY == kEltF32 ? 4 : 2);
+}
+
 template <int TY, int V>
 __global__ __launch_bounds__(kThreads) void route_fwd_kernel(
     const void* __restrict__ logits, int64_t ls, int64_t T, int E, int k, int G, int renorm,
@@ -44,12 +112,9 @@ __global__ __launch_bounds__(kThreads) void route_fwd_kernel(
   const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G;
   const bool row = t < T;
   float x[V];
+  load_lane<TY, V>(row_of<TY>(logits, t, ls), l * V, row ? E : 0, ninf(), x);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = l + i * G;
-    x[i] = row && e < E ? load1<TY>(logits, t * ls + e) : ninf();
-    x[i] = x[i] > ninf() ? x[i] : ninf();          // NaN too
-  }
+  for (int i = 0; i < V; ++i) x[i] = x[i] > ninf() ? x[i] : ninf();      // NaN too
   float most = 0.f, total = 0.f, mine = ninf();
   int chosen = -1;
   for (int j = 0; j < k; ++j) {
@@ -59,22 +124,22 @@ __global__ __launch_bounds__(kThreads) void route_fwd_kernel(
     for (int i = 0; i < V; ++i)
       if (x[i] > best) {
         best = x[i];
-        at = l + i * G;
+        at = l * V + i;
       }
-    for (int d = 1; d < G; d <<= 1) {
-      const float v = __shfl_xor(best, d);
-      const int a = __shfl_xor(at, d);
+    butterfly(G, [&](auto get) {
+      const float v = __int_as_float(get(__float_as_int(best)));
+      const int a = get(at);
       if (v > best || (v == best && a < at)) {
         best = v;
         at = a;
       }
-    }
+    });
     if (j == 0) {
       most = best;
       if (!renorm) {
 #pragma unroll
         for (int i = 0; i < V; ++i) total += x[i] > ninf() ? exp_below(x[i], most) : 0.f;
-        for (int d = 1; d < G; d <<= 1) total += __shfl_xor(total, d);
+        total = group_sum(G, total);
       }
     }
     if (renorm && best > ninf()) total += exp_below(best, most);
@@ -84,7 +149,7 @@ __global__ __launch_bounds__(kThreads) void route_fwd_kernel(
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (l + i * G == at) x[i] = ninf();
+      if (l * V + i == at) x[i] = ninf();
   }
   if (row && l < k) {
     experts[t * k + l] = chosen;
@@ -113,27 +178,25 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(
       chosen = -1;
     }
   }
-  float s = w * dw;
-  for (int d = 1; d < G; d <<= 1) s += __shfl_xor(s, d);
+  const float s = group_sum(G, w * dw);
   float q[V], g[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) q[i] = g[i] = 0.f;
   if (!renorm) {
     float most = ninf(), total = 0.f;
+    load_lane<TY, V>(row_of<TY>(logits, t, ls), l * V, row ? E : 0, ninf(), q);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = l + i * G;
-      q[i] = row && e < E ? load1<TY>(logits, t * ls + e) : ninf();
       q[i] = q[i] > ninf() ? q[i] : ninf();
       most = fmaxf(most, q[i]);
     }
-    for (int d = 1; d < G; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+    butterfly(G, [&](auto get) { most = fmaxf(most, __int_as_float(get(__float_as_int(most)))); });
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       q[i] = q[i] > ninf() ? exp_below(q[i], most) : 0.f;
       total += q[i];
     }
-    for (int d = 1; d < G; d <<= 1) total += __shfl_xor(total, d);
+    total = group_sum(G, total);
     const float by = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) q[i] *= by;
@@ -144,17 +207,15 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(
     const float wj = __shfl(w, first + j), dj = __shfl(dw, first + j);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (l + i * G == e) {
+      if (l * V + i == e) {
         g[i] = dj;
         if (renorm) q[i] = wj;
       }
   }
   if (!row) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = l + i * G;
-    if (e < E) store1<TY>(dlogits, t * dls + e, q[i] * (g[i] - s));
-  }
+  for (int i = 0; i < V; ++i) q[i] *= g[i] - s;
+  store_lane<TY, V>(const_cast<void*>(row_of<TY>(dlogits, t, dls)), l * V, E, q);
 }
 
 // --------------------------------------------------------------------------------- sort
