@@ -827,7 +827,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void wide_kernel(Pro
 // matrix instruction takes two reduction values a lane pair: lanes 0 to 31 have values
 // 8 c + e and lanes 32 to 63 values 8 c + 4 + e of both operands, so that by rows a lane's
 // next four values are one 16-byte read.
-// 64 x 64 tiles where 128 x 128 would leave compute units without a tile.
+// 64 x 64 tiles where 128 x 128 would leave compute units without a tile.  Y, dX and dW of 4096
+// x 479 x 257 in binary32, 8 uneven experts: 28, 23 and 50 us, a third of the matrix rate that
+// this size leaves (350 tiles on 256 compute units).  Two sets of waves with every other round
+// each: 28, 28 and 43 us.
 template <int TY, int KIND, int BM>
 __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
   using T = typename std::conditional<TY == kEltF32, float, uint16_t>::type;
@@ -1047,8 +1050,7 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
     }
   };
   if (r0 < r1) {
-    // (Loads two rounds ahead give nothing: 64 x 64 tiles 29 us for 27 at 4096 x 479 x 257 in
-    // binary32.)
+    // (Loads two rounds ahead give nothing: 29 us for 28.)
     load(r0);
     put(0);
     __syncthreads();
@@ -1062,29 +1064,47 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
     multiply(buf);
   }
 
-  // acc[i][j][v]: row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part
+  // acc[i][j][v]: row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part.  The
+  // biases, or the input's values that decide over dX, are loaded together before they are
+  // needed, those past the last column from the last.
+  const bool biased = KIND == kForward && g.b && e < g.E, masked = KIND == kInput && g.relu && e < g.E;
 #pragma unroll
   for (int i = 0; i < TW; ++i) {
     const int64_t r = row0 + BM / 2 * wm + 32 * i + rl;
+    float with[TW][4][4];
+    bool open = false;
+    const int first = n0 + BM / 2 * wn + 4 * kg;
+    if (biased || masked) {
+      const int64_t xr = masked && r < end ? x_row(g, r) : -1;
+      open = xr >= 0;
+      const int64_t from = biased ? (int64_t)e * g.N : (open ? xr : 0) * g.xs;
+#pragma unroll
+      for (int j = 0; j < TW; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int c = first + 32 * j + 8 * q + v;
+            const int64_t at = from + (c < cols ? c : cols - 1);
+            with[j][q][v] = KIND == kForward ? g.b[at] : rows::load1<TY>(g.X, at);
+          }
+    }
     if (r >= end) continue;
-    const bool masked = KIND == kInput && g.relu && e < g.E;
-    const int64_t xr = masked ? x_row(g, r) : 0;
 #pragma unroll
     for (int j = 0; j < TW; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int c = n0 + BM / 2 * wn + 32 * j + 8 * q + 4 * kg;
+        const int c = first + 32 * j + 8 * q;
         if (c >= cols) continue;
         float x[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           x[v] = acc[i][j][4 * q + v];
-          if (c + v >= cols) continue;
           if constexpr (KIND == kForward) {
-            if (g.b && e < g.E) x[v] += g.b[(int64_t)e * g.N + c + v];
+            if (biased) x[v] += with[j][q][v];
             if (g.relu) x[v] = x[v] > 0.f ? x[v] : 0.f;
           } else if constexpr (KIND == kInput) {
-            if (masked && !(xr >= 0 && rows::load1<TY>(g.X, xr * g.xs + c + v) > 0.f)) x[v] = 0.f;
+            if (masked && !(open && with[j][q][v] > 0.f)) x[v] = 0.f;
           }
         }
         if constexpr (KIND == kWeight || TY == kEltF32) {
@@ -1092,7 +1112,9 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
           if (c + 4 <= cols) {
             store4(out, f32x4{x[0], x[1], x[2], x[3]});
           } else {
-            for (int v = 0; v < cols - c; ++v) out[v] = x[v];
+#pragma unroll
+            for (int v = 0; v < 3; ++v)
+              if (c + v < cols) out[v] = x[v];
           }
         } else {
           uint16_t* out = static_cast<uint16_t*>(g.Y) + r * g.ys + c;

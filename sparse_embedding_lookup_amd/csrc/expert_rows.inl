@@ -14,9 +14,10 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------------------- router
 // G lanes (a power of two, at least k and at most 64) hold one row of E logits, V a lane:
-// lane l holds experts V l .. V l + V - 1, which it reads and writes together.  The k largest are taken one at a time: each lane's best
-// of what it has left, joined over the lanes by a butterfly that prefers the larger value
-// and, among equals, the lower expert; lane j keeps the j-th.  The softmax is relative to the
+// lane l holds experts V l .. V l + V - 1, which it reads and writes together.  The k largest
+// are taken one at a time: each lane's best of what it has left, joined over the lanes by a
+// butterfly that prefers the larger value and, among equals, the lower expert; lane j keeps the
+// j-th.  The softmax is relative to the
 // first value taken, the row's largest.  A logit that is -inf or NaN closes its expert.
 // Bound by the k rounds of dependent exchanges (forward 8.3 us, backward, which has one exchange,
 // 6.1 us at 65536 x 64 bf16, 4 experts; with exchanges through LDS and one logit a load 10.7 and
