@@ -37,6 +37,7 @@ struct Product {
   int64_t ys;
   float* dW;
   float* part;                  // partial sums of dW
+  int64_t most;                 // how many of them there is room for
   const struct Plan* plan;      // who takes which tile of dW
   int64_t slice;                // positions a slice of dW's reduction
   bool big;                     // dW in 256 x 256 tiles
@@ -138,7 +139,8 @@ __device__ __forceinline__ int64_t count_slices(const Product& g) {
   for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d);
   return c;
 }
-// Slice `unit` of all, or (expert >= 0) the first of that expert.
+// Slice `unit` of all, or (expert >= 0) the first of that expert.  false: no such slice, or no
+// room for its partial sums (or the expert's), which only offsets out of order can need.
 __device__ __forceinline__ bool find_slice(const Product& g, int64_t unit, int expert, Slice* u) {
   const int lane = threadIdx.x & 63;
   int64_t run = 0, partials = 0;
@@ -165,7 +167,7 @@ __device__ __forceinline__ bool find_slice(const Product& g, int64_t unit, int e
       u->lo = first + i * g.slice;
       u->hi = last < u->lo + g.slice ? last : u->lo + g.slice;
       u->partial = u->count > 1 ? partials + __shfl(mupto - m, at) + i : -1;
-      return true;
+      return u->count == 1 || u->partial + (expert >= 0 ? u->count : 1) <= g.most;
     }
     run += __shfl(upto, 63);
     partials += __shfl(mupto, 63);
@@ -248,7 +250,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(Product g, Plan* pla
     x[i].expert = e;
     x[i].lo = (int32_t)(begin[e] + (u - before) * g.slice);
     x[i].hi = stop[e] - x[i].lo < g.slice ? stop[e] : (int32_t)(x[i].lo + g.slice);
-    x[i].partial = n > 1 ? partials_to[e] - n + u - before : -1;
+    const int partial = partials_to[e] - n + u - before;
+    x[i].partial = n > 1 && partial < g.most ? partial : -1;   // all have room in ordered offsets
     x[i].tile = tiles * p / parts;
     size[i] = tiles * (p + 1) / parts - x[i].tile;
     rounds[j] = (x[i].hi - x[i].lo + 63) / 64;
@@ -1236,7 +1239,8 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Product g) {
 // db[e, c] = sum of dY over the expert's rows.  Like the weight gradient's reduction it is cut
 // into slices (of g.slice rows here), which write db itself or, where an expert has several,
 // partial sums [unit, N] that join_kernel adds in order.  A block has one slice and
-// LR lanes along the columns, VW columns each, times 256 / LR rows, four of them in flight.  Bound by reading dY once.
+// LR lanes along the columns, VW columns each, times 256 / LR rows, four of them in flight.
+// Bound by reading dY once.
 template <int TY, int VW>
 __global__ __launch_bounds__(kThreads) void bias_grad_kernel(Product g, int LR,
                                                              float* __restrict__ db) {
@@ -1428,6 +1432,12 @@ static hipError_t launch_product(experts::Product g, bool wide, hipStream_t s) {
   return hipGetLastError();
 }
 
+static int64_t most_partials(const experts::Product& g) {
+  // experts with several slices have more than `slice` rows each
+  const int64_t a = 2 * (g.n / g.slice), b = g.n / g.slice + g.E;
+  return a < b ? a : b;
+}
+
 // Positions a slice of the weight gradient's reduction.  Where every expert once around gives
 // the compute units a tile each, only experts well above the mean rows are cut, for a slice
 // more costs writing and reading N K sums: above twice the mean, or, where there are fewer than
@@ -1442,12 +1452,7 @@ static void set_slices(experts::Product& g, bool wide) {
                   : tiles * g.E >= 256 ? 3 * g.n / (2 * g.E) : g.n * tiles / 512;
   slice = slice < 512 ? 512 : slice;
   g.slice = (slice + 63) / 64 * 64;
-}
-
-static int64_t most_partials(const experts::Product& g) {
-  // experts with several slices have more than `slice` rows each
-  const int64_t a = 2 * (g.n / g.slice), b = g.n / g.slice + g.E;
-  return a < b ? a : b;
+  g.most = most_partials(g);
 }
 
 hipError_t launch_expert_dense_fwd(const void* X, int dtype, int64_t xs, int64_t x_rows,
@@ -1475,10 +1480,10 @@ size_t expert_dense_bwd_workspace_bytes(int64_t n, int E, int K, int N, int dtyp
   experts::Product g = expert_product(nullptr, K, n, nullptr, 1, nullptr, n, E, K, nullptr, N);
   // arrays that are not in whole 16-byte pieces may take the other kernel, and its slices
   set_slices(g, false);
-  int64_t need = most_partials(g) * N * K + kPlanFloats;
+  int64_t need = g.most * N * K + kPlanFloats;
   if (dtype != kEltF32 && K % 8 == 0 && N % 8 == 0) {
     set_slices(g, true);
-    const int64_t wide = most_partials(g) * N * K + kPlanFloats;
+    const int64_t wide = g.most * N * K + kPlanFloats;
     need = wide > need ? wide : need;
   }
   g.slice = bias_slice(n);
@@ -1514,12 +1519,13 @@ hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t
       set_slices(h, wide);
       h.plan = static_cast<const experts::Plan*>(workspace);
       h.part = part;
-      part += most_partials(h) * N * K;
+      part += h.most * N * K;
       e = launch_product<TY, experts::kWeight>(h, wide, s);
       if (n > h.slice) dw_blocks = E * (((int64_t)N * K + experts::kJoin - 1) / experts::kJoin);
     }
     if (e == hipSuccess && db) {
       f.slice = bias_slice(n);
+      f.most = most_partials(f);
       f.part = part;
       const int VW = TY == kEltF32 ? 4 : 8;
       const bool vec = rows::row_vec(dY, dys, N, TY == kEltF32 ? 4 : 2);

@@ -590,9 +590,9 @@ inline bool row_vec(const void* p, int64_t stride, int D, int elem) {
 
 }  // namespace rows
 
-// Logits a lane holds: the smallest of 1, 2, 4, 8, 16 that lets 64 lanes hold a row, or more
-// where that leaves lanes to rows that the k rounds of the butterfly would otherwise need.
-static int route_values(int E, int k) {
+// Logits a lane holds: up to 8, as a lane's own comparisons cost less than a step of the
+// butterfly, and 16 where 64 lanes of 8 do not hold a row.
+static int route_values(int E) {
   int V = E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8;
   while (V * 64 < E) V *= 2;
   return V;
@@ -624,7 +624,7 @@ hipError_t launch_expert_route_fwd(const void* logits, int dtype, int64_t ls, in
                                    int k, bool renorm, int32_t* experts, float* weights,
                                    hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const int V = route_values(E, k), G = route_group(E, k, V);
+  const int V = route_values(E), G = route_group(E, k, V);
   const unsigned blocks = (unsigned)((T * G + rows::kThreads - 1) / rows::kThreads);
   return by_type(dtype, [&](auto ty) {
     return by_values(V, [&](auto v) {
@@ -640,7 +640,7 @@ hipError_t launch_expert_route_bwd(const void* logits, int dtype, int64_t ls, in
                                    const float* weights, const float* dweights, void* dlogits,
                                    int64_t dls, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const int V = route_values(E, k), G = route_group(E, k, V);
+  const int V = route_values(E), G = route_group(E, k, V);
   const unsigned blocks = (unsigned)((T * G + rows::kThreads - 1) / rows::kThreads);
   return by_type(dtype, [&](auto ty) {
     return by_values(V, [&](auto v) {

@@ -197,3 +197,25 @@ def test_gpu_tensors_are_required():
         ctr.ctr_expert_route_fwd(torch.zeros(4, 8), 2)
     with pytest.raises(ValueError):
         ctr.ctr_grad_clip([torch.zeros(4)], 1.0)
+
+
+# offsets that are not ctr_expert_sort's: every second expert claims all rows
+@pytest.mark.parametrize("n,E,K,N,dtype", [(4096, 16, 64, 40, BF16), (4096, 16, 61, 33, BF16),
+                                           (2048, 64, 32, 24, F32), (16384, 8, 512, 512, F16)])
+def test_offsets_out_of_order_stay_inside(n, E, K, N, dtype):
+    say("out of order", n, E, K, N, dtype)
+    X = torch.ones(n, K, device=DEV, dtype=dtype)
+    dY = torch.ones(n, N, device=DEV, dtype=dtype)
+    W = torch.ones(E, N, K, device=DEV, dtype=dtype)
+    offsets = torch.tensor([0, n] * (E // 2) + [0], device=DEV, dtype=torch.int32)
+    size = ctr.expert_dense_bwd_workspace_bytes(n, E, K, N, ctr._dtype_code(X))
+    guard = 1 << 20
+    room = torch.full((size + guard,), 0x5A, device=DEV, dtype=torch.uint8)
+    ctr.ctr_expert_dense_bwd(X, W, offsets, dY, workspace=room[:size])
+    ctr.ctr_expert_dense_fwd(X, W, None, offsets, False)
+    torch.cuda.synchronize()
+    assert bool((room[size:] == 0x5A).all())
+    # and in order again, in the same workspace
+    offsets = torch.arange(E + 1, device=DEV, dtype=torch.int32) * (n // E)
+    _, dW, db = ctr.ctr_expert_dense_bwd(X, W, offsets, dY, workspace=room[:size])
+    assert bool((dW == n // E).all()) and bool((db == n // E).all())
