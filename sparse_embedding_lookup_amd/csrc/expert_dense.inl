@@ -1142,7 +1142,8 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
 // fourth 32 reduction values of them; weights and inputs go from memory to registers in the
 // form that the 16 x 16 matrix instruction takes (a lane 16 bytes of one row), eight loads of
 // weights in flight a wave, up to 64 rows of the expert against them.  The waves' sums are
-// added in order through LDS.
+// added in order through LDS.  (96 rows, 16 experts of 1024 x 1024: 11.5 us, of which about 5 are
+// the launch and the chain of loads before the weights'; eight waves a block 15.7 us.)
 constexpr int kFewRows = 64;
 template <int TY>
 __device__ __forceinline__ f32x4 mma16(s16x8 a, s16x8 b, f32x4 c) {
@@ -1240,7 +1241,9 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Product g) {
 // into slices (of g.slice rows here), which write db itself or, where an expert has several,
 // partial sums [unit, N] that join_kernel adds in order.  A block has one slice and
 // LR lanes along the columns, VW columns each, times 256 / LR rows, four of them in flight.
-// Bound by reading dY once.
+// Bound by reading dY once: 16384 x 1024 in 16 bits 11.4 us, 65536 x 2048 94 us after the weight
+// gradient's product, whose stores are still on their way to memory.  (In one launch with the
+// plan, in blocks of 1024 threads: 17.2 us for 11.4 + 5.9.)
 template <int TY, int VW>
 __global__ __launch_bounds__(kThreads) void bias_grad_kernel(Product g, int LR,
                                                              float* __restrict__ db) {
@@ -1287,7 +1290,8 @@ __global__ __launch_bounds__(kThreads) void bias_grad_kernel(Product g, int LR,
 
 // The gradients of the experts with several slices: their partial sums added in order.  The
 // first dw_blocks blocks have kJoin elements of one expert's dW each, the others kThreads of one
-// expert's db, whose slices (those of h) are shorter.  Bound by reading the partial sums.
+// expert's db, whose slices (those of h) are shorter.  Bound by reading the partial sums (16 uneven
+// experts of 1024 x 1024 13 us, 32 of 2208 x 2048 80 us).
 constexpr int kJoin = 16 * kThreads;
 __global__ __launch_bounds__(kThreads) void join_kernel(Product g, Product h, int64_t dw_blocks,
                                                         float* __restrict__ db) {
