@@ -10,6 +10,7 @@ import ctypes
 import functools
 import os
 from array import array
+from operator import attrgetter
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -942,25 +943,29 @@ def grad_clip_workspace_bytes(num: int) -> int:
 
 
 def _tensor_list(ts, name: str, device: torch.device, sizes=None, dtypes=None):
-    """Addresses, element counts and types of contiguous tensors on one device."""
+    """Addresses, element counts and types of contiguous tensors on one device.  (A property of
+    a tensor costs about 70 ns, five of them most of a call over hundreds of small tensors: each
+    is read once, by a map.)"""
     at = -1 if device.type == "cpu" else device.index
-    codes = [_DTYPE_CODES.get(t.dtype) for t in ts]
+    kinds = list(map(attrgetter("dtype"), ts))
+    codes = list(map(_DTYPE_CODES.get, kinds))
     if None in codes:
         i = codes.index(None)
         raise TypeError("%s[%d] must be float32, bfloat16 or float16, not %s"
-                        % (name, i, ts[i].dtype))
-    if not all([t.is_contiguous() and t.get_device() == at for t in ts]):
+                        % (name, i, kinds[i]))
+    if not all(map(torch.Tensor.is_contiguous, ts)) or \
+            set(map(torch.Tensor.get_device, ts)) - {at}:
         for i, t in enumerate(ts):
             if not t.is_contiguous():
                 raise ValueError("%s[%d] must be contiguous" % (name, i))
             if t.get_device() != at:
                 raise ValueError("%s[%d] is on %s, not %s" % (name, i, t.device, device))
-    counts = [t.numel() for t in ts]
+    counts = list(map(torch.Tensor.numel, ts))
     if sizes is not None and counts != sizes:
         raise ValueError("%s and grads differ in number or sizes" % name)
     if dtypes is not None and codes != dtypes:
         raise TypeError("%s and grads differ in type" % name)
-    return [t.data_ptr() for t in ts], counts, codes
+    return list(map(torch.Tensor.data_ptr, ts)), counts, codes
 
 
 def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepare, out_name):
