@@ -30,6 +30,7 @@
 // tiles are too few to fill the chip, the reduction is split over grid.z into fp32 partials
 // that a second pass sums in a fixed order before the update (deterministic, no atomics).
 #include "ctr_internal.h"
+#include "expert_access.h"
 
 #include <type_traits>
 

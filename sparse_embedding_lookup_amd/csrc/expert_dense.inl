@@ -1532,7 +1532,7 @@ hipError_t launch_expert_dense_bwd(const void* X, int dtype, int64_t xs, int64_t
       f.most = most_partials(f);
       f.part = part;
       const int VW = TY == kEltF32 ? 4 : 8;
-      const bool vec = rows::row_vec(dY, dys, N, TY == kEltF32 ? 4 : 2);
+      const bool vec = whole_pieces(reinterpret_cast<uintptr_t>(dY), dys, N, TY == kEltF32 ? 4 : 2);
       const int LR = row_lanes(vec ? N / VW : N), wide = LR * (vec ? VW : 1);
       f.col_tiles = (N + wide - 1) / wide;
       const unsigned blocks = (unsigned)((n / f.slice + E) * f.col_tiles);

@@ -587,11 +587,6 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(RowArgs a) {
   zero_tail<TY>(a, t, l);
 }
 
-inline bool row_vec(const void* p, int64_t stride, int D, int elem) {
-  return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * elem % 16 == 0 &&
-                (int64_t)D * elem % 16 == 0);
-}
-
 }  // namespace rows
 
 // Logits a lane holds: up to 8, as a lane's own comparisons cost less than a step of the

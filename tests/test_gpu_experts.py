@@ -493,3 +493,25 @@ def test_grad_clip_mixed_types():
     for a, b in zip(outs, grads):
         want = b.cpu().double() / 2
         assert_near(a, want, stored(want, 6 * U32 * want.abs(), b.dtype), "mixed")
+
+
+# ------------------------------------------------------------------- nothing beside an output
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [1, 33, 64, 257])
+def test_gradients_of_no_rows_stay_in_their_arrays(N, dtype):
+    """Without rows dW and db are zero, and what lies beside them in one buffer is kept."""
+    say("no rows", N, dtype)
+    E, K = 8, 24
+    X, dY = (torch.empty((0, c), dtype=dtype, device=DEV) for c in (K, N))
+    W = torch.ones((E, N, K), dtype=dtype, device=DEV)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    for shift in (64, 65):                  # aligned and not
+        flat = torch.full((E * N * K + E * N + 256,), 7.0, device=DEV)
+        dW = flat[shift:shift + E * N * K].view(E, N, K)
+        at = shift + E * N * K + 64
+        db = flat[at:at + E * N].view(E, N)
+        dX, _, _ = ctr.ctr_expert_dense_bwd(X, W, offsets, dY, dW=dW, db=db)
+        assert dX.shape == (0, K) and (dW == 0).all() and (db == 0).all()
+        dW.fill_(7.0)
+        db.fill_(7.0)
+        assert (flat == 7).all()
