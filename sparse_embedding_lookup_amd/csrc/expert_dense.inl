@@ -887,18 +887,15 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
   Piece a[PIECES], b[PIECES];
   const int kp = (t & 7) * PE, kr = t / ACROSS, c = t % ACROSS * PE;
   constexpr int STEP = kThreads / ACROSS;                      // reduction rows from q to q + 1
-  // A whole round reads whole pieces.  Rows and columns past the tile's last are not stored,
-  // so any in their place will do: rows the tile's first, and a column piece that is partly
-  // there the row's last whole one, moved down (by `down` elements) to where it belongs.
+  // A whole round reads whole pieces, all inside their rows.  Rows and columns past the tile's
+  // last are not stored, so any in their place will do: rows the tile's first, and a column piece
+  // that is not all there the row's last whole one, moved down (by `down` elements) to where it
+  // belongs if part of it is.
   const int64_t atop = AROW ? end - row0 : end, btop = cols;
-  auto column = [&](int64_t first, int64_t top, int* down) -> int64_t {
-    const int64_t at = first + c;
-    *down = at < top && at + PE > top ? (int)(at + PE - top) : 0;
-    return at < top ? at - *down : first;
-  };
-  int adown = 0, bdown = 0;
-  const int64_t acol = AROW ? 0 : column(row0, atop, &adown);
-  const int64_t bcol = BROW ? 0 : column(n0, btop, &bdown);
+  const PieceAt ap = AROW ? PieceAt{0, 0} : piece_at(row0 + c, atop, PE);
+  const PieceAt bp = BROW ? PieceAt{0, 0} : piece_at(n0 + c, btop, PE);
+  const int64_t acol = ap.column, bcol = bp.column;
+  const int adown = ap.down, bdown = bp.down;
   const bool aedge = !AROW && row0 + BM > atop, bedge = !BROW && n0 + BM > btop;
   const bool narrow = (!AROW && atop < PE) || (!BROW && btop < PE);
   auto moved = [](Piece x, int down) {

@@ -14,6 +14,11 @@ SOURCE = """
 extern "C" int whole(uint64_t p, int64_t stride, int64_t width, int size) {
   return ctr::whole_pieces((uintptr_t)p, stride, width, size);
 }
+extern "C" int64_t piece(int64_t first, int64_t width, int count, int* down) {
+  const ctr::PieceAt p = ctr::piece_at(first, width, count);
+  *down = p.down;
+  return p.column;
+}
 """
 
 
@@ -28,6 +33,9 @@ def host(tmp_path_factory):
                            "-I" + CSRC, "-o", lib, str(d / "access.cpp")])
     lib = ctypes.CDLL(lib)
     lib.whole.argtypes = [ctypes.c_uint64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
+    lib.piece.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                          ctypes.POINTER(ctypes.c_int)]
+    lib.piece.restype = ctypes.c_int64
     return lib
 
 
@@ -40,3 +48,19 @@ def test_whole_pieces_only_of_rows_that_are(host):
                 for stride in (width, width + 8, width + 16 // size):
                     want = p % 16 == 0 and stride * size % 16 == 0 and width * size % 16 == 0
                     assert bool(host.whole(p, stride, width, size)) == want, (size, width, p, stride)
+
+
+def test_pieces_of_a_tile_lie_inside_their_row(host):
+    """Every piece of every tile over rows of 1 to 300 columns: read inside the row, and what is
+    there of it found `down` elements later.  (Rows below a piece are read by elements.)"""
+    down = ctypes.c_int(0)
+    for count in (4, 8):
+        for tile in (64, 128):
+            for width in range(count, 301):
+                for first in range(0, (width + tile - 1) // tile * tile, count):
+                    column = host.piece(first, width, count, ctypes.byref(down))
+                    case = (count, tile, width, first, column, down.value)
+                    assert 0 <= column and column + count <= width, case
+                    assert 0 <= down.value < count, case
+                    if first < width:
+                        assert column + down.value == first, case

@@ -515,3 +515,35 @@ def test_gradients_of_no_rows_stay_in_their_arrays(N, dtype):
         dW.fill_(7.0)
         db.fill_(7.0)
         assert (flat == 7).all()
+
+
+# (rows, E, K, N): the last tile across has fewer columns than a 16-byte piece, the reductions end
+# with whole rounds, and the last expert's last row is the arrays' last
+EDGES = [(128, 2, 65, 64), (256, 2, 64, 257), (256, 1, 129, 131), (192, 3, 71, 128),
+         (640, 1, 135, 66), (7168, 2, 1027, 640), (128, 2, 67, 3), (128, 1, 5, 64)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,E,K,N", EDGES)
+def test_products_to_the_last_row_of_every_array(n, E, K, N, dtype, gather):
+    say("edges", n, E, K, N, dtype, gather)
+    g = gen(n + K + N)
+    X = torch.randn((n, K), generator=g).to(dtype)
+    W = (torch.randn((E, N, K), generator=g) * K ** -0.5).to(dtype)
+    dY = torch.randn((n, N), generator=g).to(dtype)
+    offsets = torch.arange(E + 1, dtype=torch.int32) * (n // E)
+    offsets[E] = n
+    order = torch.randperm(n, generator=g).int() if gather else None
+    at = None if order is None else order.to(DEV)
+    Xd, Wd, fd, dYd = X.to(DEV), W.to(DEV), offsets.to(DEV), dY.to(DEV)
+    Y = ctr.ctr_expert_dense_fwd(Xd, Wd, None, fd, False, at, 1)
+    dX, dW, db = ctr.ctr_expert_dense_bwd(Xd, Wd, fd, dYd, at, 1)
+    v, mag = ref.dense_fwd(X, W, None, offsets, False, order, 1, n)
+    assert_near(Y, v, stored(v, (K + 3) * U32 * mag, dtype), "Y")
+    want = ref.dense_bwd(X, W, offsets, dY, order, 1, False)
+    v, mag, L = want["dX"]
+    assert_near(dX, v, stored(v, (L + 2) * U32 * mag, dtype), "dX")
+    for got, name in ((dW, "dW"), (db, "db")):
+        v, mag, L = want[name]
+        assert_near(got, v, (L + 2) * U32 * mag, name)
