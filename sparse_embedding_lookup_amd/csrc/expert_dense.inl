@@ -890,14 +890,17 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
   // A whole round reads whole pieces, all inside their rows.  Rows and columns past the tile's
   // last are not stored, so any in their place will do: rows the tile's first, and a column piece
   // that is not all there the row's last whole one, moved down (by `down` elements) to where it
-  // belongs if part of it is.
+  // belongs if part of it is.  What is read for a row outside X is cleared: forward W's piece, in
+  // the weight gradient X's first row, where X has any (without, the way by elements is taken,
+  // which reads none; dY's piece in its place: dW 53 us for 50 at the size above).
   const int64_t atop = AROW ? end - row0 : end, btop = cols;
   const PieceAt ap = AROW ? PieceAt{0, 0} : piece_at(row0 + c, atop, PE);
   const PieceAt bp = BROW ? PieceAt{0, 0} : piece_at(n0 + c, btop, PE);
   const int64_t acol = ap.column, bcol = bp.column;
   const int adown = ap.down, bdown = bp.down;
   const bool aedge = !AROW && row0 + BM > atop, bedge = !BROW && n0 + BM > btop;
-  const bool narrow = (!AROW && atop < PE) || (!BROW && btop < PE);
+  const bool narrow = (!AROW && atop < PE) || (!BROW && btop < PE) ||
+                      (KIND == kWeight && g.x_rows == 0);
   auto moved = [](Piece x, int down) {
     if constexpr (TY == kEltF32) {
       if (down & 1) x = __builtin_shufflevector(x, x, 1, 2, 3, 3);
@@ -947,9 +950,10 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
         const int64_t ar = row0 + (r < atop ? r : 0), br = n0 + r < btop ? n0 + r : n0;
         const int64_t kk = k + kr + q * STEP;
         if constexpr (KIND == kForward) {
-          a[q] = all(X + (xrow[q] >= 0 ? xrow[q] : 0) * g.xs + k + kp);
+          const T* w = W + br * g.K + k + kp;
+          a[q] = all(xrow[q] >= 0 ? X + xrow[q] * g.xs + k + kp : w);
           if (xrow[q] < 0) a[q] = zero;
-          b[q] = all(W + br * g.K + k + kp);
+          b[q] = all(w);
         } else if constexpr (KIND == kInput) {
           a[q] = all(dY + ar * g.dys + k + kp);
           b[q] = all(W + kk * g.K + bcol);
@@ -1072,12 +1076,11 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
   for (int i = 0; i < TW; ++i) {
     const int64_t r = row0 + BM / 2 * wm + 32 * i + rl;
     float with[TW][4][4];
-    bool open = false;
     const int first = n0 + BM / 2 * wn + 4 * kg;
-    if (biased || masked) {
-      const int64_t xr = masked && r < end ? x_row(g, r) : -1;
-      open = xr >= 0;
-      const int64_t from = biased ? (int64_t)e * g.N : (open ? xr : 0) * g.xs;
+    const int64_t xr = masked && r < end ? x_row(g, r) : -1;
+    const bool open = xr >= 0;
+    if (biased || open) {
+      const int64_t from = biased ? (int64_t)e * g.N : xr * g.xs;
 #pragma unroll
       for (int j = 0; j < TW; ++j)
 #pragma unroll

@@ -5,6 +5,8 @@ relative to the sum of the terms' magnitudes, whatever the order (products of 16
 are exact in binary32, those of binary32 operands cost the one half step in the 2); a stored
 result adds half a step of its type.  Choices, positions and copies are equal bit for bit.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -547,3 +549,35 @@ def test_products_to_the_last_row_of_every_array(n, E, K, N, dtype, gather):
     for got, name in ((dW, "dW"), (db, "db")):
         v, mag, L = want[name]
         assert_near(got, v, (L + 2) * U32 * mag, name)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,K,N", [(40, 64, 48), (40, 65, 33), (1500, 64, 128), (1500, 67, 130)])
+def test_products_of_an_input_without_rows(n, K, N, dtype):
+    """Slots, but no row of X: every slot is outside, and nothing is read at X's address (here
+    the end of what is allocated)."""
+    say("no input rows", n, K, N, dtype)
+    E, lib = 3, ctr.load()
+    g = gen(n + K)
+    W = torch.randn((E, N, K), generator=g).to(dtype).to(DEV)
+    b = torch.randn((E, N), generator=g).to(DEV)
+    dY = torch.randn((n, N), generator=g).to(dtype).to(DEV)
+    order = torch.arange(n, dtype=torch.int32, device=DEV)
+    offsets = torch.tensor([0, n // 4, n // 2, n], dtype=torch.int32, device=DEV)
+    block = torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    X = block.data_ptr() + block.numel()
+    Y, dX = (torch.full((n, c), -3.0, dtype=dtype, device=DEV) for c in (N, K))
+    dW = torch.full((E, N, K), -3.0, device=DEV)
+    code, stream = ctr._dtype_code(W), torch.cuda.current_stream().cuda_stream
+    assert lib.ctr_expert_dense_fwd(X, code, K, 0, order.data_ptr(), 1, offsets.data_ptr(), n, E,
+                                    K, W.data_ptr(), b.data_ptr(), N, 1, Y.data_ptr(), N,
+                                    stream) == ctr.CTR_OK
+    bytes_ = ctypes.c_size_t(ctr.expert_dense_bwd_workspace_bytes(n, E, K, N, code))
+    room = torch.empty(bytes_.value, dtype=torch.uint8, device=DEV)
+    assert lib.ctr_expert_dense_bwd(X, code, K, 0, order.data_ptr(), 1, offsets.data_ptr(), n, E,
+                                    K, W.data_ptr(), N, 1, dY.data_ptr(), N, dX.data_ptr(), K,
+                                    dW.data_ptr(), None, room.data_ptr(), ctypes.byref(bytes_),
+                                    stream) == ctr.CTR_OK
+    expert = torch.bucketize(order, offsets[1:], right=True)
+    assert torch.equal(Y, torch.relu(b[expert.long()]).to(dtype))
+    assert (dX == 0).all() and (dW == 0).all()
