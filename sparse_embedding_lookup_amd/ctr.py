@@ -194,10 +194,31 @@ def _check(fn: str, status: int) -> None:
         raise CtrError(fn, status, load().ctr_last_error_message().decode())
 
 
+def _tensors(*values):
+    """The tensors among values, and in tuples of them."""
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, tuple):
+            yield from _tensors(*v)
+
+
+def _capturing(stream=None) -> bool:
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class Call:
     """A libctr call whose arguments were marshalled once; calling it only reads the current
-    stream (so it also works under stream capture) and checks the status."""
-    __slots__ = ("name", "fn", "args", "result", "keep")
+    stream (so it also works under stream capture) and checks the status.
+
+    What the binding allocated for it belongs to the stream that was current when it was made;
+    another stream that calls it has to wait for that one first, as for any tensor, and the
+    memory then outlives the call's work there.  A graph that a call was captured into uses its
+    memory in every replay: keep the call as long as the graph."""
+    __slots__ = ("name", "fn", "args", "result", "keep", "streams")
 
     def __init__(self, name: str, args: tuple, result=None, keep=None):
         self.name = name
@@ -206,12 +227,24 @@ class Call:
         self.result = result
         self.keep = keep                  # a workspace that the binding allocated for the call
                                           # (and host arrays that the library reads)
+        # streams that the memory of result and keep is not taken from before their work is done
+        self.streams = {_stream()} if torch.cuda.is_initialized() else set()
 
     def __call__(self, stream=None):
-        st = self.fn(*self.args, _stream(stream))
+        s = _stream() if stream is None else stream.cuda_stream
+        st = self.fn(*self.args, s)
         if st != CTR_OK:
             _check(self.name, st)
+        if s not in self.streams:
+            self._used_on(stream, s)
         return self.result
+
+    def _used_on(self, stream, address: int) -> None:
+        if _capturing(stream):
+            return
+        for t in _tensors(self.result, self.keep):
+            t.record_stream(stream if stream is not None else torch.cuda.current_stream())
+        self.streams.add(address)
 
 
 def _run(name: str, args: tuple, stream, prepare: bool, result=None, keep=None):
@@ -650,10 +683,8 @@ def _launch(name: str, device: torch.device, args: tuple, stream, prepare: bool,
     if stream is not None and not prepare:
         # what the binding allocated belongs to the current stream: its memory is not reused
         # there before this stream's work is done
-        for t in (result if isinstance(result, tuple) else (result,)) + (
-                keep if isinstance(keep, tuple) else (keep,)):
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
+        for t in _tensors(result, keep):
+            t.record_stream(stream)
     return got
 
 

@@ -223,3 +223,28 @@ def test_definitions_agree_with_autograd():
     dX, _ = ref.combine_fwd(got["dX"][0], slots, None)
     for a, c in zip((dX, got["dW"][0], got["db"][0], dv), want):
         assert torch.allclose(a, c)
+
+
+class _Recorded(torch.Tensor):
+    def record_stream(self, stream):
+        self.streams = getattr(self, "streams", []) + [stream]
+
+
+class _Stream:
+    def __init__(self, address):
+        self.cuda_stream = address
+
+
+def test_a_prepared_call_keeps_its_memory_for_the_streams_it_runs_on(monkeypatch):
+    """What the binding allocated for a prepared call is recorded, once, with every stream that
+    the call runs on, but with none that is being captured."""
+    lib()
+    made, given, room = (torch.zeros(4).as_subclass(_Recorded) for _ in range(3))
+    call = ctr.Call("ctr_version", (), (made, None, given), (room, [1, 2]))
+    call.fn = lambda *a: ctr.CTR_OK
+    a, b = _Stream(0x100), _Stream(0x200)
+    for capturing, stream in ((True, a), (False, a), (False, b), (False, a)):
+        monkeypatch.setattr(ctr, "_capturing", lambda s: capturing, raising=False)
+        assert call(stream=stream) is call.result
+    for t in (made, given, room):
+        assert t.streams == [a, b]

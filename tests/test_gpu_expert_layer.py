@@ -219,3 +219,39 @@ def test_offsets_out_of_order_stay_inside(n, E, K, N, dtype):
     offsets = torch.arange(E + 1, device=DEV, dtype=torch.int32) * (n // E)
     _, dW, db = ctr.ctr_expert_dense_bwd(X, W, offsets, dY, workspace=room[:size])
     assert bool((dW == n // E).all()) and bool((db == n // E).all())
+
+
+def test_memory_of_a_prepared_call_on_another_stream():
+    """The same of a prepared call that is gone before its work has run."""
+    say("prepared on another stream")
+    side = torch.cuda.Stream()
+    g = torch.Generator().manual_seed(4)
+    experts = torch.randint(0, 7, (60000, 2), generator=g, dtype=torch.int32)
+    want = ref.sort(experts, 7)
+    e = experts.to(DEV)
+    a = torch.randn(4096, 4096, device=DEV)
+    call = ctr.ctr_expert_sort(e, 7, prepare=True)
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(10):
+            a = a @ a * 1e-3                    # the sort waits behind these
+    got = call(stream=side)
+    del call
+    for _ in range(8):                          # the workspace's memory, were it free
+        torch.empty(200 * 7 * 4 + 512, dtype=torch.uint8, device=DEV).fill_(255)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x.cpu(), y)
+    # the outputs of a call that nobody keeps
+    call = ctr.ctr_expert_sort(e, 7, prepare=True)
+    places = [t.data_ptr() for t in call.result]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(10):
+            a = a @ a * 1e-3
+        call()
+    del call
+    taken = [torch.empty_like(t) for t in got]
+    assert not set(places) & {t.data_ptr() for t in taken}
+    torch.cuda.synchronize()
