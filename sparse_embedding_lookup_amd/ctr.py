@@ -674,18 +674,26 @@ def ctr_logistic_ne(logits: torch.Tensor, labels: torch.Tensor,
 _DTYPE_CODES = {torch.float32: CTR_F32, torch.bfloat16: CTR_BF16, torch.float16: CTR_F16}
 
 
-def _launch(name: str, device: torch.device, args: tuple, stream, prepare: bool, result=None,
-            keep=None):
-    """_run of arguments that are all on `device`, which has to be a GPU."""
+def _on(stream, call, *args, **named):
+    """call(..) with `stream` current.  What the binding allocates then is memory of that stream,
+    where nothing else is still under way.  The results are the caller's, so the stream that was
+    current counts as their user too, as `stream` does of what the caller gave."""
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        got = call(*args, **named)
+    made = got.result if isinstance(got, Call) else got
+    for t in _tensors(made):
+        t.record_stream(here)
+    for t in _tensors(made, *args):
+        t.record_stream(stream)
+    return got
+
+
+def _launch(name: str, device: torch.device, args: tuple, prepare: bool, result=None, keep=None):
+    """_run of arguments that are all on `device`, which has to be a GPU, on the current stream."""
     if device.type != "cuda":
         raise ValueError("%s takes tensors on a GPU, not on %s" % (name, device))
-    got = _run(name, args, stream, prepare, result, keep)
-    if stream is not None and not prepare:
-        # what the binding allocated belongs to the current stream: its memory is not reused
-        # there before this stream's work is done
-        for t in _tensors(result, keep):
-            t.record_stream(stream)
-    return got
+    return _run(name, args, None, prepare, result, keep)
 
 
 def _expert_arg(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
@@ -763,13 +771,16 @@ def ctr_expert_route_fwd(logits: torch.Tensor, k: int, renormalize: bool = True,
     """The k experts of the largest logits of every token ([T, E]; rows may be strided), the
     larger first, ties to the lower expert, and their softmax weights (over the chosen, or over
     all experts): (experts int32 [T, k], weights fp32 [T, k]).  -inf closes an expert."""
+    if stream is not None:
+        return _on(stream, ctr_expert_route_fwd, logits, k, renormalize, experts, weights,
+                   prepare=prepare)
     code, ls = _expert_type(logits, "logits"), _row_stride(logits, "logits")
     T, E = logits.shape
     dev = logits.device
     experts, ep = _dense(experts, "experts", (T, k), (k, 1), torch.int32, dev)
     weights, wp = _dense(weights, "weights", (T, k), (k, 1), torch.float32, dev)
     args = (logits.data_ptr(), code, ls, T, E, k, int(bool(renormalize)), ep, wp)
-    return _launch("ctr_expert_route_fwd", dev, args, stream, prepare, (experts, weights))
+    return _launch("ctr_expert_route_fwd", dev, args, prepare, (experts, weights))
 
 
 def ctr_expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor,
@@ -778,6 +789,9 @@ def ctr_expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, weights: t
                          prepare: bool = False):
     """The gradient of the logits from that of the weights; experts and weights as the forward
     gave them."""
+    if stream is not None:
+        return _on(stream, ctr_expert_route_bwd, logits, experts, weights, dweights, renormalize,
+                   dlogits, prepare=prepare)
     code, ls = _expert_type(logits, "logits"), _row_stride(logits, "logits")
     T, E = logits.shape
     dev, k = logits.device, experts.shape[-1]
@@ -786,7 +800,7 @@ def ctr_expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, weights: t
             _expert_arg(experts, "experts", (T, k), torch.int32, dev),
             _expert_arg(weights, "weights", (T, k), torch.float32, dev),
             _expert_arg(dweights, "dweights", (T, k), torch.float32, dev), dp, dls)
-    return _launch("ctr_expert_route_bwd", dev, args, stream, prepare, dlogits)
+    return _launch("ctr_expert_route_bwd", dev, args, prepare, dlogits)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -805,6 +819,9 @@ def ctr_expert_sort(experts: torch.Tensor, num_experts: int,
                     prepare: bool = False):
     """The slots of experts [T, k] sorted by expert: (offsets int32 [E + 1], slots int32 [T, k],
     order int32 [T * k]).  An expert outside [0, num_experts) drops its slot."""
+    if stream is not None:
+        return _on(stream, ctr_expert_sort, experts, num_experts, offsets, slots, order,
+                   workspace, prepare=prepare)
     if experts.dim() != 2:
         raise ValueError("experts must be [T, k]")
     T, k = experts.shape
@@ -817,7 +834,7 @@ def ctr_expert_sort(experts: torch.Tensor, num_experts: int,
     wsb = ctypes.c_size_t(workspace.numel())
     args = (_expert_arg(experts, "experts", (T, k), torch.int32, dev), T, k, num_experts, fp, sp,
             op, workspace.data_ptr(), ctypes.byref(wsb))
-    return _launch("ctr_expert_sort", dev, args, stream, prepare, (offsets, slots, order),
+    return _launch("ctr_expert_sort", dev, args, prepare, (offsets, slots, order),
                    workspace)
 
 
@@ -838,13 +855,15 @@ def ctr_expert_dispatch(X: torch.Tensor, slots: torch.Tensor, offsets: torch.Ten
                         P: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
     """The tokens' rows in the experts' order: P [T * k, D], P[slots[t, j]] = X[t]; positions of
     no slot are zero."""
+    if stream is not None:
+        return _on(stream, ctr_expert_dispatch, X, slots, offsets, P, prepare=prepare)
     code, dev = _expert_type(X, "X"), X.device
     T, k, sp, op, E = _slot_args(slots, offsets, dev)
     D = X.shape[-1]
     xp, xs = _rows_arg(X, "X", (T, D), X.dtype, dev)
     P, pp, ps = _matrix(P, "P", T * k, D, X.dtype, dev)
     args = (xp, code, xs, T, k, D, sp, op, E, pp, ps)
-    return _launch("ctr_expert_dispatch", dev, args, stream, prepare, P)
+    return _launch("ctr_expert_dispatch", dev, args, prepare, P)
 
 
 def ctr_expert_combine_fwd(P: torch.Tensor, slots: torch.Tensor,
@@ -852,6 +871,8 @@ def ctr_expert_combine_fwd(P: torch.Tensor, slots: torch.Tensor,
                            stream=None, prepare: bool = False):
     """Y[t] = sum_j weights[t, j] P[slots[t, j]] (weights None: 1, the gradient of
     ctr_expert_dispatch)."""
+    if stream is not None:
+        return _on(stream, ctr_expert_combine_fwd, P, slots, weights, Y, prepare=prepare)
     code, dev = _expert_type(P, "P"), P.device
     T, k, sp, _, _ = _slot_args(slots, None, dev)
     D = P.shape[-1]
@@ -859,7 +880,7 @@ def ctr_expert_combine_fwd(P: torch.Tensor, slots: torch.Tensor,
     Y, yp, ys = _matrix(Y, "Y", T, D, P.dtype, dev)
     wp = None if weights is None else _expert_arg(weights, "weights", (T, k), torch.float32, dev)
     args = (pp, code, ps, T, k, D, sp, wp, yp, ys)
-    return _launch("ctr_expert_combine_fwd", dev, args, stream, prepare, Y)
+    return _launch("ctr_expert_combine_fwd", dev, args, prepare, Y)
 
 
 def ctr_expert_combine_bwd(dY: torch.Tensor, P: Optional[torch.Tensor], slots: torch.Tensor,
@@ -869,6 +890,9 @@ def ctr_expert_combine_bwd(dY: torch.Tensor, P: Optional[torch.Tensor], slots: t
                            prepare: bool = False):
     """(dP [T * k, D], dweights fp32 [T, k]) of ctr_expert_combine_fwd; P None: dP alone (then
     dweights is None)."""
+    if stream is not None:
+        return _on(stream, ctr_expert_combine_bwd, dY, P, slots, offsets, weights, dP, dweights,
+                   prepare=prepare)
     code, dev = _expert_type(dY, "dY"), dY.device
     T, k, sp, op, E = _slot_args(slots, offsets, dev)
     D = dY.shape[-1]
@@ -882,7 +906,7 @@ def ctr_expert_combine_bwd(dY: torch.Tensor, P: Optional[torch.Tensor], slots: t
         raise ValueError("dweights needs P")
     wp = None if weights is None else _expert_arg(weights, "weights", (T, k), torch.float32, dev)
     args = (yp, code, dys, T, k, D, pp, ps, sp, op, E, wp, dpp, dps, dwp)
-    return _launch("ctr_expert_combine_bwd", dev, args, stream, prepare, (dP, dweights))
+    return _launch("ctr_expert_combine_bwd", dev, args, prepare, (dP, dweights))
 
 
 def _product_args(X, W, offsets, order, k):
@@ -914,12 +938,15 @@ def ctr_expert_dense_fwd(X: torch.Tensor, W: torch.Tensor, b: Optional[torch.Ten
     """Each expert's layer over its rows: Y [n, N] = act(x W[e]^T + b[e]) with W [E, N, K], b
     fp32 [E, N] or None.  x is X [n, K] by position, or with `order` (ctr_expert_sort's, and its
     k) the token's row X [T, K]."""
+    if stream is not None:
+        return _on(stream, ctr_expert_dense_fwd, X, W, b, offsets, relu, order, k, Y,
+                   prepare=prepare)
     first, n, E, N, K = _product_args(X, W, offsets, order, k)
     dev = X.device
     Y, yp, ys = _matrix(Y, "Y", n, N, X.dtype, dev)
     bp = None if b is None else _expert_arg(b, "b", (E, N), torch.float32, dev)
     args = first + (bp, N, int(bool(relu)), yp, ys)
-    return _launch("ctr_expert_dense_fwd", dev, args, stream, prepare, Y)
+    return _launch("ctr_expert_dense_fwd", dev, args, prepare, Y)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -943,6 +970,9 @@ def ctr_expert_dense_bwd(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor
     """(dX [n, K] by position, dW fp32 [E, N, K], db fp32 [E, N]) from dY [n, N], the gradient
     before the activation; x_relu: X is a rectified output, and dX the gradient before it.  What
     is not wanted (bias, want_dx, want_dw) is None."""
+    if stream is not None:
+        return _on(stream, ctr_expert_dense_bwd, X, W, offsets, dY, order, k, x_relu, bias,
+                   want_dx, want_dw, dX, dW, db, workspace, prepare=prepare)
     first, n, E, N, K = _product_args(X, W, offsets, order, k)
     dev = X.device
     yp, dys = _rows_arg(dY, "dY", (n, N), X.dtype, dev)
@@ -958,7 +988,7 @@ def ctr_expert_dense_bwd(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor
     wsb = ctypes.c_size_t(workspace.numel())
     args = first + (N, int(bool(x_relu)), yp, dys, xp, dxs, wp, bp, workspace.data_ptr(),
                     ctypes.byref(wsb))
-    return _launch("ctr_expert_dense_bwd", dev, args, stream, prepare,
+    return _launch("ctr_expert_dense_bwd", dev, args, prepare,
                    (dX if want_dx else None, dW if want_dw else None, db if bias else None),
                    workspace)
 
@@ -1000,6 +1030,9 @@ def _tensor_list(ts, name: str, device: torch.device, sizes=None, dtypes=None):
 
 
 def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepare, out_name):
+    if stream is not None:
+        return _on(stream, _clip_call, name, grads, outs, lr, max_norm, stats, workspace, None,
+                   prepare, out_name)
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
@@ -1022,7 +1055,7 @@ def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepar
         at.append(None)
     args = (num, *at) + (() if lr is None else (float(lr),)) + (
         float(max_norm), sp, workspace.data_ptr(), ctypes.byref(wsb))
-    return _launch(name, dev, args, stream, prepare, stats, (workspace, host))
+    return _launch(name, dev, args, prepare, stats, (workspace, host))
 
 
 def ctr_grad_clip(grads: Sequence[torch.Tensor], max_norm: float,

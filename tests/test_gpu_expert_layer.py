@@ -255,3 +255,60 @@ def test_memory_of_a_prepared_call_on_another_stream():
     taken = [torch.empty_like(t) for t in got]
     assert not set(places) & {t.data_ptr() for t in taken}
     torch.cuda.synchronize()
+
+
+def _operators(stream=None):
+    """One small call of every operator: names and calls that take the stream."""
+    g = torch.Generator().manual_seed(6)
+    T, E, k, K, N = 300, 5, 2, 72, 40
+    logits = torch.randn((T, E), generator=g).to(DEV)
+    X, Q = (torch.randn((r, K), generator=g).to(DEV) for r in (T, T * k))
+    W, dY = torch.randn((E, N, K), generator=g).to(DEV), torch.randn((T * k, N), generator=g).to(DEV)
+    dw = torch.randn((T, k), generator=g).to(DEV)
+    experts, weights = ctr.ctr_expert_route_fwd(logits, k)
+    offsets, slots, order = ctr.ctr_expert_sort(experts, E)
+    return [
+        ("route_fwd", lambda **a: ctr.ctr_expert_route_fwd(logits, k, **a)),
+        ("route_bwd", lambda **a: ctr.ctr_expert_route_bwd(logits, experts, weights, dw, **a)),
+        ("sort", lambda **a: ctr.ctr_expert_sort(experts, E, **a)),
+        ("dispatch", lambda **a: ctr.ctr_expert_dispatch(X, slots, offsets, **a)),
+        ("combine_fwd", lambda **a: ctr.ctr_expert_combine_fwd(Q, slots, weights, **a)),
+        ("combine_bwd", lambda **a: ctr.ctr_expert_combine_bwd(X, Q, slots, offsets, weights, **a)),
+        ("dense_fwd", lambda **a: ctr.ctr_expert_dense_fwd(X, W, None, offsets, True, order, k, **a)),
+        ("dense_bwd", lambda **a: ctr.ctr_expert_dense_bwd(X, W, offsets, dY, order, k, **a)),
+        ("clip", lambda **a: ctr.ctr_grad_clip([dw, X], 0.5, [torch.empty_like(dw),
+                                                             torch.empty_like(X)], **a)),
+        ("clip_sgd", lambda **a: ctr.ctr_grad_clip_sgd([dw], [dw.clone()], 0.1, 0.5, **a))]
+
+
+@pytest.mark.parametrize("prepare", [False, True])
+def test_calls_on_another_stream_take_none_of_the_current_streams_memory(prepare):
+    """Memory that was freed while the current stream still writes to it is not given to a call on
+    another stream, which does not wait for that."""
+    say("memory under way", prepare)
+    side = torch.cuda.Stream()
+    calls = _operators()
+    want = [tuple(ctr._tensors(call())) for _, call in calls]
+    sizes = sorted({t.numel() * t.element_size() for w in want for t in w})
+    torch.cuda.synchronize()
+    a = torch.randn(4096, 4096, device=DEV)
+    for (name, call), right in zip(calls, want):
+        torch.cuda.synchronize()
+        for _ in range(10):
+            a = a @ a * 1e-3
+        places = set()
+        for size in sizes + [256, 16384, 1 << 20]:
+            for _ in range(4):
+                held = torch.empty(size, dtype=torch.uint8, device=DEV)
+                held.fill_(255)                 # waits behind the products
+                places.add(held.untyped_storage().data_ptr())
+                del held
+        got = call(stream=side, prepare=prepare)
+        if prepare:
+            got = got(stream=side)
+        got = tuple(ctr._tensors(got))
+        assert not places & {t.untyped_storage().data_ptr() for t in got}, name
+        torch.cuda.synchronize()
+        assert len(got) == len(right) > 0
+        for x, y in zip(got, right):
+            assert torch.equal(x, y), name
