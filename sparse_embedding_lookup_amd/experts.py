@@ -61,6 +61,9 @@ class ExpertLayer:
         self.params: List[torch.Tensor] = [self.Wg, self.W1, self.b1, self.W2, self.b2]
         self.grads = [torch.zeros(p.shape, dtype=f32, device=dev) for p in self.params]
         self.stats = torch.zeros(2, dtype=f32, device=dev)
+        # a graph that holds an update uses this memory after the call itself has gone
+        self.clip_room = torch.empty(ctr.grad_clip_workspace_bytes(len(self.grads)),
+                                     dtype=torch.uint8, device=dev)
         self._update = {}
 
         p = dict(prepare=True)
@@ -101,12 +104,13 @@ class ExpertLayer:
         return self.dX.add_(self.dXg)
 
     def update(self, lr: float, max_norm: float) -> torch.Tensor:
-        """The SGD step with gradients clipped to `max_norm`; returns [norm, scale] (device)."""
+        """The SGD step with gradients clipped to `max_norm`; returns [norm, scale] (device).  A
+        captured step keeps the lr and max_norm it was captured with."""
         call = self._update.get((lr, max_norm))
         if call is None:
             self._update.clear()
             call = ctr.ctr_grad_clip_sgd(self.grads, self.params, lr, max_norm, self.stats,
-                                         prepare=True)
+                                         self.clip_room, prepare=True)
             self._update[lr, max_norm] = call
         return call()
 

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from sparse_embedding_lookup_amd import ctr
+from sparse_embedding_lookup_amd.experts import ExpertLayer
 from tests import experts_ref as ref
 
 A = ctypes.c_void_p(0x10000)
@@ -248,3 +249,20 @@ def test_a_prepared_call_keeps_its_memory_for_the_streams_it_runs_on(monkeypatch
         assert call(stream=stream) is call.result
     for t in (made, given, room):
         assert t.streams == [a, b]
+
+
+def test_updates_of_a_layer_share_memory_that_stays(monkeypatch):
+    """An update of another rate replaces the prepared call, whose workspace a captured graph may
+    still use: all of them have the layer's own."""
+    layer = ExpertLayer.__new__(ExpertLayer)
+    layer.grads, layer.params, layer.stats, layer._update = [], [], torch.zeros(2), {}
+    layer.clip_room = torch.zeros(256, dtype=torch.uint8)
+    rooms = []
+
+    def prepared(grads, params, lr, max_norm, stats=None, workspace=None, prepare=False):
+        rooms.append(workspace)
+        return lambda: stats
+    monkeypatch.setattr(ctr, "ctr_grad_clip_sgd", prepared)
+    for lr in (0.1, 0.2, 0.2, 0.1):
+        assert layer.update(lr, 1.0) is layer.stats
+    assert len(rooms) == 3 and all(r is layer.clip_room for r in rooms)

@@ -312,3 +312,34 @@ def test_calls_on_another_stream_take_none_of_the_current_streams_memory(prepare
         assert len(got) == len(right) > 0
         for x, y in zip(got, right):
             assert torch.equal(x, y), name
+
+
+def test_a_captured_step_after_updates_of_other_rates():
+    """Steps replayed from a graph do not depend on what eager updates of other rates, and memory
+    allocated after them, hold."""
+    say("captured step, other rates")
+    pair = [ExpertLayer(200, 32, 48, 16, 4, 2, F32) for _ in range(2)]
+    for L in pair:
+        _fill(L, 8)
+
+    def step(L, lr):
+        L.forward()
+        L.backward()
+        L.update(lr, 0.5)
+    for L in pair:
+        step(L, 0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(pair[0], 0.1)
+    size = ctr.grad_clip_workspace_bytes(len(pair[0].grads))
+    for lr in (0.3, 0.05, 0.2):
+        for L in pair:
+            step(L, lr)
+        held = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        graph.replay()
+        step(pair[1], 0.1)
+        torch.cuda.synchronize()
+        assert all(bool((h == 255).all()) for h in held)
+        for a, b in zip(pair[0].params, pair[1].params):
+            assert torch.equal(a, b)
