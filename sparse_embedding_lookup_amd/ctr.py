@@ -1034,9 +1034,9 @@ def _clip_call(name, grads, outs, lr, max_norm, stats, workspace, stream, prepar
         return _on(stream, _clip_call, name, grads, outs, lr, max_norm, stats, workspace, None,
                    prepare, out_name)
     grads = list(grads)
-    if not grads:
-        raise ValueError("no gradients")
-    dev = grads[0].device
+    if not grads and stats is None:
+        raise ValueError("no gradients, and no stats to say on which device")
+    dev = grads[0].device if grads else stats.device
     ptrs, counts, codes = _tensor_list(grads, "grads", dev)
     num = len(grads)
     stats, sp = _dense(stats, "stats", (2,), (1,), torch.float32, dev)
@@ -1064,7 +1064,7 @@ def ctr_grad_clip(grads: Sequence[torch.Tensor], max_norm: float,
                   workspace: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
     """Scales the gradients (contiguous tensors of any of the three types) so that the norm of
     them all is at most max_norm, in place or into `outs` (same sizes and types); returns stats
-    [norm, scale] (device)."""
+    [norm, scale] (device).  Without gradients, which takes a given `stats`: norm 0, scale 1."""
     return _clip_call("ctr_grad_clip", grads, outs, None, max_norm, stats, workspace, stream,
                       prepare, "outs")
 

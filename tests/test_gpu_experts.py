@@ -581,3 +581,18 @@ def test_products_of_an_input_without_rows(n, K, N, dtype):
     expert = torch.bucketize(order, offsets[1:], right=True)
     assert torch.equal(Y, torch.relu(b[expert.long()]).to(dtype))
     assert (dX == 0).all() and (dW == 0).all()
+
+
+def test_clipping_no_gradients():
+    """A step without gradients has norm 0 and scale 1, where there are stats to write them to."""
+    say("no gradients")
+    for call in (lambda s: ctr.ctr_grad_clip([], 1.0, stats=s),
+                 lambda s: ctr.ctr_grad_clip([], 1.0, [], stats=s),
+                 lambda s: ctr.ctr_grad_clip_sgd([], [], 0.1, 0.0, stats=s)):
+        stats = torch.full((2,), -3.0, device=DEV)
+        assert call(stats) is stats and stats.tolist() == [0.0, 1.0]
+    with pytest.raises(ValueError):
+        ctr.ctr_grad_clip([], 1.0)
+    with pytest.raises(ValueError):
+        ctr.ctr_grad_clip_sgd([], [torch.zeros(3, device=DEV)], 0.1, 1.0,
+                              stats=torch.zeros(2, device=DEV))
