@@ -339,7 +339,7 @@ def ctr_unique_ids(ids: torch.Tensor, *, offsets: Optional[torch.Tensor] = None,
                    src_layout(sorted_src), _ptr(ws), ctypes.byref(wsb))
     res = (uniq[:n], (inv[:n] if inv is not None else None), nu,
            (perm[:n] if perm is not None else None), seg)
-    return _run("ctr_unique_ids", full, stream, prepare, res)
+    return _run("ctr_unique_ids", full, stream, prepare, res, workspace)
 
 
 def ctr_gather_rows(table: torch.Tensor, rows: torch.Tensor, num_rows: torch.Tensor,
@@ -378,7 +378,7 @@ def ctr_embbag_fwd(table: torch.Tensor, indices: torch.Tensor, offsets: torch.Te
     args = (_ptr(table), _dtype_code(table), total_rows, dim, _ptr(row_base), num_tables,
             _ptr(indices), _index_code(indices), nnz, _ptr(offsets), batch, _ptr(out),
             _dtype_code(out), out_stride_b, out_stride_t, _ptr(workspace), ctypes.byref(wsb))
-    return _run("ctr_embbag_fwd", args, stream, prepare, out)
+    return _run("ctr_embbag_fwd", args, stream, prepare, out, workspace)
 
 
 def ctr_embbag_bwd(grad: torch.Tensor, grad_stride_b: int, grad_stride_t: int,
@@ -409,7 +409,7 @@ def ctr_embbag_bwd(grad: torch.Tensor, grad_stride_b: int, grad_stride_t: int,
     ws = workspace
     wsb = ctypes.c_size_t(ws.numel())
     return _run("ctr_embbag_bwd", args + (_ptr(ws), ctypes.byref(wsb)), stream, prepare,
-                row_grads)
+                row_grads, workspace)
 
 
 def ctr_embbag_bwd_sgd(grad: torch.Tensor, grad_stride_b: int, grad_stride_t: int,
@@ -435,7 +435,7 @@ def ctr_embbag_bwd_sgd(grad: torch.Tensor, grad_stride_b: int, grad_stride_t: in
             _ptr(uniq), ctypes.c_float(lr), rounding,
             ctypes.c_uint64(seed & 0xFFFFFFFFFFFFFFFF), _ptr(row_grads), _ptr(workspace),
             ctypes.byref(wsb))
-    return _run("ctr_embbag_bwd_sgd", args, stream, prepare, row_grads)
+    return _run("ctr_embbag_bwd_sgd", args, stream, prepare, row_grads, workspace)
 
 
 def ctr_embbag_bwd_sgd_noalloc(grad: torch.Tensor, grad_stride_b: int, grad_stride_t: int,
@@ -652,7 +652,7 @@ def ctr_dense_bwd_sgd(X: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor
     args = (_ptr(X), xs, M, K, _ptr(W), _ptr(b), N, int(bool(relu)), _ptr(Y), ys, _ptr(dY),
             _dtype_code(dY), dys, compute, float(lr), _ptr(dX), dxs, _ptr(workspace),
             ctypes.byref(wsb))
-    return _run("ctr_dense_bwd_sgd", args, stream, prepare, dX)
+    return _run("ctr_dense_bwd_sgd", args, stream, prepare, dX, workspace)
 
 
 def ctr_logistic_ne(logits: torch.Tensor, labels: torch.Tensor,
