@@ -253,6 +253,9 @@ def _run(name: str, args: tuple, stream, prepare: bool, result=None, keep=None):
     st = getattr(_lib or load(), name)(*args, _stream(stream))
     if st != CTR_OK:
         _check(name, st)
+    if stream is not None:                # what is dropped now is not reused before its work there
+        for t in _tensors(result, keep):
+            t.record_stream(stream)
     return result
 
 

@@ -7,6 +7,15 @@ import torch
 
 from sparse_embedding_lookup_amd import ctr
 
+class Recorded(torch.Tensor):
+    def record_stream(self, stream):
+        self.streams = getattr(self, "streams", []) + [stream]
+
+
+class Stream:
+    cuda_stream = 0x100
+
+
 F, I = torch.zeros, torch.int32
 
 
@@ -34,3 +43,16 @@ def test_prepared_call_keeps_the_workspace_it_was_made_with(which):
     addresses = [a.value for a in call.args if isinstance(a, ctypes.c_void_p)]
     kept = [t for t in ctr._tensors(call.keep) if t.dtype == torch.uint8]
     assert len(kept) == 1 and kept[0].data_ptr() in addresses, call.name
+
+
+def test_immediate_call_on_a_stream_records_what_it_leaves(monkeypatch):
+    """Outputs and the workspace of a call on a given stream may be dropped before it has run."""
+    class Lib:
+        @staticmethod
+        def ctr_logistic_ne(*args):
+            return ctr.CTR_OK
+    monkeypatch.setattr(ctr, "_lib", Lib)
+    out, room = (F(4).as_subclass(Recorded) for _ in range(2))
+    stream = Stream()
+    assert ctr._run("ctr_logistic_ne", (), stream, False, (out, None), room) == (out, None)
+    assert out.streams == [stream] and room.streams == [stream]
