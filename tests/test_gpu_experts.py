@@ -596,3 +596,30 @@ def test_clipping_no_gradients():
     with pytest.raises(ValueError):
         ctr.ctr_grad_clip_sgd([], [torch.zeros(3, device=DEV)], 0.1, 1.0,
                               stats=torch.zeros(2, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [65, 129, 192, 300])
+def test_few_rows_with_most_of_them_in_one_expert(rows, dtype):
+    """A request small enough for the few-rows kernel, one of whose experts has more rows than the
+    kernel takes at a time."""
+    say("few rows", rows, dtype)
+    E, n, K, N = 16, 300, 136, 72
+    g = gen(rows)
+    left, tail = n - rows, (n - rows) // 4      # tail: positions of no expert
+    counts = torch.zeros(E, dtype=torch.int32)
+    counts[3] = rows
+    counts[4:8] = (left - tail) // 4
+    counts[11] = left - tail - 4 * ((left - tail) // 4)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int32), counts.cumsum(0).int()])
+    X = torch.randn((n, K), generator=g).to(dtype)
+    W = (torch.randn((E, N, K), generator=g) * K ** -0.5).to(dtype)
+    b = torch.randn((E, N), generator=g)
+    order = torch.randperm(n, generator=g).int()
+    for o, relu, bias in ((None, True, b), (order, False, None)):
+        Y, untouched = canvas(n, N, 8, 0, dtype)
+        ctr.ctr_expert_dense_fwd(X.to(DEV), W.to(DEV), None if bias is None else bias.to(DEV),
+                                 offsets.to(DEV), relu, None if o is None else o.to(DEV), 1, Y)
+        want, mag = ref.dense_fwd(X, W, bias, offsets, relu, o, 1, n)
+        assert_near(Y, want, stored(want, (K + 3) * U32 * mag, dtype), "Y")
+        untouched()
