@@ -7,8 +7,9 @@
 //   backward  dX[p, :] = W[e]^T dY[p, :], times [x(p) > 0] where x is a rectified output
 //             dW[e]    = sum_p dY[p, :] x(p)^T,   db[e] = sum_p dY[p, :]        (fp32)
 // Three products of one shape: rows by columns over a reduction, the rows cut at the experts'
-// borders.  The row counts stay on the device: the grid has a block for every tile that n
-// rows in E pieces can need, and a block finds its expert by a scan over the offsets.
+// borders.  The row counts stay on the device: a grid is for every tile that n rows in E pieces
+// can need, a block for each (loose_kernel) or as many blocks as run at once, which take the tiles
+// there are in turn (wide_kernel); a block finds a tile's expert by a scan over the offsets.
 // Positions from offsets[E] on belong to no expert; their rows of Y and dX are zero.
 // Products are exact in the matrix cores (binary32 operands: rounded once), sums are fp32.
 namespace ctr {
@@ -1142,8 +1143,9 @@ __global__ __launch_bounds__(kThreads, 2) void loose_kernel(Product g) {
 // fourth 32 reduction values of them; weights and inputs go from memory to registers in the
 // form that the 16 x 16 matrix instruction takes (a lane 16 bytes of one row), eight loads of
 // weights in flight a wave, up to 64 rows of the expert against them.  The waves' sums are
-// added in order through LDS.  (96 rows, 16 experts of 1024 x 1024: 11.5 us, of which about 5 are
-// the launch and the chain of loads before the weights'; eight waves a block 15.7 us.)
+// added in order through LDS.  (96 rows, 16 experts of 1024 x 1024: 11.7 us, of which about 5 are
+// the launch and the chain of loads before the weights'; eight waves a block 15.7 us.)  An expert
+// with more rows than that has its weights read again for every 64 of them, one after the other.
 constexpr int kFewRows = 64;
 template <int TY>
 __device__ __forceinline__ f32x4 mma16(s16x8 a, s16x8 b, f32x4 c) {
@@ -1352,9 +1354,16 @@ static experts::Product expert_product(const void* X, int64_t xs, int64_t x_rows
   return g;
 }
 
-// Rows up to which the few-rows kernel takes the forward product: 16 an expert, and 64 (16
-// experts of 1024 x 1024: 96 rows 10 and 16 us with 128 x 128 tiles, 256 rows 14 and 16 us, 512
-// rows 18 and 16 us; one expert: 64 rows 8 and 16 us, 256 rows 25 and 16 us).
+// Rows up to which the few-rows kernel takes the forward product: 16 an expert, and 64.  Times
+// of that many rows, and of one more in tiles, of 1024 x 1024 in 16 bits, back to back:
+//   experts  rows  even              half in one expert  all in one
+//      1       80    9.4 and 15 us
+//     16      320   12.1 and 16 us    18 and 16 us         29 and 15 us
+//     32      576   21.5 and 17 us    30 and 18 us         51 and 15 us
+//    128     2112     76 and 49 us   100 and 61 us        184 and 16 us
+//   1024    16448    601 and 570 us  767 and 590 us      1410 and 65 us
+// The rule fits up to 16 experts with even rows; beyond, and the more uneven the rows are (which
+// the host does not know), fewer rows would do better in tiles already.
 static int64_t few_most(int E) { return 16 * (int64_t)E + 64; }
 
 // Row tiles that n rows in E + 1 pieces can need.
@@ -1447,7 +1456,10 @@ static int64_t most_partials(const experts::Product& g) {
 // more costs writing and reading N K sums: above twice the mean, or, where there are fewer than
 // two tiles a compute unit, one and a half (product and join of 16384 rows in 16 uneven experts
 // of 1024 x 1024, 256 tiles: 96 us with twice, 81 us; 8 experts of 2048 x 2048, 512 tiles: 147
-// and 161 us).  Else as many slices as fill the chip.
+// and 161 us).  Else as many slices as fill the chip.  The two steps are measured at those tile
+// counts alone.  With many more tiles a compute unit the cuts still cost their sums: 32 uneven
+// experts of 2208 x 2048, nine tiles a compute unit, 80 us for the join beside 622 us for the
+// product, and room for up to as many sums as dW has elements.
 static void set_slices(experts::Product& g, bool wide) {
   auto across = [&](int64_t t) { return (g.N + t - 1) / t * ((g.K + t - 1) / t); };
   g.big = across(256) * g.E >= 256;

@@ -19,9 +19,10 @@ constexpr int kThreads = 256;
 // butterfly that prefers the larger value and, among equals, the lower expert; lane j keeps the
 // j-th.  The softmax is relative to the first value taken, the row's largest.  A logit that is
 // -inf or NaN closes its expert.
-// Bound by the k rounds of dependent exchanges (forward 8.6 us, backward, which has one exchange,
-// 6.1 us at 65536 x 64 bf16, 4 experts; with exchanges through LDS and one logit a load 10.7 and
-// 7.1 us; their bytes are 2 us each).
+// Bound by the instructions of the k rounds: forward 8.6 us, backward, whose k entries of a token
+// are exchanged through LDS, 6.1 us at 65536 x 64 bf16, 4 experts (bytes: 2 us each).  A wave has
+// 440 and 206 vector instructions, eight waves a SIMD: 5.9 and 2.7 us of issue at 2.4 GHz.  With
+// the forward's exchanges through LDS and one logit a load 10.7 and 7.1 us.
 template <int TY>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
   if constexpr (TY == kEltF32) return static_cast<const float*>(p)[i];
@@ -226,8 +227,10 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(
 // blocks before it and of the experts before each expert, its waves count their own slots,
 // and each wave then walks its slots 64 at a time: a lane's place among the lanes of the same
 // expert comes from a ballot per key bit, so the order within an expert is the slots' own.
-// Bound by the launches and the dependent steps of a block, not by its 12 bytes a slot: 2.7 and
-// 4.9 us for 16384 slots, 4.8 and 10.8 us for 65542 (one launch, 74 slots: 3.2 us).
+// Bound by the launches and the steps of a block, not by its 12 bytes a slot: 2.7 and 4.9 us for
+// 16384 slots, 4.8 and 10.8 us for 65542 (one launch, 74 slots: 3.2 us).  Many experts make the
+// walk over all blocks' counts, blocks x E cells with two divisions each in every block, the
+// larger part: 131072 slots take 18.7 us with 64 experts and 196 us with 1024 (both launches).
 constexpr int kSortThreads = 512, kSortWaves = kSortThreads / kWave;
 
 __device__ __forceinline__ int sort_key(const int32_t* experts, int64_t i, int64_t end, int E) {
@@ -278,7 +281,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
       all[e] = s;
     }
   } else {
-    // threads in groups of pow2 >= E (or the whole block) walk the blocks' counts
+    // the block walks the cells of all blocks' counts, one a thread at a time
     const int64_t cells = (int64_t)gridDim.x * E;
     for (int64_t c = tid; c < cells; c += kSortThreads) {
       const int32_t v = counts[c];

@@ -10,6 +10,11 @@ by their global norm and takes the SGD step.  Parameters and rows are of one typ
 fp16), biases fp32.  The first product reads the tokens' rows in place, or with
 ``gather=False`` rows copied into the experts' order.
 
+What passes from call to call is of the rows' type too, as the calls take it: each result is
+rounded to it once, from fp32 sums.  So are the gate's logits, which the experts are chosen by,
+and the two parts of dX, the experts' and the gate's, whose sum is rounded again.  A layer that
+has to choose by fp32 logits is an fp32 layer.
+
 Every call is marshalled once on buffers that stay, so a step allocates nothing and can be
 captured into a HIP graph.  Torch adds the gate's part of dX; everything else is libctr.
 
