@@ -343,3 +343,18 @@ def test_a_captured_step_after_updates_of_other_rates():
         assert all(bool((h == 255).all()) for h in held)
         for a, b in zip(pair[0].params, pair[1].params):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gather", [True, False])
+def test_layer_without_tokens(gather, dtype):
+    """An empty batch: gradients of zero, norm 0, parameters as they were."""
+    say("layer without tokens", gather, dtype)
+    L = ExpertLayer(0, 16, 24, 1, 4, 2, dtype, gather=gather)
+    before = [p.clone() for p in L.params]
+    for g in L.grads:
+        g.fill_(-3.0)
+    assert L.forward().shape == (0, 1) and L.backward().shape == (0, 16)
+    assert all(bool((g == 0).all()) for g in L.grads)
+    assert L.update(0.1, 1.0).tolist() == [0.0, 1.0]
+    assert all(torch.equal(a, b) for a, b in zip(L.params, before))

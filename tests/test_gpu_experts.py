@@ -623,3 +623,29 @@ def test_few_rows_with_most_of_them_in_one_expert(rows, dtype):
         want, mag = ref.dense_fwd(X, W, bias, offsets, relu, o, 1, n)
         assert_near(Y, want, stored(want, (K + 3) * U32 * mag, dtype), "Y")
         untouched()
+
+
+# the tiles of both kernels: 128 and 256 wide, 64 and 128 at any width
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,k,E,K,N,pad,off", [(150, 2, 5, 136, 72, 8, 8), (150, 2, 5, 61, 33, 3, 1),
+                                               (4000, 2, 4, 2048, 96, 0, 0),
+                                               (4000, 2, 4, 1031, 40, 0, 0)])
+def test_gradient_of_rectified_rows_read_in_place(T, k, E, K, N, pad, off, dtype):
+    """x_relu with an order: dX of a position is masked by its token's row."""
+    say("rectified rows in place", T, k, E, K, N, pad, off, dtype)
+    g = gen(T + K)
+    offsets, slots, order = ref.sort(choose(g, T, E, k, 1.0, 0.1), E)
+    X = torch.relu(torch.randn((T, K), generator=g)).to(dtype)
+    W = (torch.randn((E, N, K), generator=g) * K ** -0.5).to(dtype)
+    dY = torch.randn((T * k, N), generator=g).to(dtype)
+    dX, untouched = canvas(T * k, K, pad, off, dtype)
+    _, dW, db = ctr.ctr_expert_dense_bwd(strided(X, pad, off), W.to(DEV), offsets.to(DEV),
+                                         strided(dY, pad, off), order.to(DEV), k, x_relu=True,
+                                         dX=dX)
+    want = ref.dense_bwd(X, W, offsets, dY, order, k, True)
+    v, mag, L = want["dX"]
+    assert_near(dX, v, stored(v, (L + 2) * U32 * mag, dtype), "dX")
+    untouched()
+    for got, name in ((dW, "dW"), (db, "db")):
+        v, mag, L = want[name]
+        assert_near(got, v, (L + 2) * U32 * mag, name)
