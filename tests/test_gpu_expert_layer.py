@@ -358,3 +358,31 @@ def test_layer_without_tokens(gather, dtype):
     assert all(bool((g == 0).all()) for g in L.grads)
     assert L.update(0.1, 1.0).tolist() == [0.0, 1.0]
     assert all(torch.equal(a, b) for a, b in zip(L.params, before))
+
+
+def test_calls_on_another_stream_inside_a_capture():
+    """stream= in a captured pass: forked, joined, and replayed like the eager one."""
+    say("another stream, captured")
+    side = torch.cuda.Stream()
+    calls = [c for name, c in _operators() if not name.startswith("clip")]
+    want = [tuple(ctr._tensors(call())) for call in calls]
+    torch.cuda.synchronize()
+
+    def forked():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = [tuple(ctr._tensors(call(stream=side))) for call in calls]
+        here.wait_stream(side)
+        return got
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = forked()
+    for _ in range(3):
+        for t in [t for g in got for t in g]:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for passed in (got, forked()):
+            torch.cuda.synchronize()
+            for a, b in zip([t for g in passed for t in g], [t for w in want for t in w]):
+                assert torch.equal(a, b)
