@@ -63,8 +63,10 @@ typedef enum {
 } ctr_status_t;
 
 /* Element types.  Tables: CTR_F32, CTR_BF16 or CTR_F16 (IEEE binary16, "DHEN" notes 6.4: FP16
- * embeddings); gradients, interaction operands and dZ: CTR_F32 or CTR_BF16. */
-typedef enum { CTR_F32 = 0, CTR_BF16 = 1, CTR_F16 = 2 } ctr_dtype_t;
+ * embeddings); gradients, interaction operands and dZ: CTR_F32 or CTR_BF16.  CTR_F8 (e4m3:
+ * 1 sign, 4 exponent and 3 fraction bits, largest 448, no infinity) is taken where a call says so
+ * only. */
+typedef enum { CTR_F32 = 0, CTR_BF16 = 1, CTR_F16 = 2, CTR_F8 = 3 } ctr_dtype_t;
 typedef enum { CTR_I32 = 0, CTR_I64 = 1 } ctr_index_t;
 /* Layout of sorted_src, one entry per sorted position (ctr_unique_ids writes it, the
  * backward reads it):
@@ -77,7 +79,9 @@ typedef enum { CTR_SRC_FULL = 0, CTR_SRC_ROWS = 1 } ctr_src_layout_t;
 
 /* Library version (major*10000 + minor*100 + patch).  0.2.0 added src_layout (ctr_unique_ids,
  * ctr_embbag_bwd_sgd*), out_dtype (ctr_embbag_fwd) and z_dtype (ctr_dot_interaction_fwd/bwd,
- * ctr_step_t); 0.3.0 the experts (ctr_expert_*) and gradient clipping (ctr_grad_clip*). */
+ * ctr_step_t); 0.3.0 the experts (ctr_expert_*) and gradient clipping (ctr_grad_clip*); 0.4.0 the
+ * click history (ctr_token_embed_*, ctr_rms_norm_*, ctr_quantize_rows, ctr_quant_dense_fwd,
+ * ctr_gated_scan_*). */
 int32_t ctr_version(void);
 
 /* Text of a status code (static storage). */
@@ -771,6 +775,116 @@ int32_t ctr_grad_clip_sgd(int32_t num, const void* const* grads, const int64_t* 
                           const int32_t* dtypes, void* const* params,
                           const int32_t* param_dtypes, float lr, float max_norm, float* stats,
                           void* workspace, size_t* workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------- click histories
+ * A user's clicks as a sequence: looked up token by token, normed, projected and folded into a
+ * state.  Common to these calls: dtype CTR_F32, CTR_BF16 or CTR_F16, the type of all rows of a
+ * call; parameters' gradients, weights of the norm, biases, scales and states fp32; sums,
+ * statistics and states fp32, each result rounded once (nearest-even) at its store; row strides
+ * in elements, at least the row; any alignment to the element.  n = 0 is legal.  No two arrays of
+ * a call overlap unless it says so.  All results are the same in every run (no floating-point
+ * atomics).
+ *
+ * ctr_token_embed_fwd -- Y[i, :] = scale * table[ids[i], :] for i < n; a negative id is no token
+ * and gives zeros, one from V on a row of NaN.  table: [V, D] of dtype, contiguous, V >= 1; ids:
+ * int32 or int64 [n] (id_type); Y: rows of out_dtype.  n <= 2^25, V < 2^31 - 1, 1 <= D <= 65536.
+ * ctr_token_embed_bwd -- the gradient of the whole table, dtable[v, :] = scale * sum over i with
+ * ids[i] == v of dY[i, :] (in the order of i, cut at fixed places; rows of no token are zero).
+ * Ids outside [0, V) add nothing.  dY: rows of dtype; dtable: fp32 [V, D], contiguous.
+ * Workspace: two-call query.
+ */
+int32_t ctr_token_embed_fwd(const void* table, int32_t dtype, int64_t V, int32_t D,
+                            const void* ids, int32_t id_type, int64_t n, float scale, void* Y,
+                            int32_t out_dtype, int64_t y_stride, void* stream);
+int32_t ctr_token_embed_bwd(const void* dY, int32_t dtype, int64_t dy_stride, const void* ids,
+                            int32_t id_type, int64_t n, int64_t V, int32_t D, float scale,
+                            float* dtable, void* workspace, size_t* workspace_bytes,
+                            void* stream);
+
+/*
+ * ctr_rms_norm_fwd -- root-mean-square norm of n rows of D values, after the residual's addition:
+ *   s = X + R, rounded to dtype (R NULL: s = X)             S[i, :] = s  (with R; required)
+ *   y = s * rstd * weight,  rstd = (sum of s^2 / D + eps)^(-1/2)     rstd[i]  (nullable)
+ * weight: fp32 [D] or NULL (1).  Y: y_dtype, which is dtype or CTR_F8.  CTR_F8:
+ *   t = max(largest |y| of the row, 2^-100),  y_scale[i] = t / 448,  code = e4m3(y * (448 / t))
+ * so that code * y_scale is y to within half a step of e4m3 of it (and t 2^-10 / 448 near zero); a
+ * row that holds a NaN or an infinity stands for NaN.  Rows of codes are 16-byte aligned, their
+ * stride a multiple of 16 and at least D rounded up to one; the codes from D on up to there are
+ * zeros.  S may be X or R, and Y (of dtype) may be X.  1 <= D <= 8192, eps >= 0.
+ * ctr_rms_norm_bwd -- with S the forward's s, rstd its statistic, dn = dY * weight, and dS (or NULL)
+ * the gradient that reached S by another way:
+ *   dX[i, :] = rstd (dn - S rstd^2 sum(dn S) / D) + dS     the gradient of X, and of R
+ *   dweight  = sum over i of dY S rstd                     fp32 [D], nullable
+ * dX may be dY or dS.  Workspace: two-call query.
+ * ctr_quantize_rows -- rows in 8 bits as above, with y = X.
+ */
+int32_t ctr_rms_norm_fwd(const void* X, int32_t dtype, int64_t x_stride, int64_t n, int32_t D,
+                         const void* R, int64_t r_stride, const float* weight, float eps, void* S,
+                         int64_t s_stride, void* Y, int32_t y_dtype, int64_t y_stride,
+                         float* y_scale, float* rstd, void* stream);
+int32_t ctr_rms_norm_bwd(const void* dY, int32_t dtype, int64_t dy_stride, int64_t n, int32_t D,
+                         const void* S, int64_t s_stride, const float* rstd, const float* weight,
+                         const void* dS, int64_t ds_stride, void* dX, int64_t dx_stride,
+                         float* dweight, void* workspace, size_t* workspace_bytes, void* stream);
+int32_t ctr_quantize_rows(const void* X, int32_t dtype, int64_t x_stride, int64_t n, int32_t D,
+                          void* Y, int64_t y_stride, float* y_scale, void* stream);
+
+/*
+ * ctr_quant_dense_fwd -- a fully connected layer over rows in 8 bits, for serving:
+ *   Y[m, n] = act(x_scale[m] w_scale[n] sum_k X[m, k] W[n, k] + b[n]) + R[m, n]
+ * X: CTR_F8 [M, K] and W: CTR_F8 [N, K], 16-byte aligned rows whose strides (bytes) and K are
+ * multiples of 16, as ctr_rms_norm_fwd and ctr_quantize_rows write them (the padding is part of
+ * K); products exact, sums fp32.  b: fp32 [N] or NULL.  act: CTR_ACT_*; silu x sigmoid(x), gelu
+ * x (1 + erf(x / sqrt 2)) / 2.  R: rows of dtype or NULL; Y: rows of dtype; Y may be R.
+ * 16 <= K <= 65536, 1 <= N <= 65536.
+ */
+enum { CTR_ACT_NONE = 0, CTR_ACT_RELU = 1, CTR_ACT_SILU = 2, CTR_ACT_GELU = 3 };
+int32_t ctr_quant_dense_fwd(const void* X, int64_t x_stride, int64_t M, int32_t K,
+                            const float* x_scale, const void* W, int64_t w_stride,
+                            const float* w_scale, int32_t N, const float* b, int32_t act,
+                            const void* R, int64_t r_stride, int32_t dtype, void* Y,
+                            int64_t y_stride, void* stream);
+
+/*
+ * ctr_gated_scan_fwd -- a gated linear recurrence over num_seqs sequences that lie one after the
+ * other: sequence b has the rows [offsets[b], offsets[b + 1]) of n; rows outside all of them are
+ * neither read nor written.  For every channel, with f = sigmoid(gate):
+ *   h_t = f_t h_{t-1} + (1 - f_t) value_t,   before the first row h = h0[b]  (NULL: 0)
+ *   Y_t = h_t, or h_t silu(out_gate_t)       (out_gate NULL: the former)
+ *   hN[b] = h after the last row of b, h0[b] where b has none               (nullable)
+ * gate, value, out_gate, Y: rows of D values (parts of one wider row, if need be); h0, hN: fp32
+ * [num_seqs, D]; offsets: int64 [num_seqs + 1], non-decreasing (else some numbers are wrong, and
+ * nothing outside the arrays is touched).  states: fp32 [ctr_gated_scan_chunks(n), D] or NULL, the
+ * states that the backward takes.  n <= 2^29, num_seqs < 2^31, 1 <= D <= 65536.
+ * ctr_gated_scan_bwd -- from dY and dhN (or NULL) the gradients of gate, value, out_gate (with an
+ * out_gate; else NULL) and h0 (nullable); the arrays otherwise as in the forward, states its own.
+ * Workspaces: two-call queries.
+ * ctr_gated_scan_step -- one row of each of B sequences: row i takes state[slot], slot = index[i]
+ * (NULL: i), one row further, into new_state[slot] (which may be state: in place; other slots are
+ * not written).  Rows of the same slot follow each other in their order.  A slot outside [0,
+ * num_slots) has a Y of zeros and no state.  state, new_state: fp32 [num_slots, D], contiguous;
+ * index: int32 [B].  Without index num_slots >= B.
+ */
+int64_t ctr_gated_scan_chunks(int64_t n);
+int32_t ctr_gated_scan_fwd(const void* gate, int64_t gate_stride, const void* value,
+                           int64_t value_stride, const void* out_gate, int64_t out_stride,
+                           int32_t dtype, const int64_t* offsets, int64_t n, int64_t num_seqs,
+                           int32_t D, const float* h0, void* Y, int64_t y_stride, float* hN,
+                           float* states, void* workspace, size_t* workspace_bytes, void* stream);
+int32_t ctr_gated_scan_bwd(const void* gate, int64_t gate_stride, const void* value,
+                           int64_t value_stride, const void* out_gate, int64_t out_stride,
+                           int32_t dtype, const int64_t* offsets, int64_t n, int64_t num_seqs,
+                           int32_t D, const float* h0, const float* states, const void* dY,
+                           int64_t dy_stride, const float* dhN, void* dgate, int64_t dgate_stride,
+                           void* dvalue, int64_t dvalue_stride, void* dout_gate,
+                           int64_t dout_stride, float* dh0, void* workspace,
+                           size_t* workspace_bytes, void* stream);
+int32_t ctr_gated_scan_step(const void* gate, int64_t gate_stride, const void* value,
+                            int64_t value_stride, const void* out_gate, int64_t out_stride,
+                            int32_t dtype, int64_t B, int32_t D, const int32_t* index,
+                            int64_t num_slots, const float* state, float* new_state, void* Y,
+                            int64_t y_stride, void* stream);
 
 #ifdef __cplusplus
 }

@@ -88,7 +88,7 @@ extern "C" {
 
 // 0.2.0: sorted_src layouts (src_layout), bf16 pooled vectors (out_dtype) and bf16 Z (z_dtype)
 // 0.3.0: experts (ctr_expert_*) and gradient clipping (ctr_grad_clip*)
-int32_t ctr_version(void) { return 300; }
+int32_t ctr_version(void) { return 400; }
 
 const char* ctr_status_string(int32_t status) {
   switch (status) {
@@ -1184,6 +1184,334 @@ int32_t ctr_grad_clip_sgd(int32_t num, const void* const* grads, const int64_t* 
   return hip_status(ctr::launch_grad_clip(num, grads, sizes, dtypes, params, param_dtypes, true,
                                           lr, max_norm, stats, workspace, (hipStream_t)stream),
                     "ctr_grad_clip_sgd");
+}
+
+// ------------------------------------------------------------------------- click histories
+static int32_t check_type(int32_t dtype) {
+  if (!elt_ok(dtype))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "dtype %d is not CTR_F32, CTR_BF16 or CTR_F16", dtype);
+  return CTR_OK;
+}
+
+// The two-call query: *query is set where only the size was asked for.
+static int32_t check_workspace(const void* workspace, size_t* workspace_bytes, size_t need,
+                               bool* query) {
+  *query = false;
+  if (!workspace_bytes) return fail(CTR_ERR_INVALID_ARGUMENT, "workspace_bytes is required");
+  if (!workspace) {
+    *workspace_bytes = need;
+    *query = true;
+    return CTR_OK;
+  }
+  if (*workspace_bytes < need)
+    return fail(CTR_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes (got %zu)", need,
+                *workspace_bytes);
+  if (!aligned16(workspace)) return fail(CTR_ERR_UNSUPPORTED, "workspace is not 16-byte aligned");
+  return CTR_OK;
+}
+
+static int32_t check_tokens(int32_t dtype, const void* ids, int32_t id_type, int64_t n, int64_t V,
+                            int32_t D) {
+  int32_t st = check_type(dtype);
+  if (st) return st;
+  if (id_type != CTR_I32 && id_type != CTR_I64)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "id_type %d is not CTR_I32 or CTR_I64", id_type);
+  if (n < 0 || V < 1 || V >= kMaxElems)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "need n >= 0 and V in [1, 2^31 - 1)");
+  if (n > kMaxTokens) return fail(CTR_ERR_UNSUPPORTED, "n above 2^25");
+  if (D < 1 || D > kMaxWidth) return fail(CTR_ERR_INVALID_ARGUMENT, "D must be in [1, 65536]");
+  if ((reinterpret_cast<uintptr_t>(ids) & (id_type == CTR_I64 ? 7u : 3u)) != 0)
+    return fail(CTR_ERR_UNSUPPORTED, "ids is not aligned to its elements");
+  return CTR_OK;
+}
+
+int32_t ctr_token_embed_fwd(const void* table, int32_t dtype, int64_t V, int32_t D,
+                            const void* ids, int32_t id_type, int64_t n, float scale, void* Y,
+                            int32_t out_dtype, int64_t y_stride, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_tokens(dtype, ids, id_type, n, V, D);
+  if (st) return st;
+  st = check_type(out_dtype);
+  if (st) return st;
+  if (y_stride < D) return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride < D");
+  if (n > 0 && (!table || !ids || !Y))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "table, ids and Y are required");
+  if (!elt_aligned(table, dtype) || !elt_aligned(Y, out_dtype))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_token_embed_fwd(table, dtype, V, D, ids, id_type == CTR_I64, n,
+                                                scale, Y, out_dtype, y_stride,
+                                                (hipStream_t)stream),
+                    "ctr_token_embed_fwd");
+}
+
+int32_t ctr_token_embed_bwd(const void* dY, int32_t dtype, int64_t dy_stride, const void* ids,
+                            int32_t id_type, int64_t n, int64_t V, int32_t D, float scale,
+                            float* dtable, void* workspace, size_t* workspace_bytes,
+                            void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_tokens(dtype, ids, id_type, n, V, D);
+  if (st) return st;
+  bool query;
+  st = check_workspace(workspace, workspace_bytes,
+                       ctr::token_embed_bwd_workspace_bytes(n, D, dtype), &query);
+  if (st || query) return st;
+  if (dy_stride < D) return fail(CTR_ERR_INVALID_ARGUMENT, "dy_stride < D");
+  if (!dtable || (n > 0 && (!dY || !ids)))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "dY, ids and dtable are required");
+  if (!elt_aligned(dY, dtype) || !aligned4(dtable))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_token_embed_bwd(dY, dtype, dy_stride, ids, id_type == CTR_I64, n,
+                                                V, D, scale, dtable, workspace,
+                                                (hipStream_t)stream),
+                    "ctr_token_embed_bwd");
+}
+
+static int32_t check_norm(int32_t dtype, int64_t n, int32_t D) {
+  int32_t st = check_type(dtype);
+  if (st) return st;
+  if (n < 0 || n > kMaxElems) return fail(CTR_ERR_INVALID_ARGUMENT, "n must be in [0, 2^31)");
+  if (D < 1) return fail(CTR_ERR_INVALID_ARGUMENT, "D must be at least 1");
+  if (D > 8192) return fail(CTR_ERR_UNSUPPORTED, "D %d above 8192", D);
+  return CTR_OK;
+}
+
+// Rows of 8-bit codes: whole 16-byte pieces.
+static int32_t check_codes(const void* p, int64_t stride, int64_t width, const char* name) {
+  if (stride < width)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "the stride of %s is less than its rows", name);
+  if (!aligned16(p) || stride % 16 != 0)
+    return fail(CTR_ERR_UNSUPPORTED, "%s is not in whole 16-byte pieces", name);
+  return CTR_OK;
+}
+
+int32_t ctr_rms_norm_fwd(const void* X, int32_t dtype, int64_t x_stride, int64_t n, int32_t D,
+                         const void* R, int64_t r_stride, const float* weight, float eps, void* S,
+                         int64_t s_stride, void* Y, int32_t y_dtype, int64_t y_stride,
+                         float* y_scale, float* rstd, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_norm(dtype, n, D);
+  if (st) return st;
+  const bool f8 = y_dtype == CTR_F8;
+  if (!f8 && y_dtype != dtype)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "y_dtype %d is neither dtype nor CTR_F8", y_dtype);
+  if (!(eps >= 0.f)) return fail(CTR_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+  if (x_stride < D || (R && (r_stride < D || s_stride < D)))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "strides must be at least D");
+  if (n > 0 && (!X || !Y || (R && !S) || (f8 && !y_scale)))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "X, Y (S with R, y_scale with CTR_F8) are required");
+  if (f8) {
+    st = check_codes(Y, y_stride, (D + 15) / 16 * 16, "Y");
+    if (st) return st;
+  } else if (y_stride < D) {
+    return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride < D");
+  }
+  if (!elt_aligned(X, dtype) || !elt_aligned(R, dtype) || !elt_aligned(S, dtype) ||
+      (!f8 && !elt_aligned(Y, dtype)) || !aligned4(weight) || !aligned4(y_scale) ||
+      !aligned4(rstd))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_rms_norm_fwd(X, dtype, x_stride, n, D, R, r_stride, weight, eps, S,
+                                             s_stride, Y, f8, y_stride, y_scale, rstd,
+                                             (hipStream_t)stream),
+                    "ctr_rms_norm_fwd");
+}
+
+int32_t ctr_rms_norm_bwd(const void* dY, int32_t dtype, int64_t dy_stride, int64_t n, int32_t D,
+                         const void* S, int64_t s_stride, const float* rstd, const float* weight,
+                         const void* dS, int64_t ds_stride, void* dX, int64_t dx_stride,
+                         float* dweight, void* workspace, size_t* workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_norm(dtype, n, D);
+  if (st) return st;
+  bool query;
+  st = check_workspace(workspace, workspace_bytes, ctr::rms_norm_bwd_workspace_bytes(n, D, dtype),
+                       &query);
+  if (st || query) return st;
+  if (dy_stride < D || s_stride < D || dx_stride < D || (dS && ds_stride < D))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "strides must be at least D");
+  if (n > 0 && (!dY || !S || !rstd || !dX))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "dY, S, rstd and dX are required");
+  if (!elt_aligned(dY, dtype) || !elt_aligned(S, dtype) || !elt_aligned(dS, dtype) ||
+      !elt_aligned(dX, dtype) || !aligned4(rstd) || !aligned4(weight) || !aligned4(dweight))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_rms_norm_bwd(dY, dtype, dy_stride, n, D, S, s_stride, rstd, weight,
+                                             dS, ds_stride, dX, dx_stride, dweight, workspace,
+                                             (hipStream_t)stream),
+                    "ctr_rms_norm_bwd");
+}
+
+int32_t ctr_quantize_rows(const void* X, int32_t dtype, int64_t x_stride, int64_t n, int32_t D,
+                          void* Y, int64_t y_stride, float* y_scale, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_norm(dtype, n, D);
+  if (st) return st;
+  if (x_stride < D) return fail(CTR_ERR_INVALID_ARGUMENT, "x_stride < D");
+  if (n > 0 && (!X || !Y || !y_scale))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "X, Y and y_scale are required");
+  st = check_codes(Y, y_stride, (D + 15) / 16 * 16, "Y");
+  if (st) return st;
+  if (!elt_aligned(X, dtype) || !aligned4(y_scale))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_quantize_rows(X, dtype, x_stride, n, D, Y, y_stride, y_scale,
+                                              (hipStream_t)stream),
+                    "ctr_quantize_rows");
+}
+
+int32_t ctr_quant_dense_fwd(const void* X, int64_t x_stride, int64_t M, int32_t K,
+                            const float* x_scale, const void* W, int64_t w_stride,
+                            const float* w_scale, int32_t N, const float* b, int32_t act,
+                            const void* R, int64_t r_stride, int32_t dtype, void* Y,
+                            int64_t y_stride, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_type(dtype);
+  if (st) return st;
+  if (M < 0 || M > kMaxElems) return fail(CTR_ERR_INVALID_ARGUMENT, "M must be in [0, 2^31)");
+  if (K < 1 || K > kMaxWidth || N < 1 || N > kMaxWidth)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "layer widths must be in [1, %d] (got K=%d, N=%d)",
+                kMaxWidth, K, N);
+  if (K % 16 != 0) return fail(CTR_ERR_UNSUPPORTED, "K %d is not a multiple of 16", K);
+  if (act < CTR_ACT_NONE || act > CTR_ACT_GELU)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "act %d is not a CTR_ACT_ code", act);
+  st = check_codes(X, x_stride, K, "X");
+  if (st) return st;
+  st = check_codes(W, w_stride, K, "W");
+  if (st) return st;
+  // a tile's rows lie within 2^31 bytes of its first
+  if (x_stride >= (1 << 22) || w_stride >= (1 << 22))
+    return fail(CTR_ERR_UNSUPPORTED, "x_stride and w_stride must be below 2^22");
+  if (y_stride < N || (R && r_stride < N))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride and r_stride must be at least N");
+  if ((M / 256 + 1) * (N / 256 + 1) > ((int64_t)1 << 22))
+    return fail(CTR_ERR_UNSUPPORTED, "more than 2^22 tiles of 256 x 256");
+  if (M > 0 && (!X || !x_scale || !W || !w_scale || !Y))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "X, x_scale, W, w_scale and Y are required");
+  if (!elt_aligned(R, dtype) || !elt_aligned(Y, dtype) || !aligned4(x_scale) ||
+      !aligned4(w_scale) || !aligned4(b))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_quant_dense_fwd(X, x_stride, M, K, x_scale, W, w_stride, w_scale,
+                                                N, b, act, R, r_stride, dtype, Y, y_stride,
+                                                (hipStream_t)stream),
+                    "ctr_quant_dense_fwd");
+}
+
+int64_t ctr_gated_scan_chunks(int64_t n) { return n > 0 ? ctr::gated_scan_chunks(n) : 0; }
+
+static int32_t check_scan(const void* gate, int64_t gs, const void* value, int64_t vs,
+                          const void* out_gate, int64_t os, int32_t dtype, int64_t n, int32_t D) {
+  int32_t st = check_type(dtype);
+  if (st) return st;
+  if (n < 0) return fail(CTR_ERR_INVALID_ARGUMENT, "the number of rows must be >= 0");
+  if (D < 1 || D > kMaxWidth) return fail(CTR_ERR_INVALID_ARGUMENT, "D must be in [1, 65536]");
+  if (gs < D || vs < D || (out_gate && os < D))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "strides must be at least D");
+  if (n > 0 && (!gate || !value))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "gate and value are required");
+  if (!elt_aligned(gate, dtype) || !elt_aligned(value, dtype) || !elt_aligned(out_gate, dtype))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return CTR_OK;
+}
+static int32_t check_sequences(const int64_t* offsets, int64_t n, int64_t num_seqs) {
+  if (n > ((int64_t)1 << 29)) return fail(CTR_ERR_UNSUPPORTED, "n above 2^29");
+  if (num_seqs < 0 || num_seqs > kMaxElems)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "num_seqs must be in [0, 2^31)");
+  if (!offsets) return fail(CTR_ERR_INVALID_ARGUMENT, "offsets is required");
+  if ((reinterpret_cast<uintptr_t>(offsets) & 7u) != 0)
+    return fail(CTR_ERR_UNSUPPORTED, "offsets is not aligned to its elements");
+  return CTR_OK;
+}
+// Sizes of the workspace query, which may come without arrays.
+static int32_t check_scan_query(int64_t n, int32_t D) {
+  if (n < 0 || D < 1 || D > kMaxWidth)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "need n >= 0 and D in [1, 65536]");
+  if (n > ((int64_t)1 << 29)) return fail(CTR_ERR_UNSUPPORTED, "n above 2^29");
+  return CTR_OK;
+}
+
+int32_t ctr_gated_scan_fwd(const void* gate, int64_t gate_stride, const void* value,
+                           int64_t value_stride, const void* out_gate, int64_t out_stride,
+                           int32_t dtype, const int64_t* offsets, int64_t n, int64_t num_seqs,
+                           int32_t D, const float* h0, void* Y, int64_t y_stride, float* hN,
+                           float* states, void* workspace, size_t* workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_scan_query(n, D);
+  if (st) return st;
+  bool query;
+  st = check_workspace(workspace, workspace_bytes, ctr::gated_scan_fwd_workspace_bytes(n, D),
+                       &query);
+  if (st || query) return st;
+  st = check_scan(gate, gate_stride, value, value_stride, out_gate, out_stride, dtype, n, D);
+  if (st) return st;
+  st = check_sequences(offsets, n, num_seqs);
+  if (st) return st;
+  if (y_stride < D) return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride < D");
+  if (n > 0 && !Y) return fail(CTR_ERR_INVALID_ARGUMENT, "Y is required");
+  if (!elt_aligned(Y, dtype) || !aligned4(h0) || !aligned4(hN) || !aligned4(states))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_gated_scan_fwd(gate, gate_stride, value, value_stride, out_gate,
+                                               out_gate ? out_stride : 0, dtype, offsets, n,
+                                               num_seqs, D, h0, Y, y_stride, hN, states,
+                                               workspace, (hipStream_t)stream),
+                    "ctr_gated_scan_fwd");
+}
+
+int32_t ctr_gated_scan_bwd(const void* gate, int64_t gate_stride, const void* value,
+                           int64_t value_stride, const void* out_gate, int64_t out_stride,
+                           int32_t dtype, const int64_t* offsets, int64_t n, int64_t num_seqs,
+                           int32_t D, const float* h0, const float* states, const void* dY,
+                           int64_t dy_stride, const float* dhN, void* dgate, int64_t dgate_stride,
+                           void* dvalue, int64_t dvalue_stride, void* dout_gate,
+                           int64_t dout_stride, float* dh0, void* workspace,
+                           size_t* workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_scan_query(n, D);
+  if (st) return st;
+  bool query;
+  st = check_workspace(workspace, workspace_bytes, ctr::gated_scan_bwd_workspace_bytes(n, D),
+                       &query);
+  if (st || query) return st;
+  st = check_scan(gate, gate_stride, value, value_stride, out_gate, out_stride, dtype, n, D);
+  if (st) return st;
+  st = check_sequences(offsets, n, num_seqs);
+  if (st) return st;
+  if ((out_gate != nullptr) != (dout_gate != nullptr) && n > 0)
+    return fail(CTR_ERR_INVALID_ARGUMENT, "out_gate and dout_gate go together");
+  if (dy_stride < D || dgate_stride < D || dvalue_stride < D || (out_gate && dout_stride < D))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "strides must be at least D");
+  if (n > 0 && (!states || !dY || !dgate || !dvalue))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "states, dY, dgate and dvalue are required");
+  if (!elt_aligned(dY, dtype) || !elt_aligned(dgate, dtype) || !elt_aligned(dvalue, dtype) ||
+      !elt_aligned(dout_gate, dtype) || !aligned4(h0) || !aligned4(states) || !aligned4(dhN) ||
+      !aligned4(dh0))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_gated_scan_bwd(
+                        gate, gate_stride, value, value_stride, out_gate,
+                        out_gate ? out_stride : 0, dtype, offsets, n, num_seqs, D, h0, states, dY,
+                        dy_stride, dhN, dgate, dgate_stride, dvalue, dvalue_stride, dout_gate,
+                        out_gate ? dout_stride : 0, dh0, workspace, (hipStream_t)stream),
+                    "ctr_gated_scan_bwd");
+}
+
+int32_t ctr_gated_scan_step(const void* gate, int64_t gate_stride, const void* value,
+                            int64_t value_stride, const void* out_gate, int64_t out_stride,
+                            int32_t dtype, int64_t B, int32_t D, const int32_t* index,
+                            int64_t num_slots, const float* state, float* new_state, void* Y,
+                            int64_t y_stride, void* stream) {
+  g_msg[0] = 0;
+  int32_t st = check_scan(gate, gate_stride, value, value_stride, out_gate, out_stride, dtype, B, D);
+  if (st) return st;
+  if (num_slots < 0 || num_slots > kMaxElems || (!index && num_slots < B))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "num_slots must be in [0, 2^31), and B without index");
+  if (y_stride < D) return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride < D");
+  if (B > kMaxElems || B * ((D + 255) / 256) > kMaxBlocks)
+    return fail(CTR_ERR_UNSUPPORTED, "more than 2^23 blocks of 256 channels");
+  if (B > 0 && (!Y || (num_slots > 0 && (!state || !new_state))))
+    return fail(CTR_ERR_INVALID_ARGUMENT, "state, new_state and Y are required");
+  if (!elt_aligned(Y, dtype) || !aligned4(index) || !aligned4(state) || !aligned4(new_state))
+    return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
+  return hip_status(ctr::launch_gated_scan_step(gate, gate_stride, value, value_stride, out_gate,
+                                                out_gate ? out_stride : 0, dtype, B, D, index,
+                                                num_slots, state, new_state, Y, y_stride,
+                                                (hipStream_t)stream),
+                    "ctr_gated_scan_step");
 }
 
 int32_t ctr_validate_csr(const void* indices, int32_t index_type, int64_t nnz,

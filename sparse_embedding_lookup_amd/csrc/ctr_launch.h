@@ -172,4 +172,52 @@ hipError_t launch_grad_clip(int num, const void* const* grads, const int64_t* si
                             bool sgd, float lr, float max_norm, float* stats, void* workspace,
                             hipStream_t s);
 
+// token_rows.inl (unique.hip): rows of a table by token, and the whole table's gradient
+size_t token_embed_bwd_workspace_bytes(int64_t n, int D, int dtype);
+hipError_t launch_token_embed_fwd(const void* table, int dtype, int64_t V, int D, const void* ids,
+                                  bool ids64, int64_t n, float scale, void* Y, int out_dtype,
+                                  int64_t ys, hipStream_t s);
+hipError_t launch_token_embed_bwd(const void* dY, int dtype, int64_t dys, const void* ids,
+                                  bool ids64, int64_t n, int64_t V, int D, float scale, float* dT,
+                                  void* workspace, hipStream_t s);
+
+// rms_norm.inl (dense.hip): norm with the residual's addition, rows in 8 bits
+hipError_t launch_rms_norm_fwd(const void* X, int dtype, int64_t xs, int64_t n, int D,
+                               const void* R, int64_t rs, const float* w, float eps, void* S,
+                               int64_t ss, void* Y, bool y8, int64_t ys, float* y_scale,
+                               float* rstd, hipStream_t s);
+hipError_t launch_quantize_rows(const void* X, int dtype, int64_t xs, int64_t n, int D, void* Y,
+                                int64_t ys, float* y_scale, hipStream_t s);
+size_t rms_norm_bwd_workspace_bytes(int64_t n, int D, int dtype);
+hipError_t launch_rms_norm_bwd(const void* dY, int dtype, int64_t dys, int64_t n, int D,
+                               const void* S, int64_t ss, const float* rstd, const float* w,
+                               const void* dS, int64_t dss, void* dX, int64_t dxs, float* dw,
+                               void* workspace, hipStream_t s);
+
+// quant_dense.inl (dense.hip): the product of 8-bit rows
+hipError_t launch_quant_dense_fwd(const void* X, int64_t xs, int64_t M, int K,
+                                  const float* x_scale, const void* W, int64_t ws,
+                                  const float* w_scale, int N, const float* b, int act,
+                                  const void* R, int64_t rs, int dtype, void* Y, int64_t ys,
+                                  hipStream_t s);
+
+// gated_scan.inl (fused.hip): the gated recurrence
+int64_t gated_scan_chunks(int64_t n);
+size_t gated_scan_fwd_workspace_bytes(int64_t n, int D);
+size_t gated_scan_bwd_workspace_bytes(int64_t n, int D);
+hipError_t launch_gated_scan_fwd(const void* g, int64_t gs, const void* v, int64_t vs,
+                                 const void* o, int64_t os, int dtype, const int64_t* offsets,
+                                 int64_t n, int64_t B, int D, const float* h0, void* y, int64_t ys,
+                                 float* hN, float* states, void* workspace, hipStream_t s);
+hipError_t launch_gated_scan_bwd(const void* g, int64_t gs, const void* v, int64_t vs,
+                                 const void* o, int64_t os, int dtype, const int64_t* offsets,
+                                 int64_t n, int64_t B, int D, const float* h0, const float* states,
+                                 const void* dy, int64_t dys, const float* dhN, void* dg,
+                                 int64_t dgs, void* dv, int64_t dvs, void* dout, int64_t dos,
+                                 float* dh0, void* workspace, hipStream_t s);
+hipError_t launch_gated_scan_step(const void* g, int64_t gs, const void* v, int64_t vs,
+                                  const void* o, int64_t os, int dtype, int64_t B, int D,
+                                  const int32_t* index, int64_t slots, const float* state,
+                                  float* next, void* y, int64_t ys, hipStream_t s);
+
 }  // namespace ctr

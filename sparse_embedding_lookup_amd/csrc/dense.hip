@@ -666,8 +666,11 @@ hipError_t launch_logistic_ne(const float* logits, int64_t ls, const float* labe
 
 }  // namespace ctr
 
-// The experts and the gradient clipping belong to this translation unit, so that every
-// library linked from the sources' objects holds them with the dense layers.
+// The experts, the gradient clipping, the norm and the 8-bit product belong to this translation
+// unit, so that every library linked from the sources' objects holds them with the dense layers.
 #include "expert_rows.inl"
 #include "expert_dense.inl"
 #include "grad_clip.inl"
+#include "run_io.h"
+#include "rms_norm.inl"
+#include "quant_dense.inl"

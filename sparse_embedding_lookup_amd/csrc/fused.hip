@@ -426,3 +426,8 @@ hipError_t launch_embbag_interaction_fwd(const void* table, bool table_bf16, int
 }
 
 }  // namespace ctr
+
+// The gated recurrence belongs to this translation unit, so that every library linked from the
+// sources' objects holds it.
+#include "run_io.h"
+#include "gated_scan.inl"

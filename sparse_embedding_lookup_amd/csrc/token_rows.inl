@@ -1,0 +1,438 @@
+// token_rows.inl -- rows of a table by token, scaled, and the gradient of the whole table by
+// sorted tokens.  Part of the translation unit of unique.hip, whose radix sort it uses.
+//
+//   Y[i, :]  = scale * table[ids[i], :]                        (ids[i] < 0: zeros)
+//   dT[v, :] = scale * sum over i with ids[i] == v of dY[i, :]  (fp32, rows of no token zero)
+//
+// Gradient: the tokens sorted by row, so that each row's terms are neighbours and are added in
+// the order of their positions: the same bits in every run, no atomics.
+namespace ctr {
+namespace tokens {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+template <bool ID64>
+__device__ __forceinline__ int64_t id_of(const void* ids, int64_t i) {
+  return ID64 ? static_cast<const int64_t*>(ids)[i] : (int64_t) static_cast<const int32_t*>(ids)[i];
+}
+
+// ------------------------------------------------------------------------------ forward
+// G lanes (a power of two, at most 64) take a row in runs of E elements, ROWS rows at a time, so
+// that as many loads of far rows are in flight.
+template <int TT, int TO, bool ID64, int ROWS>
+__global__ __launch_bounds__(kThreads) void fwd_kernel(const void* __restrict__ table, int64_t V,
+                                                       int D, const void* __restrict__ ids,
+                                                       int64_t n, float scale,
+                                                       void* __restrict__ Y, int64_t ys, int G) {
+  constexpr int E = TT == kEltF32 && TO == kEltF32 ? 4 : 8;
+  const int l = threadIdx.x & (G - 1);
+  const int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G * ROWS;
+  int64_t id[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) id[r] = i0 + r < n ? id_of<ID64>(ids, i0 + r) : -1;
+  for (int c = l * E; c < D; c += G * E) {
+    Run<TT, E> x[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const bool in = id[r] >= 0 && id[r] < V;
+      x[r].load_some(table, in ? id[r] * D + c : 0, in ? D - c : 0);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (i0 + r >= n) break;
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = id[r] >= V ? qnan() : x[r].at(e) * scale;
+      store_some<TO, E>(Y, (i0 + r) * ys + c, v, D - c);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- gradient
+// Key of a token: its row, or V (the last in order, summed nowhere).
+template <bool ID64>
+__device__ __forceinline__ uint32_t key_of(const void* ids, int64_t i, int64_t V) {
+  const int64_t id = id_of<ID64>(ids, i);
+  return (uint32_t)(id >= 0 && id < V ? id : V);
+}
+
+// `count` floats from p on cleared by the blocks from `first` on.
+__device__ __forceinline__ void clear(float* p, int64_t count, int first) {
+  const int64_t t = (int64_t)(blockIdx.x - first) * kThreads + threadIdx.x;
+  const int64_t step = (int64_t)(gridDim.x - first) * kThreads;
+  const int64_t head = (4 - (reinterpret_cast<uintptr_t>(p) >> 2 & 3)) & 3;   // to 16 bytes
+  const int64_t h = head < count ? head : count, whole = (count - h) / 4;
+  float4* q = reinterpret_cast<float4*>(p + h);
+  for (int64_t i = t; i < whole; i += step) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (t < h) p[t] = 0.f;
+  if (t < count - h - 4 * whole) p[h + 4 * whole + t] = 0.f;
+}
+
+// The keys in token order, and the table's gradient cleared.
+template <bool ID64>
+__global__ __launch_bounds__(kThreads) void keys_kernel(const void* __restrict__ ids, int64_t n,
+                                                        int64_t V, int key_blocks,
+                                                        uint32_t* __restrict__ keys,
+                                                        float* __restrict__ dT, int64_t count) {
+  if ((int)blockIdx.x >= key_blocks) {
+    clear(dT, count, key_blocks);
+    return;
+  }
+  const int64_t step = (int64_t)key_blocks * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step)
+    keys[i] = key_of<ID64>(ids, i, V);
+}
+
+// Few tokens: sorted in this launch.  A token's place is the number of tokens before it in
+// order; a block has 16 tokens and each of them 16 threads, which compare it with every
+// sixteenth of all.
+constexpr int kRankTile = 4096, kRankOf = 16;
+template <bool ID64>
+__global__ __launch_bounds__(kThreads) void rank_kernel(const void* __restrict__ ids, int n,
+                                                        int64_t V, int key_blocks,
+                                                        uint32_t* __restrict__ sk,
+                                                        uint32_t* __restrict__ sv,
+                                                        float* __restrict__ dT, int64_t count) {
+  if ((int)blockIdx.x >= key_blocks) {
+    clear(dT, count, key_blocks);
+    return;
+  }
+  __shared__ uint32_t tile[kRankTile];
+  const int t = threadIdx.x, i = (int)blockIdx.x * kRankOf + t / kRankOf, part = t % kRankOf;
+  const uint32_t key = i < n ? key_of<ID64>(ids, i, V) : kNone;
+  int before = 0;
+  for (int t0 = 0; t0 < n; t0 += kRankTile) {
+    const int m = n - t0 < kRankTile ? n - t0 : kRankTile;
+    __syncthreads();
+    for (int j = t; j < m; j += kThreads) tile[j] = key_of<ID64>(ids, t0 + j, V);
+    __syncthreads();
+#pragma unroll 8
+    for (int j = part; j < m; j += kRankOf) {
+      const uint32_t k = tile[j];
+      before += k < key || (k == key && t0 + j < i);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kRankOf; d <<= 1) before += __shfl_xor(before, d);
+  if (i < n && part == 0) {
+    sk[before] = key;
+    sv[before] = (uint32_t)i;
+  }
+}
+
+// Sums of the sorted tokens' rows.  A block has 256 / G groups of G lanes, a group `chunk`
+// neighbouring sorted positions and a lane E columns of them.  A group stores the sums of the
+// rows that begin and end inside it; its first and its last go through LDS, where one group
+// joins them in order.  What a block shares with its neighbours (the rows of its first and last
+// position) goes to `part`, two sums a block, for join_kernel.
+struct Sums {
+  const uint32_t* sk;
+  const uint32_t* sv;
+  int64_t n;
+  uint32_t V;
+  const void* dY;
+  int64_t dys;
+  int D, G, chunk;
+  float scale;
+  float* dT;
+  float* part;                  // [2 * blocks, D]: of the row that came in, of the row that goes on
+  uint32_t* part_key;           // [2 * blocks], kNone: there is none
+};
+
+template <int TY>
+constexpr int kSumElts = TY == kEltF32 ? 4 : 8;
+
+template <int N>
+__device__ __forceinline__ void put_sum(float* row, int c, int D, const float* s, float scale) {
+  float v[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = s[e] * scale;
+  store_some<kEltF32, N>(row, c, v, D - c);
+}
+
+template <int TY>
+__global__ __launch_bounds__(kThreads) void sum_kernel(Sums g) {
+  constexpr int E = kSumElts<TY>, DEEP = 8;
+  __shared__ float sums[2][kThreads * E];
+  __shared__ uint32_t keys[2][kThreads];
+  const int t = threadIdx.x, l = t & (g.G - 1), group = t / g.G, groups = kThreads / g.G;
+  const int c = ((int)blockIdx.y * g.G + l) * E;
+  const int there = c < g.D ? g.D - c : 0;
+  const int64_t a = ((int64_t)blockIdx.x * groups + group) * g.chunk;
+  const int64_t b = a + g.chunk < g.n ? a + g.chunk : g.n;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  uint32_t cur = kNone, first = kNone;
+  bool head = true;
+  for (int64_t p = a; p < b; p += DEEP) {
+    uint32_t key[DEEP], row[DEEP];
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      const bool in = p + i < b;
+      key[i] = in ? g.sk[p + i] : kNone;
+      row[i] = in ? g.sv[p + i] : 0u;
+    }
+    Run<TY, E> x[DEEP];
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      const bool in = key[i] < g.V;
+      x[i].load_some(g.dY, in ? (int64_t)row[i] * g.dys + c : 0, in ? there : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      if (p + i >= b) break;
+      if (key[i] != cur) {
+        if (cur != kNone) {
+          if (head) {
+            first = cur;
+#pragma unroll
+            for (int e = 0; e < E; ++e) sums[0][e * kThreads + t] = acc[e];
+            head = false;
+          } else if (cur < g.V && there > 0) {
+            put_sum<E>(g.dT + (int64_t)cur * g.D, c, g.D, acc, g.scale);
+          }
+        }
+        cur = key[i];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += x[i].at(e);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sums[1][e * kThreads + t] = acc[e];
+  keys[0][t] = first;
+  keys[1][t] = cur;
+  __syncthreads();
+  if (group != 0) return;
+  const int64_t lo = (int64_t)blockIdx.x * groups * g.chunk;
+  const int64_t hi = lo + (int64_t)groups * g.chunk < g.n ? lo + (int64_t)groups * g.chunk : g.n;
+  const uint32_t came = lo > 0 ? g.sk[lo - 1] : kNone, goes = hi < g.n ? g.sk[hi] : kNone;
+  uint32_t in = kNone, on = kNone;
+  float s[E];
+  uint32_t run = kNone;
+  auto emit = [&] {
+    if (run >= g.V) return;                    // no row, or that of no token
+    if (run == came) {
+      in = run;
+      if (there > 0) put_sum<E>(g.part + (int64_t)blockIdx.x * 2 * g.D, c, g.D, s, 1.f);
+    } else if (run == goes) {
+      on = run;
+      if (there > 0) put_sum<E>(g.part + ((int64_t)blockIdx.x * 2 + 1) * g.D, c, g.D, s, 1.f);
+    } else if (there > 0) {
+      put_sum<E>(g.dT + (int64_t)run * g.D, c, g.D, s, g.scale);
+    }
+  };
+  for (int u = 0; u < groups; ++u)
+    for (int q = 0; q < 2; ++q) {
+      const int at = u * g.G + l;
+      const uint32_t key = keys[q][at];
+      if (key == kNone) continue;
+      if (key != run) {
+        emit();
+        run = key;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] = sums[q][e * kThreads + at];
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] += sums[q][e * kThreads + at];
+      }
+    }
+  emit();
+  if (l == 0 && blockIdx.y == 0) {
+    g.part_key[2 * blockIdx.x] = in;
+    g.part_key[2 * blockIdx.x + 1] = on;
+  }
+}
+
+// The rows that several blocks share: the block where one begins adds what goes on from there
+// and what came into the blocks after it, each group every 256 / G-th of them, then the groups'
+// sums in order.
+template <int E>
+__global__ __launch_bounds__(kThreads) void join_kernel(Sums g, int64_t blocks) {
+  __shared__ float sums[kThreads * E];
+  const uint32_t key = g.part_key[2 * blockIdx.x + 1];
+  if (key == kNone) return;                    // the same in the whole block
+  const int t = threadIdx.x, l = t & (g.G - 1), group = t / g.G, groups = kThreads / g.G;
+  const int c = ((int)blockIdx.y * g.G + l) * E;
+  const int there = c < g.D ? g.D - c : 0;
+  float s[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e] = 0.f;
+  constexpr int DEEP = 4;
+  bool more = true;
+  for (int64_t j = (int64_t)blockIdx.x + 1 + group; more && j < blocks; j += DEEP * groups) {
+    Run<kEltF32, E> x[DEEP];
+    bool in[DEEP];
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      const int64_t k = j + i * groups;
+      in[i] = k < blocks && g.part_key[2 * k] == key;
+    }
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i)
+      x[i].load_some(g.part, in[i] ? 2 * (j + i * groups) * g.D + c : 0, in[i] ? there : 0);
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[e] += x[i].at(e);
+    more = in[DEEP - 1];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sums[e * kThreads + t] = s[e];
+  __syncthreads();
+  if (group != 0 || there == 0) return;
+  Run<kEltF32, E> x;
+  x.load_some(g.part, (2 * (int64_t)blockIdx.x + 1) * g.D + c, there);
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e] = x.at(e);
+  for (int u = 0; u < groups; ++u)
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[e] += sums[e * kThreads + u * g.G + l];
+  put_sum<E>(g.dT + (int64_t)key * g.D, c, g.D, s, g.scale);
+}
+
+// Lanes a row of D elements in runs of E: a power of two, at most 64.
+int lanes(int D, int E) {
+  int G = 1;
+  while (G < 64 && G * E < D) G <<= 1;
+  return G;
+}
+
+constexpr int64_t kRankMost = 4096;
+
+int key_bits(int64_t V) {
+  int b = 1;
+  while (V >> b) ++b;
+  return b;
+}
+
+// Sorted positions a group takes: enough blocks for the chip first, then longer runs, which
+// leave fewer sums to join.
+int chunk_of(int64_t n, int G) {
+  const int64_t groups = kThreads / G;
+  int chunk = 8;
+  while (chunk < 32 && n > 1024 * groups * chunk) chunk *= 2;
+  return chunk;
+}
+
+struct Workspace {
+  uint32_t* keys[2];
+  uint32_t* vals[2];
+  uint32_t* hist;
+  uint32_t* totals;
+  float* part;
+  uint32_t* part_key;
+  int64_t blocks;
+  size_t bytes;
+};
+Workspace carve_tokens(void* base, int64_t n, int D, int E) {
+  Workspace w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base ? static_cast<char*>(base) + off : nullptr;
+    off += align256(bytes);
+    return p;
+  };
+  for (int i = 0; i < 2; ++i) w.keys[i] = reinterpret_cast<uint32_t*>(take(4 * (size_t)n));
+  for (int i = 0; i < 2; ++i) w.vals[i] = reinterpret_cast<uint32_t*>(take(4 * (size_t)n));
+  w.hist = reinterpret_cast<uint32_t*>(take(4 * (size_t)kBuckets * kMaxBlocks));
+  w.totals = reinterpret_cast<uint32_t*>(take(4 * (size_t)kBuckets));
+  const int G = lanes(D, E);
+  const int64_t each = (int64_t)(kThreads / G) * chunk_of(n, G);
+  w.blocks = (n + each - 1) / each;
+  w.part = reinterpret_cast<float*>(take(8 * (size_t)w.blocks * (size_t)D));
+  w.part_key = reinterpret_cast<uint32_t*>(take(8 * (size_t)w.blocks));
+  w.bytes = off;
+  return w;
+}
+
+}  // namespace tokens
+
+size_t token_embed_bwd_workspace_bytes(int64_t n, int D, int dtype) {
+  return tokens::carve_tokens(nullptr, n, D, dtype == kEltF32 ? 4 : 8).bytes;
+}
+
+hipError_t launch_token_embed_fwd(const void* table, int dtype, int64_t V, int D, const void* ids,
+                                  bool ids64, int64_t n, float scale, void* Y, int out_dtype,
+                                  int64_t ys, hipStream_t s) {
+  if (n == 0) return hipSuccess;
+  return for_type(dtype, [&](auto tt) {
+    return for_type(out_dtype, [&](auto to) {
+      constexpr int TT = decltype(tt)::value, TO = decltype(to)::value;
+      const int G = tokens::lanes(D, TT == kEltF32 && TO == kEltF32 ? 4 : 8);
+      // one row a group until that fills the chip, then four
+      auto launch = [&](auto id64, auto rows) {
+        constexpr int R = decltype(rows)::value;
+        const int64_t groups = (n + R - 1) / R, per = tokens::kThreads / G;
+        tokens::fwd_kernel<TT, TO, decltype(id64)::value, R>
+            <<<(unsigned)((groups + per - 1) / per), tokens::kThreads, 0, s>>>(
+                table, V, D, ids, n, scale, Y, ys, G);
+        return hipGetLastError();
+      };
+      auto by_id = [&](auto rows) {
+        return ids64 ? launch(std::true_type{}, rows) : launch(std::false_type{}, rows);
+      };
+      return n * G < (int64_t)1 << 18 ? by_id(std::integral_constant<int, 1>{})
+                                      : by_id(std::integral_constant<int, 4>{});
+    });
+  });
+}
+
+hipError_t launch_token_embed_bwd(const void* dY, int dtype, int64_t dys, const void* ids,
+                                  bool ids64, int64_t n, int64_t V, int D, float scale, float* dT,
+                                  void* workspace, hipStream_t s) {
+  const int64_t count = V * D;
+  const int E = dtype == kEltF32 ? 4 : 8;
+  tokens::Workspace w = tokens::carve_tokens(workspace, n, D, E);
+  int64_t clear = (count + 16 * tokens::kThreads - 1) / (16 * tokens::kThreads);
+  if (clear > 4096) clear = 4096;
+  const uint32_t* sk = w.keys[0];
+  const uint32_t* sv = w.vals[0];
+  if (n <= tokens::kRankMost) {
+    const int kb = (int)((n + tokens::kRankOf - 1) / tokens::kRankOf);
+    if (kb + clear == 0) return hipSuccess;
+    if (ids64)
+      tokens::rank_kernel<true><<<(unsigned)(kb + clear), tokens::kThreads, 0, s>>>(
+          ids, (int)n, V, kb, w.keys[0], w.vals[0], dT, count);
+    else
+      tokens::rank_kernel<false><<<(unsigned)(kb + clear), tokens::kThreads, 0, s>>>(
+          ids, (int)n, V, kb, w.keys[0], w.vals[0], dT, count);
+  } else {
+    int64_t kb = (n + 4 * tokens::kThreads - 1) / (4 * tokens::kThreads);
+    if (kb > 2048) kb = 2048;
+    if (ids64)
+      tokens::keys_kernel<true><<<(unsigned)(kb + clear), tokens::kThreads, 0, s>>>(
+          ids, n, V, (int)kb, w.keys[0], dT, count);
+    else
+      tokens::keys_kernel<false><<<(unsigned)(kb + clear), tokens::kThreads, 0, s>>>(
+          ids, n, V, (int)kb, w.keys[0], dT, count);
+    const uint16_t* none;
+    const int bits = tokens::key_bits(V);
+    if (n <= (1 << 20))
+      radix_sort<uint32_t, 4>(bits, w.keys[0], w.keys[1], w.vals[0], w.vals[1], nullptr, nullptr,
+                              n, w.hist, w.totals, &sk, &sv, &none, nullptr, s);
+    else
+      radix_sort<uint32_t, 8>(bits, w.keys[0], w.keys[1], w.vals[0], w.vals[1], nullptr, nullptr,
+                              n, w.hist, w.totals, &sk, &sv, &none, nullptr, s);
+  }
+  if (n == 0) return hipGetLastError();
+  tokens::Sums g{};
+  g.sk = sk; g.sv = sv; g.n = n; g.V = (uint32_t)V;
+  g.dY = dY; g.dys = dys; g.D = D; g.scale = scale; g.dT = dT;
+  g.part = w.part; g.part_key = w.part_key;
+  g.G = tokens::lanes(D, E);
+  g.chunk = tokens::chunk_of(n, g.G);
+  const dim3 grid((unsigned)w.blocks, (unsigned)((D + g.G * E - 1) / (g.G * E)));
+  return for_type(dtype, [&](auto ty) {
+    constexpr int TY = decltype(ty)::value;
+    tokens::sum_kernel<TY><<<grid, tokens::kThreads, 0, s>>>(g);
+    tokens::join_kernel<tokens::kSumElts<TY>><<<grid, tokens::kThreads, 0, s>>>(g, w.blocks);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace ctr

@@ -21,7 +21,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("CTR_LIB") or os.path.join(_HERE, "libctr.so")
 
 CTR_OK, CTR_ERR_INVALID_ARGUMENT, CTR_ERR_UNSUPPORTED, CTR_ERR_WORKSPACE_TOO_SMALL, CTR_ERR_HIP = range(5)
-CTR_F32, CTR_BF16, CTR_F16 = 0, 1, 2
+CTR_F32, CTR_BF16, CTR_F16, CTR_F8 = 0, 1, 2, 3
 CTR_I32, CTR_I64 = 0, 1
 
 EXPORTED = [
@@ -41,6 +41,9 @@ EXPORTED = [
     "ctr_expert_route_fwd", "ctr_expert_route_bwd", "ctr_expert_sort", "ctr_expert_dispatch",
     "ctr_expert_combine_fwd", "ctr_expert_combine_bwd", "ctr_expert_dense_fwd",
     "ctr_expert_dense_bwd", "ctr_grad_clip", "ctr_grad_clip_sgd",
+    "ctr_token_embed_fwd", "ctr_token_embed_bwd", "ctr_rms_norm_fwd", "ctr_rms_norm_bwd",
+    "ctr_quantize_rows", "ctr_quant_dense_fwd", "ctr_gated_scan_chunks", "ctr_gated_scan_fwd",
+    "ctr_gated_scan_bwd", "ctr_gated_scan_step",
 ]
 
 CTR_STEP_POOLED_INTERACTION, CTR_STEP_BATCH_MATRIX = 0, 1
@@ -49,6 +52,7 @@ CTR_SCHEDULE_PIPELINED_OVERLAP = 3
 CTR_ROUND_NEAREST, CTR_ROUND_STOCHASTIC = 0, 1
 CTR_MARK_POOLING, CTR_MARK_BACKWARD = 0, 1
 CTR_SRC_FULL, CTR_SRC_ROWS = 0, 1
+CTR_ACT_NONE, CTR_ACT_RELU, CTR_ACT_SILU, CTR_ACT_GELU = range(4)
 
 
 class CtrStep(ctypes.Structure):
@@ -150,6 +154,22 @@ def load() -> ctypes.CDLL:
                                        P, i64, P, i64, P, P, P, PS, P]),
         "ctr_grad_clip": (i32, [i32, P, P, P, P, f32, P, P, PS, P]),
         "ctr_grad_clip_sgd": (i32, [i32, P, P, P, P, P, f32, f32, P, P, PS, P]),
+        "ctr_token_embed_fwd": (i32, [P, i32, i64, i32, P, i32, i64, f32, P, i32, i64, P]),
+        "ctr_token_embed_bwd": (i32, [P, i32, i64, P, i32, i64, i64, i32, f32, P, P, PS, P]),
+        "ctr_rms_norm_fwd": (i32, [P, i32, i64, i64, i32, P, i64, P, f32, P, i64, P, i32, i64, P,
+                                   P, P]),
+        "ctr_rms_norm_bwd": (i32, [P, i32, i64, i64, i32, P, i64, P, P, P, i64, P, i64, P, P, PS,
+                                   P]),
+        "ctr_quantize_rows": (i32, [P, i32, i64, i64, i32, P, i64, P, P]),
+        "ctr_quant_dense_fwd": (i32, [P, i64, i64, i32, P, P, i64, P, i32, P, i32, P, i64, i32, P,
+                                      i64, P]),
+        "ctr_gated_scan_chunks": (i64, [i64]),
+        "ctr_gated_scan_fwd": (i32, [P, i64, P, i64, P, i64, i32, P, i64, i64, i32, P, P, i64, P,
+                                     P, P, PS, P]),
+        "ctr_gated_scan_bwd": (i32, [P, i64, P, i64, P, i64, i32, P, i64, i64, i32, P, P, P, i64,
+                                     P, P, i64, P, i64, P, i64, P, P, PS, P]),
+        "ctr_gated_scan_step": (i32, [P, i64, P, i64, P, i64, i32, i64, i32, P, i64, P, P, P, i64,
+                                      P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -1080,6 +1100,359 @@ def ctr_grad_clip_sgd(grads: Sequence[torch.Tensor], params: Sequence[torch.Tens
     gradients are kept.  Returns stats [norm, scale] (device)."""
     return _clip_call("ctr_grad_clip_sgd", grads, params, lr, max_norm, stats, workspace, stream,
                       prepare, "params")
+
+
+# ----------------------------------------------------------------------- click histories
+F8 = torch.float8_e4m3fn
+ACTS = {"none": CTR_ACT_NONE, "relu": CTR_ACT_RELU, "silu": CTR_ACT_SILU, "gelu": CTR_ACT_GELU}
+
+
+def _launch_here(name: str, device: torch.device, args: tuple, prepare: bool, result=None,
+                 keep=None):
+    """_launch of arguments that are all on the current device, whose current stream it takes."""
+    if device.type == "cuda" and device.index != torch._C._cuda_getDevice():
+        raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
+                         % (name, device, torch._C._cuda_getDevice()))
+    return _launch(name, device, args, prepare, result, keep)
+
+
+def _queried(name: str, args: tuple) -> int:
+    """Bytes of a workspace (the library's two-call query)."""
+    wsb = ctypes.c_size_t(0)
+    _check(name, getattr(load(), name)(*args, None, ctypes.byref(wsb), None))
+    return wsb.value
+
+
+@functools.lru_cache(maxsize=1024)
+def token_embed_bwd_workspace_bytes(n: int, num_rows: int, dim: int, dtype: int) -> int:
+    """Workspace of ctr_token_embed_bwd."""
+    return _queried("ctr_token_embed_bwd",
+                    (None, dtype, dim, None, CTR_I64, n, num_rows, dim, 1.0, None))
+
+
+@functools.lru_cache(maxsize=1024)
+def rms_norm_bwd_workspace_bytes(n: int, dim: int, dtype: int) -> int:
+    """Workspace of ctr_rms_norm_bwd."""
+    return _queried("ctr_rms_norm_bwd", (None, dtype, dim, n, dim, None, dim, None, None, None, dim,
+                                         None, dim, None))
+
+
+@functools.lru_cache(maxsize=1024)
+def gated_scan_fwd_workspace_bytes(n: int, dim: int) -> int:
+    """Workspace of ctr_gated_scan_fwd."""
+    return _queried("ctr_gated_scan_fwd", (None, dim, None, dim, None, dim, CTR_F32, None, n, 0,
+                                           dim, None, None, dim, None, None))
+
+
+@functools.lru_cache(maxsize=1024)
+def gated_scan_bwd_workspace_bytes(n: int, dim: int) -> int:
+    """Workspace of ctr_gated_scan_bwd."""
+    return _queried("ctr_gated_scan_bwd",
+                    (None, dim, None, dim, None, dim, CTR_F32, None, n, 0, dim, None, None, None,
+                     dim, None, None, dim, None, dim, None, dim, None))
+
+
+def _token_ids(ids: torch.Tensor, dev) -> tuple:
+    """(address, type code, number) of a list of tokens."""
+    if ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous list")
+    if ids.device != dev:
+        raise ValueError("ids is on %s, not %s" % (ids.device, dev))
+    return ids.data_ptr(), _index_code(ids), ids.shape[0]
+
+
+def ctr_token_embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
+                        Y: Optional[torch.Tensor] = None,
+                        out_dtype: Optional[torch.dtype] = None, stream=None,
+                        prepare: bool = False):
+    """Y [n, D] = scale * table[ids] with table [V, D] and ids int32 or int64 [n]; a negative id
+    is no token and gives zeros, one from V on a row of NaN.  Y is of Y's type, or out_dtype (the
+    table's unless given)."""
+    if stream is not None:
+        return _on(stream, ctr_token_embed_fwd, table, ids, scale, Y, out_dtype, prepare=prepare)
+    code, dev = _expert_type(table, "table"), table.device
+    if table.dim() != 2:
+        raise ValueError("table must be [V, D]")
+    V, D = table.shape
+    tp = _expert_arg(table, "table", (V, D), table.dtype, dev)
+    ip, itype, n = _token_ids(ids, dev)
+    out_dtype = out_dtype or (table.dtype if Y is None else Y.dtype)
+    if out_dtype not in _DTYPE_CODES:
+        raise TypeError("Y must be float32, bfloat16 or float16, not %s" % out_dtype)
+    Y, yp, ys = _matrix(Y, "Y", n, D, out_dtype, dev)
+    args = (tp, code, V, D, ip, itype, n, float(scale), yp, _DTYPE_CODES[out_dtype], ys)
+    return _launch_here("ctr_token_embed_fwd", dev, args, prepare, Y)
+
+
+def ctr_token_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, num_rows: int, scale: float = 1.0,
+                        dtable: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None,
+                        prepare: bool = False):
+    """The gradient of the whole table, fp32 [num_rows, D]: scale times the sum of the tokens'
+    rows of dY [n, D], zeros for rows of no token.  Ids outside [0, num_rows) add nothing."""
+    if stream is not None:
+        return _on(stream, ctr_token_embed_bwd, dY, ids, num_rows, scale, dtable, workspace,
+                   prepare=prepare)
+    code, dev = _expert_type(dY, "dY"), dY.device
+    ip, itype, n = _token_ids(ids, dev)
+    D = dY.shape[-1]
+    yp, dys = _rows_arg(dY, "dY", (n, D), dY.dtype, dev)
+    dtable, tp = _dense(dtable, "dtable", (num_rows, D), (D, 1), torch.float32, dev)
+    if workspace is None:
+        workspace = _workspace(token_embed_bwd_workspace_bytes(n, num_rows, D, code), dev)
+    wsb = ctypes.c_size_t(workspace.numel())
+    args = (yp, code, dys, ip, itype, n, num_rows, D, float(scale), tp, workspace.data_ptr(),
+            ctypes.byref(wsb))
+    return _launch_here("ctr_token_embed_bwd", dev, args, prepare, dtable, workspace)
+
+
+def _codes_out(out: Optional[torch.Tensor], name: str, rows: int, width: int, dev) -> tuple:
+    """An output of 8-bit rows: (tensor [rows, width to a multiple of 16], address, row stride)."""
+    return _matrix(out, name, rows, (width + 15) // 16 * 16, F8, dev)
+
+
+def ctr_rms_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor],
+                     residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     quantize: bool = False, want_rstd: bool = False,
+                     S: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                     y_scale: Optional[torch.Tensor] = None,
+                     rstd: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """(Y, y_scale, S, rstd) of the rows X [n, D]: S = X + residual in their type (X itself without
+    residual), Y = S * rstd * weight with rstd fp32 [n] (None unless wanted, for the backward) the
+    inverse root of S's mean square plus eps, weight fp32 [D] or None.  quantize: Y in 8 bits
+    (float8_e4m3fn [n, D to a multiple of 16], zeros behind the row), worth Y * y_scale with
+    y_scale fp32 [n]; else y_scale is None."""
+    if stream is not None:
+        return _on(stream, ctr_rms_norm_fwd, X, weight, residual, eps, quantize, want_rstd, S, Y,
+                   y_scale, rstd, prepare=prepare)
+    code, xs, dev = _expert_type(X, "X"), _row_stride(X, "X"), X.device
+    n, D = X.shape
+    rp, rs, sp, ss = None, D, None, D
+    if residual is not None:
+        rp, rs = _rows_arg(residual, "residual", (n, D), X.dtype, dev)
+        S, sp, ss = _matrix(S, "S", n, D, X.dtype, dev)
+    elif S is not None:
+        raise ValueError("S needs a residual")
+    wp = None if weight is None else _expert_arg(weight, "weight", (D,), torch.float32, dev)
+    cp, qp, ycode = None, None, code
+    if want_rstd or rstd is not None:
+        rstd, qp = _dense(rstd, "rstd", (n,), (1,), torch.float32, dev)
+    if quantize:
+        Y, yp, ys = _codes_out(Y, "Y", n, D, dev)
+        y_scale, cp = _dense(y_scale, "y_scale", (n,), (1,), torch.float32, dev)
+        ycode = CTR_F8
+    else:
+        if y_scale is not None:
+            raise ValueError("y_scale needs quantize")
+        Y, yp, ys = _matrix(Y, "Y", n, D, X.dtype, dev)
+    args = (X.data_ptr(), code, xs, n, D, rp, rs, wp, float(eps), sp, ss, yp, ycode, ys, cp, qp)
+    return _launch_here("ctr_rms_norm_fwd", dev, args, prepare,
+                        (Y, y_scale, S if residual is not None else X, rstd))
+
+
+def ctr_rms_norm_bwd(dY: torch.Tensor, S: torch.Tensor, rstd: torch.Tensor,
+                     weight: Optional[torch.Tensor], dS: Optional[torch.Tensor] = None,
+                     want_dw: bool = True, dX: Optional[torch.Tensor] = None,
+                     dweight: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None,
+                     prepare: bool = False):
+    """(dX [n, D], dweight fp32 [D]) from dY, the forward's S and rstd, and dS, the gradient that
+    reached S by another way.  dX is the gradient of X and of the residual; without want_dw
+    dweight is None."""
+    if stream is not None:
+        return _on(stream, ctr_rms_norm_bwd, dY, S, rstd, weight, dS, want_dw, dX, dweight,
+                   workspace, prepare=prepare)
+    code, ys, dev = _expert_type(dY, "dY"), _row_stride(dY, "dY"), dY.device
+    n, D = dY.shape
+    sp, ss = _rows_arg(S, "S", (n, D), dY.dtype, dev)
+    gp, gs = (None, D) if dS is None else _rows_arg(dS, "dS", (n, D), dY.dtype, dev)
+    dX, xp, xs = _matrix(dX, "dX", n, D, dY.dtype, dev)
+    wp = None if weight is None else _expert_arg(weight, "weight", (D,), torch.float32, dev)
+    dwp = None
+    if want_dw:
+        dweight, dwp = _dense(dweight, "dweight", (D,), (1,), torch.float32, dev)
+    if workspace is None:
+        workspace = _workspace(rms_norm_bwd_workspace_bytes(n, D, code), dev)
+    wsb = ctypes.c_size_t(workspace.numel())
+    args = (dY.data_ptr(), code, ys, n, D, sp, ss,
+            _expert_arg(rstd, "rstd", (n,), torch.float32, dev), wp, gp, gs, xp, xs, dwp,
+            workspace.data_ptr(), ctypes.byref(wsb))
+    return _launch_here("ctr_rms_norm_bwd", dev, args, prepare,
+                        (dX, dweight if want_dw else None), workspace)
+
+
+def ctr_quantize_rows(X: torch.Tensor, Y: Optional[torch.Tensor] = None,
+                      y_scale: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """(Y, y_scale): the rows X [n, D] in 8 bits, worth Y * y_scale (see ctr_rms_norm_fwd)."""
+    if stream is not None:
+        return _on(stream, ctr_quantize_rows, X, Y, y_scale, prepare=prepare)
+    code, xs, dev = _expert_type(X, "X"), _row_stride(X, "X"), X.device
+    n, D = X.shape
+    Y, yp, ys = _codes_out(Y, "Y", n, D, dev)
+    y_scale, cp = _dense(y_scale, "y_scale", (n,), (1,), torch.float32, dev)
+    args = (X.data_ptr(), code, xs, n, D, yp, ys, cp)
+    return _launch_here("ctr_quantize_rows", dev, args, prepare, (Y, y_scale))
+
+
+def ctr_quant_dense_fwd(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor,
+                        w_scale: torch.Tensor, b: Optional[torch.Tensor] = None,
+                        act: str = "none", residual: Optional[torch.Tensor] = None,
+                        Y: Optional[torch.Tensor] = None,
+                        out_dtype: Optional[torch.dtype] = None, stream=None,
+                        prepare: bool = False):
+    """Y [M, N] = act((X x_scale) (W w_scale)^T + b) + residual of 8-bit rows X [M, K] and W [N, K]
+    with a scale each, as ctr_rms_norm_fwd and ctr_quantize_rows give them; act: none, relu, silu
+    or gelu.  Y is of Y's type, or out_dtype (the residual's, or bfloat16).  Y may be the
+    residual."""
+    if stream is not None:
+        return _on(stream, ctr_quant_dense_fwd, X, x_scale, W, w_scale, b, act, residual, Y,
+                   out_dtype, prepare=prepare)
+    if act not in ACTS:
+        raise ValueError("act must be one of %s, not %r" % (", ".join(ACTS), act))
+    dev = X.device
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X must be [M, K] and W [N, K]")
+    M, K = X.shape
+    N = W.shape[0]
+    xp, xs = _rows_arg(X, "X", (M, K), F8, dev)
+    wp, ws = _rows_arg(W, "W", (N, K), F8, dev)
+    given = Y if Y is not None else residual
+    out_dtype = out_dtype or (torch.bfloat16 if given is None else given.dtype)
+    if out_dtype not in _DTYPE_CODES:
+        raise TypeError("Y must be float32, bfloat16 or float16, not %s" % out_dtype)
+    rp, rs = (None, N) if residual is None else _rows_arg(residual, "residual", (M, N), out_dtype,
+                                                          dev)
+    Y, yp, ys = _matrix(Y, "Y", M, N, out_dtype, dev)
+    bp = None if b is None else _expert_arg(b, "b", (N,), torch.float32, dev)
+    args = (xp, xs, M, K, _expert_arg(x_scale, "x_scale", (M,), torch.float32, dev), wp, ws,
+            _expert_arg(w_scale, "w_scale", (N,), torch.float32, dev), N, bp, ACTS[act], rp, rs,
+            _DTYPE_CODES[out_dtype], yp, ys)
+    return _launch_here("ctr_quant_dense_fwd", dev, args, prepare, Y)
+
+
+def ctr_gated_scan_chunks(n: int) -> int:
+    """Rows of the states that ctr_gated_scan_fwd leaves for the backward."""
+    return int(load().ctr_gated_scan_chunks(n))
+
+
+def _scan_args(gate, value, out_gate):
+    """The rows of a scan: (their first arguments, n, D, type)."""
+    code, gs, dev = _expert_type(gate, "gate"), _row_stride(gate, "gate"), gate.device
+    n, D = gate.shape
+    vp, vs = _rows_arg(value, "value", (n, D), gate.dtype, dev)
+    op, os_ = (None, D) if out_gate is None else _rows_arg(out_gate, "out_gate", (n, D),
+                                                           gate.dtype, dev)
+    return (gate.data_ptr(), gs, vp, vs, op, os_, code), n, D, dev
+
+
+def _sequence_args(offsets, dev):
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be [num_seqs + 1]")
+    return _expert_arg(offsets, "offsets", offsets.shape, torch.int64, dev), offsets.shape[0] - 1
+
+
+def _state_arg(t: Optional[torch.Tensor], name: str, shape: tuple, dev):
+    return None if t is None else _expert_arg(t, name, shape, torch.float32, dev)
+
+
+def ctr_gated_scan_fwd(gate: torch.Tensor, value: torch.Tensor, offsets: torch.Tensor,
+                       out_gate: Optional[torch.Tensor] = None,
+                       h0: Optional[torch.Tensor] = None, want_states: bool = False,
+                       want_last: bool = True, Y: Optional[torch.Tensor] = None,
+                       hN: Optional[torch.Tensor] = None, states: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None,
+                       prepare: bool = False):
+    """(Y [n, D], hN fp32 [B, D], states) of the recurrence h = f h + (1 - f) value with f the
+    sigmoid of gate, over the B sequences [offsets[b], offsets[b + 1]) (int64 [B + 1]) of the rows
+    gate, value and out_gate [n, D] (which may be parts of wider rows); Y = h, or h * silu(out_gate).
+    A sequence begins with h0[b] (fp32 [B, D]; None: zeros) and ends with hN[b].  want_states:
+    what the backward needs (else None).  Rows of Y in no sequence are not written."""
+    if stream is not None:
+        return _on(stream, ctr_gated_scan_fwd, gate, value, offsets, out_gate, h0, want_states,
+                   want_last, Y, hN, states, workspace, prepare=prepare)
+    first, n, D, dev = _scan_args(gate, value, out_gate)
+    fp, B = _sequence_args(offsets, dev)
+    Y, yp, ys = _matrix(Y, "Y", n, D, gate.dtype, dev)
+    np_, sp = None, None
+    if want_last or hN is not None:
+        hN, np_ = _dense(hN, "hN", (B, D), (D, 1), torch.float32, dev)
+    if want_states or states is not None:
+        states, sp = _dense(states, "states", (ctr_gated_scan_chunks(n), D), (D, 1), torch.float32,
+                            dev)
+    if workspace is None:
+        workspace = _workspace(gated_scan_fwd_workspace_bytes(n, D), dev)
+    wsb = ctypes.c_size_t(workspace.numel())
+    args = first + (fp, n, B, D, _state_arg(h0, "h0", (B, D), dev), yp, ys, np_, sp,
+                    workspace.data_ptr(), ctypes.byref(wsb))
+    return _launch_here("ctr_gated_scan_fwd", dev, args, prepare, (Y, hN, states), workspace)
+
+
+def ctr_gated_scan_bwd(gate: torch.Tensor, value: torch.Tensor, offsets: torch.Tensor,
+                       dY: torch.Tensor, states: torch.Tensor,
+                       out_gate: Optional[torch.Tensor] = None,
+                       h0: Optional[torch.Tensor] = None, dhN: Optional[torch.Tensor] = None,
+                       want_dh0: bool = True, dgate: Optional[torch.Tensor] = None,
+                       dvalue: Optional[torch.Tensor] = None,
+                       dout_gate: Optional[torch.Tensor] = None,
+                       dh0: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None,
+                       prepare: bool = False):
+    """(dgate, dvalue, dout_gate, dh0) from dY [n, D] and dhN (fp32 [B, D], or None); the rest as
+    the forward had it, with its states.  dout_gate is None without out_gate, dh0 unless wanted.
+    Rows of the gradients in no sequence are not written."""
+    if stream is not None:
+        return _on(stream, ctr_gated_scan_bwd, gate, value, offsets, dY, states, out_gate, h0, dhN,
+                   want_dh0, dgate, dvalue, dout_gate, dh0, workspace, prepare=prepare)
+    first, n, D, dev = _scan_args(gate, value, out_gate)
+    fp, B = _sequence_args(offsets, dev)
+    yp, dys = _rows_arg(dY, "dY", (n, D), gate.dtype, dev)
+    dgate, gp, gs = _matrix(dgate, "dgate", n, D, gate.dtype, dev)
+    dvalue, vp, vs = _matrix(dvalue, "dvalue", n, D, gate.dtype, dev)
+    op, os_, hp = None, D, None
+    if out_gate is not None:
+        dout_gate, op, os_ = _matrix(dout_gate, "dout_gate", n, D, gate.dtype, dev)
+    elif dout_gate is not None:
+        raise ValueError("dout_gate needs an out_gate")
+    if want_dh0 or dh0 is not None:
+        dh0, hp = _dense(dh0, "dh0", (B, D), (D, 1), torch.float32, dev)
+    sp = _expert_arg(states, "states", (ctr_gated_scan_chunks(n), D), torch.float32, dev)
+    if workspace is None:
+        workspace = _workspace(gated_scan_bwd_workspace_bytes(n, D), dev)
+    wsb = ctypes.c_size_t(workspace.numel())
+    args = first + (fp, n, B, D, _state_arg(h0, "h0", (B, D), dev), sp, yp, dys,
+                    _state_arg(dhN, "dhN", (B, D), dev), gp, gs, vp, vs, op, os_, hp,
+                    workspace.data_ptr(), ctypes.byref(wsb))
+    return _launch_here("ctr_gated_scan_bwd", dev, args, prepare, (dgate, dvalue, dout_gate, dh0),
+                        workspace)
+
+
+def ctr_gated_scan_step(gate: torch.Tensor, value: torch.Tensor, state: torch.Tensor,
+                        index: Optional[torch.Tensor] = None,
+                        out_gate: Optional[torch.Tensor] = None, new_state=False,
+                        Y: Optional[torch.Tensor] = None, stream=None, prepare: bool = False):
+    """(Y [B, D], the state): one row of each of B sequences.  Row i takes state[index[i]] (index
+    int32 [B]; None: state[i]) of state fp32 [slots, D] one row further, in place, or into
+    new_state (a tensor, or True: a new one; without index, as slots that no row names are not
+    written).  Rows of one slot follow each other in their order; a slot that there is not gives
+    zeros."""
+    if stream is not None:
+        return _on(stream, ctr_gated_scan_step, gate, value, state, index, out_gate, new_state, Y,
+                   prepare=prepare)
+    first, B, D, dev = _scan_args(gate, value, out_gate)
+    if state.dim() != 2:
+        raise ValueError("state must be [slots, D]")
+    slots = state.shape[0]
+    sp = _expert_arg(state, "state", (slots, D), torch.float32, dev)
+    ip = None if index is None else _expert_arg(index, "index", (B,), torch.int32, dev)
+    to, tp = state, sp
+    if new_state is not False and new_state is not None:
+        if new_state is True and (index is not None or slots != B):
+            raise ValueError("a new state needs a row for every slot")
+        to, tp = _dense(None if new_state is True else new_state, "new_state", (slots, D), (D, 1),
+                        torch.float32, dev)
+    Y, yp, ys = _matrix(Y, "Y", B, D, gate.dtype, dev)
+    args = first + (B, D, ip, slots, sp, tp, yp, ys)
+    return _launch_here("ctr_gated_scan_step", dev, args, prepare, (Y, to))
 
 
 def ctr_init_tables_hash(table: torch.Tensor, rows: Sequence[int], seed: int,
