@@ -12,14 +12,31 @@
 //
 // Both directions are one long scan of affine maps h -> A h + H down all rows, A between 0 and 1.
 // A map in which a sequence begins takes nothing over from before, not even an infinity times
-// zero: its A has its sign bit set (-1 where a sequence begins, which products keep).  The rows are cut into chunks of kChunk, whose maps
-// are made side by side, joined, and applied: work for the whole chip however few sequences and
-// channels there are.
+// zero: its A has its sign bit set (-1 where a sequence begins, which products keep).
+//
+// The rows are cut into chunks; a block has one chunk of 64 or 128 channels, a wave some rows of
+// it, which it reads once and keeps in registers.  The block joins its waves' maps, leaves the
+// chunk's map for those behind it, looks back over the chunks before it for the state that comes
+// in, leaves the state that goes out, and finishes its rows.  Blocks take their chunks by a
+// counter, in order: who is waited for has begun, and waits for none behind it, so every wait ends.
+// What a block leaves is one 64-bit word a channel, map and all, so that no word has to be ordered
+// with another.
 namespace ctr {
 namespace scan {
 
-constexpr int kRows = 16, kWaves = 8, kChunk = kRows * kWaves;  // rows a wave, waves a block
-constexpr int kThreads = kWaves * 64;
+constexpr int kWaves = 8, kThreads = kWaves * 64;
+constexpr int kGroup = 16;                     // rows that one entry of marks tells of
+constexpr int kFwdRows = 16, kBwdRows = 8;     // rows a wave
+constexpr int kFwdChunk = kFwdRows * kWaves, kBwdChunk = kBwdRows * kWaves;
+// The backward takes the state before each of its chunks from the forward.
+static_assert(kFwdChunk % kBwdChunk == 0 && kBwdChunk % kFwdRows == 0, "states at whole waves");
+
+// Of kGroup rows: the last sequence that begins at or before the first of them (-1: none), which
+// rows are in a sequence, begin one, end one.
+struct Marks {
+  int32_t seq;
+  uint16_t in, begins, ends, pad;
+};
 
 struct Args {
   const void* g;
@@ -30,14 +47,12 @@ struct Args {
   int64_t os;
   const int64_t* offsets;
   int64_t n, B;
-  int D;
+  int D, tiles;
   const float* h0;              // nullable: 0
   void* y;
   int64_t ys;
   float* hN;                    // nullable
-  float* states;                // [chunks, D]: the state before each chunk
-  float* A;                     // [chunks, D]: the chunks' maps
-  float* H;
+  float* states;                // [rows / kBwdChunk, D]: the state before each chunk
   // backward
   const void* dy;
   int64_t dys;
@@ -49,7 +64,11 @@ struct Args {
   void* dout;
   int64_t dos;
   float* dh0;                   // nullable
-  float* carries;               // [chunks, D]: f dh of the row after each chunk
+  // workspace
+  uint32_t* ticket;
+  Marks* marks;                 // [rows / kGroup]
+  unsigned long long* words;    // [chunks, D]
+  int64_t chunks;
 };
 
 // 1 / (1 + exp(-x)) and 1 / (1 + exp(x)), each to a few units of its last place.
@@ -68,82 +87,106 @@ __device__ __forceinline__ void sigmoids(float x, float* up, float* down) {
   *down = x >= 0.f ? s : x < 0.f ? r : x;
 }
 
-__device__ __forceinline__ int64_t first_row(const Args& a) {
-  return a.B > 0 ? clamp64(a.offsets[0], 0, a.n) : a.n;
-}
-__device__ __forceinline__ int64_t end_row(const Args& a) {
-  return a.B > 0 ? clamp64(a.offsets[a.B], 0, a.n) : 0;
-}
-
-// The last sequence of those in [0, B) that begin at or before row p, 64 probes at a time; -1:
-// none does.  The same in the whole wave.
+// The last sequence of those in [0, B) that begin at or before row p; -1: none does.
 __device__ __forceinline__ int64_t sequence_of(const Args& a, int64_t p) {
-  const int lane = threadIdx.x & 63;
-  int64_t lo = -1, hi = a.B;                   // offsets[lo] <= p < offsets[hi]
+  int64_t lo = -1, hi = a.B;
   while (hi - lo > 1) {
-    const int64_t step = (hi - lo + 64) / 65;  // probes lo + step, lo + 2 step, ..
-    const int64_t at = lo + (lane + 1) * step;
-    const uint64_t le = __ballot(at < hi && a.offsets[at < hi ? at : hi - 1] <= p);
-    const int below = le == ~0ull ? 64 : __builtin_ctzll(~le);
-    const int64_t to = lo + (below + 1) * step;
-    lo += below * step;
-    hi = to < hi ? to : hi;
+    const int64_t mid = (lo + hi) >> 1;
+    if (a.offsets[mid] <= p) lo = mid;
+    else hi = mid;
   }
   return lo;
 }
-
-// What a wave knows of its rows [p, p + kRows): which of them are in a sequence, begin one or
-// end one, and the sequence of the first.
-struct Marks {
-  int64_t seq;                  // of row p (or -1)
-  uint32_t in, begins, ends;    // bits
-};
-// Sequence of row i of the wave, m.seq or a later one.
-__device__ __forceinline__ int64_t sequence_at(const Args& a, const Marks& m, int64_t p, int i) {
-  for (int64_t b = m.seq; b < m.seq + 2; ++b)
-    if (b + 1 >= a.B || a.offsets[b + 1] > p + i) return b < a.B ? b : a.B - 1;
-  return sequence_of(a, p + i);
+// Sequence of row p, m.seq or a later one; at least 0, as it indexes arrays.
+__device__ __forceinline__ int64_t sequence_at(const Args& a, const Marks& m, int64_t p) {
+  int64_t b = m.seq;
+  for (int k = 0; k < 2; ++k, ++b)
+    if (b + 1 >= a.B || a.offsets[b + 1] > p) return b < 0 ? 0 : b < a.B ? b : a.B - 1;
+  b = sequence_of(a, p);
+  return b < 0 ? 0 : b;
 }
 
-__device__ __forceinline__ Marks marks_of(const Args& a, int64_t p) {
-  Marks m;
-  m.in = m.begins = m.ends = 0u;
-  const int64_t lo = first_row(a), hi = end_row(a);
-  m.seq = -1;
-  if (p >= hi || p + kRows <= lo) return m;
-  m.seq = sequence_of(a, p);
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) m.in |= (p + i >= lo && p + i < hi ? 1u : 0u) << i;
-  // offsets that lie in (p, p + kRows]: bit i of `at` is set where a sequence begins at row i
-  uint32_t at = m.seq >= 0 && a.offsets[m.seq] == p ? 1u : 0u;
-  for (int64_t b0 = m.seq + 1; b0 <= a.B; b0 += 64) {
-    const int64_t b = b0 + lane;
-    const int64_t off = b <= a.B ? a.offsets[b] : INT64_MAX;
-    uint32_t mine = off > p && off <= p + kRows ? 1u << (int)(off - p) : off == p ? 1u : 0u;
-    for (int d = 1; d < 64; d <<= 1) mine |= __shfl_xor(mine, d);
-    at |= mine;
-    if (__ballot(off > p + kRows)) break;
+// Before a scan: the counter and the words cleared, the marks made, and the states (or gradients
+// of them) of sequences without rows taken through.
+constexpr unsigned long long kEmpty = ~0ull;   // a word that nobody has written
+__global__ __launch_bounds__(256) void prepare_kernel(Args a, const float* __restrict__ from,
+                                                      float* __restrict__ to) {
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  if (t == 0) *a.ticket = 0u;
+  for (int64_t i = t; i < a.chunks * a.D; i += step) a.words[i] = kEmpty;
+  const int64_t groups = (a.n + kGroup - 1) / kGroup;
+  const int64_t lo = clamp64(a.offsets[0], 0, a.n), hi = clamp64(a.offsets[a.B], 0, a.n);
+  for (int64_t i = t; i < groups; i += step) {
+    const int64_t p = i * kGroup;
+    uint32_t in = 0u, at = 0u;                 // bit q of `at`: a sequence (or their end) at p + q
+    for (int q = 0; q < kGroup; ++q) in |= (p + q >= lo && p + q < hi ? 1u : 0u) << q;
+    int64_t b = sequence_of(a, p);
+    const int64_t seq = b;
+    if (b >= 0 && a.offsets[b] == p) at |= 1u;
+    // the next sequences, from one place where some begin to the next (B: the end of them)
+    for (int k = 0; k <= kGroup && b < a.B; ++k) {
+      const int64_t off = a.offsets[b + 1];
+      if (off > p + kGroup) break;
+      if (off >= p) at |= 1u << (int)(off - p);
+      b = b + 2 <= a.B && a.offsets[b + 2] > off ? b + 1 : off > p ? sequence_of(a, off) : b + 1;
+    }
+    Marks m;
+    m.seq = (int32_t)seq;
+    m.in = (uint16_t)in;
+    m.begins = (uint16_t)(at & in);
+    m.ends = (uint16_t)((at >> 1) & in);
+    m.pad = 0;
+    a.marks[i] = m;
   }
-  at = __builtin_amdgcn_readfirstlane(at);
-  m.in = __builtin_amdgcn_readfirstlane(m.in);
-  m.begins = at & m.in;
-  m.ends = (at >> 1) & m.in;
+  if (!to) return;
+  for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (a.offsets[b + 1] > a.offsets[b]) continue;
+    for (int c = threadIdx.x; c < a.D; c += 256) to[b * a.D + c] = from ? from[b * a.D + c] : 0.f;
+  }
+}
+
+// Marks of the ROWS rows from p on, the same in the whole wave.
+template <int ROWS>
+__device__ __forceinline__ Marks marks_of(const Args& a, int64_t p) {
+  Marks m{-1, 0, 0, 0, 0};
+  if (p >= a.n) return m;
+  m = a.marks[p / kGroup];
+  const int by = (int)(p % kGroup);
+  m.seq = __builtin_amdgcn_readfirstlane(m.seq);
+  const uint32_t mask = (1u << ROWS) - 1u;
+  m.in = (uint16_t)__builtin_amdgcn_readfirstlane((m.in >> by) & mask);
+  m.begins = (uint16_t)__builtin_amdgcn_readfirstlane((m.begins >> by) & mask);
+  m.ends = (uint16_t)__builtin_amdgcn_readfirstlane((m.ends >> by) & mask);
   return m;
 }
 
-// The wave's runs of VW channels of its rows; rows outside every sequence are zeros.
-template <int TY, int VW>
-__device__ __forceinline__ void load_rows(Run<TY, VW> (&x)[kRows], const void* p, int64_t stride,
-                                          int64_t row, uint32_t in, int c, int D) {
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    x[i].load_some(p, (row + i) * stride + c, in >> i & 1u ? D - c : 0);
+// The block's chunk and its column tile.
+__device__ __forceinline__ void take_ticket(const Args& a, int64_t* chunk, int* tile) {
+  __shared__ uint32_t mine;
+  if (threadIdx.x == 0) mine = atomicAdd(a.ticket, 1u);
+  __syncthreads();
+  const uint32_t t = __builtin_amdgcn_readfirstlane(mine);
+  *chunk = t / (uint32_t)a.tiles;
+  *tile = (int)(t % (uint32_t)a.tiles);
 }
 
-// A map applied to what comes in.
+// The wave's runs of VW channels of its rows.  (Rows outside the sequences are read and not used.)
+template <int TY, int VW, int ROWS>
+__device__ __forceinline__ void load_rows(Run<TY, VW> (&x)[ROWS], const void* p, int64_t stride,
+                                          int64_t row, int64_t n, int c, int D) {
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+    x[i].load_some(p, (row + i) * stride + c, row + i < n ? D - c : 0);
+}
+
+// A map applied to what comes in, and one map after another.
+__device__ __forceinline__ bool constant(float A) { return __float_as_uint(A) >> 31; }
 __device__ __forceinline__ float map_on(float A, float H, float h) {
-  return __float_as_uint(A) >> 31 ? H : A * h + H;
+  return constant(A) ? H : A * h + H;
+}
+__device__ __forceinline__ void map_after(float A, float H, float* a, float* h) {
+  *h = map_on(A, H, *h);
+  *a = constant(A) ? A : A * *a;
 }
 
 // The maps of all waves of a block: of those before wave w (in the scan's direction), and of all.
@@ -151,9 +194,10 @@ template <int VW>
 struct Joined {
   float A[VW], H[VW], allA[VW], allH[VW];
 };
+template <int VW>
+using Room = float[kWaves][2][64 * VW];
 template <int VW, bool BACK>
-__device__ __forceinline__ Joined<VW> join_waves(float (*room)[2][64 * VW], const float* A,
-                                                 const float* H) {
+__device__ __forceinline__ Joined<VW> join_waves(Room<VW>& room, const float* A, const float* H) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
@@ -172,9 +216,7 @@ __device__ __forceinline__ Joined<VW> join_waves(float (*room)[2][64 * VW], cons
         j.A[e] = pa;
         j.H[e] = ph;
       }
-      const float ua = room[u][0][e * 64 + lane], uh = room[u][1][e * 64 + lane];
-      ph = map_on(ua, uh, ph);
-      pa = __float_as_uint(ua) >> 31 ? ua : ua * pa;
+      map_after(room[u][0][e * 64 + lane], room[u][1][e * 64 + lane], &pa, &ph);
     }
     j.allA[e] = pa;
     j.allH[e] = ph;
@@ -182,21 +224,106 @@ __device__ __forceinline__ Joined<VW> join_waves(float (*room)[2][64 * VW], cons
   return j;
 }
 
-// APPLY false: the chunks' maps into a.A and a.H.  true: from the states before the chunks the
-// rows' results.
-template <int TY, int VW, bool OUT, bool APPLY>
-__global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
-  __shared__ float room[kWaves][2][64 * VW];
+// A chunk's word: its map, later the constant map of the state that goes out of it.  The A of a
+// written word is never the empty word's.
+__device__ __forceinline__ void leave(unsigned long long* word, float A, float H) {
+  const uint32_t a = __float_as_uint(A);
+  __hip_atomic_store(word,
+                     (unsigned long long)(a == 0xFFFFFFFFu ? 0x7FC00000u : a) << 32 |
+                         __float_as_uint(H),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What comes into the block's chunk: wave w looks at the chunk w + 1 before it (in the scan's
+// direction), then the next kWaves, until the joined maps are constant in every channel.
+template <int VW, bool BACK>
+__device__ __forceinline__ void look_back(const Args& a, int64_t chunk, int c, Room<VW>& room,
+                                          float* state) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  float A[VW], H[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    A[e] = 1.f;
+    H[e] = 0.f;
+  }
+  for (int64_t k = 1;; k += kWaves) {
+    const int64_t at = BACK ? chunk + k + w : chunk - k - w;
+    const bool there = at >= 0 && at < a.chunks;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      float x = -1.f, y = 0.f;                 // before the first chunk there is nothing
+      if (there && c + e < a.D) {
+        unsigned long long word;
+        while ((word = __hip_atomic_load(a.words + at * a.D + c + e, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT)) == kEmpty)
+          __builtin_amdgcn_s_sleep(1);
+        x = __uint_as_float((uint32_t)(word >> 32));
+        y = __uint_as_float((uint32_t)word);
+      }
+      room[w][0][e * 64 + lane] = x;
+      room[w][1][e * 64 + lane] = y;
+    }
+    __syncthreads();
+    bool open = false;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+#pragma unroll
+      for (int u = 0; u < kWaves; ++u) {
+        // A, H after the map of chunk u
+        const float x = room[u][0][e * 64 + lane], y = room[u][1][e * 64 + lane];
+        if (!constant(A[e])) {
+          H[e] = A[e] * y + H[e];
+          A[e] = constant(x) ? x : A[e] * x;
+        }
+      }
+      open |= !constant(A[e]);
+    }
+    if (!__any(open)) break;                   // the same in every wave
+    __syncthreads();
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e) state[e] = H[e];
+}
+
+// The chunk's map left, the state that comes in (unless a sequence begins with it), and the state
+// that goes out left.
+template <int VW, bool BACK>
+__device__ __forceinline__ void exchange(const Args& a, int64_t chunk, int c, bool begins,
+                                         const Joined<VW>& j, Room<VW>& room, float* state) {
+  unsigned long long* words = a.words + chunk * a.D + c;
+  const bool mine = threadIdx.x < 64;
+  if (mine)
+#pragma unroll
+    for (int e = 0; e < VW; ++e)
+      if (c + e < a.D) leave(words + e, j.allA[e], j.allH[e]);
+#pragma unroll
+  for (int e = 0; e < VW; ++e) state[e] = 0.f;
+  if (begins) return;                          // every map is constant then
+  look_back<VW, BACK>(a, chunk, c, room, state);
+  if (mine)
+#pragma unroll
+    for (int e = 0; e < VW; ++e)
+      if (c + e < a.D && !constant(j.allA[e]))
+        leave(words + e, -1.f, map_on(j.allA[e], j.allH[e], state[e]));
+}
+
+template <int TY, int VW, bool OUT>
+__global__ __launch_bounds__(kThreads, 4) void fwd_kernel(Args a) {
+  constexpr int ROWS = kFwdRows;
+  __shared__ Room<VW> room, back;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t chunk = blockIdx.x;
-  const int c = ((int)blockIdx.y * 64 + lane) * VW;
-  const int64_t p = chunk * kChunk + w * kRows;
-  const Marks m = marks_of(a, p);
-  Run<TY, VW> g[kRows], v[kRows], o[OUT && APPLY ? kRows : 1];
-  load_rows<TY, VW>(g, a.g, a.gs, p, m.in, c, a.D);
-  load_rows<TY, VW>(v, a.v, a.vs, p, m.in, c, a.D);
-  if constexpr (OUT && APPLY) load_rows<TY, VW>(o, a.o, a.os, p, m.in, c, a.D);
+  int64_t chunk;
+  int tile;
+  take_ticket(a, &chunk, &tile);
+  const int c = (tile * 64 + lane) * VW;
+  const int64_t p = chunk * kFwdChunk + w * ROWS;
+  Run<TY, VW> g[ROWS], v[ROWS], o[OUT ? ROWS : 1];
+  load_rows<TY, VW, ROWS>(g, a.g, a.gs, p, a.n, c, a.D);
+  load_rows<TY, VW, ROWS>(v, a.v, a.vs, p, a.n, c, a.D);
+  if constexpr (OUT) load_rows<TY, VW, ROWS>(o, a.o, a.os, p, a.n, c, a.D);
+  const Marks m = marks_of<ROWS>(a, p);
+  const Marks top = marks_of<ROWS>(a, chunk * kFwdChunk);
   float A[VW], H[VW], start[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
@@ -205,16 +332,14 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
   }
   // the state that a sequence begins with
   auto begin = [&](int i) {
-    const int64_t b = sequence_at(a, m, p, i);
+    const int64_t b = a.h0 ? sequence_at(a, m, p + i) : 0;
 #pragma unroll
-    for (int e = 0; e < VW; ++e)
-      start[e] = a.h0 && b >= 0 && c + e < a.D ? a.h0[b * a.D + c + e] : 0.f;
+    for (int e = 0; e < VW; ++e) start[e] = a.h0 && c + e < a.D ? a.h0[b * a.D + c + e] : 0.f;
   };
-  float f[kRows][VW], x[kRows][VW];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (!(m.in >> i & 1u)) continue;
-    if (m.begins >> i & 1u) {
+  for (int i = 0; i < ROWS; ++i) {
+    if (!(m.in >> i & 1)) continue;
+    if (m.begins >> i & 1) {
       begin(i);
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
@@ -224,139 +349,112 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
     }
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      float down;
-      sigmoids<TY>(g[i].at(e), &f[i][e], &down);
-      x[i][e] = down * v[i].at(e);
-      A[e] *= f[i][e];
-      H[e] = f[i][e] * H[e] + x[i][e];
+      float up, down;
+      sigmoids<TY>(g[i].at(e), &up, &down);
+      A[e] *= up;
+      H[e] = up * H[e] + down * v[i].at(e);
     }
   }
   const Joined<VW> j = join_waves<VW, false>(room, A, H);
-  if constexpr (!APPLY) {
-    if (w == 0)
+  float state[VW], h[VW];
+  exchange<VW, false>(a, chunk, c, top.begins & 1, j, back, state);
 #pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (c + e < a.D) {
-          a.A[chunk * a.D + c + e] = j.allA[e];
-          a.H[chunk * a.D + c + e] = j.allH[e];
-        }
-  } else {
-    float h[VW];
+  for (int e = 0; e < VW; ++e) {
+    h[e] = map_on(j.A[e], j.H[e], state[e]);
+    if (a.states && w * ROWS % kBwdChunk == 0 && p < a.n && c + e < a.D)
+      a.states[p / kBwdChunk * a.D + c + e] = h[e];
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (!(m.in >> i & 1)) continue;
+    if (m.begins >> i & 1) {
+      begin(i);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) h[e] = start[e];
+    }
+    float y[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      const float s = c + e < a.D ? a.states[chunk * a.D + c + e] : 0.f;
-      h[e] = map_on(j.A[e], j.H[e], s);
+      float up, down;
+      sigmoids<TY>(g[i].at(e), &up, &down);
+      h[e] = up * h[e] + down * v[i].at(e);
+      y[e] = h[e];
+      if constexpr (OUT) {
+        const float z = o[i].at(e);
+        sigmoids<TY>(z, &up, &down);
+        y[e] *= z * up;
+      }
     }
+    store_some<TY, VW>(a.y, (p + i) * a.ys + c, y, a.D - c);
+    if (a.hN && (m.ends >> i & 1)) {
+      const int64_t b = sequence_at(a, m, p + i);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (!(m.in >> i & 1u)) continue;
-      if (m.begins >> i & 1u) {
-        begin(i);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) h[e] = start[e];
-      }
-      float y[VW];
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        h[e] = f[i][e] * h[e] + x[i][e];
-        y[e] = h[e];
-        if constexpr (OUT) {
-          float up, down;
-          const float z = o[i].at(e);
-          sigmoids<TY>(z, &up, &down);
-          y[e] *= z * up;
-        }
-      }
-      store_some<TY, VW>(a.y, (p + i) * a.ys + c, y, a.D - c);
-      if (a.hN && (m.ends >> i & 1u)) {
-        const int64_t b = sequence_at(a, m, p, i);
-#pragma unroll
-        for (int e = 0; e < VW; ++e)
-          if (b >= 0 && c + e < a.D) a.hN[b * a.D + c + e] = h[e];
-      }
+      for (int e = 0; e < VW; ++e)
+        if (c + e < a.D) a.hN[b * a.D + c + e] = h[e];
     }
   }
 }
 
-// Backwards.  APPLY false: the maps of the chunks, from their last row to their first.  true: the
-// gradients, from the states before the chunks and the carries into them from behind.
-template <int TY, int VW, bool OUT, bool APPLY>
-__global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
-  __shared__ float room[2][kWaves][2][64 * VW];
+// Backwards: a map takes f dh of the row behind it to f dh of its first row.  The states within
+// the chunk are made again from the one before it.
+template <int TY, int VW, bool OUT>
+__global__ __launch_bounds__(kThreads, 4) void bwd_kernel(Args a) {
+  constexpr int ROWS = kBwdRows;
+  __shared__ Room<VW> room[2], back;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t chunk = blockIdx.x;
-  const int c = ((int)blockIdx.y * 64 + lane) * VW;
-  const int64_t p = chunk * kChunk + w * kRows;
-  const Marks m = marks_of(a, p);
-  Run<TY, VW> g[kRows], v[APPLY ? kRows : 1], o[OUT ? kRows : 1], dy[kRows];
-  load_rows<TY, VW>(g, a.g, a.gs, p, m.in, c, a.D);
-  load_rows<TY, VW>(dy, a.dy, a.dys, p, m.in, c, a.D);
-  if constexpr (OUT) load_rows<TY, VW>(o, a.o, a.os, p, m.in, c, a.D);
-  if constexpr (APPLY) load_rows<TY, VW>(v, a.v, a.vs, p, m.in, c, a.D);
-  // row of h0, dhN or dh0 of the sequence of row i
+  int64_t chunk;
+  int tile;
+  take_ticket(a, &chunk, &tile);
+  chunk = a.chunks - 1 - chunk;
+  const int c = (tile * 64 + lane) * VW;
+  const int64_t p = chunk * kBwdChunk + w * ROWS;
+  Run<TY, VW> g[ROWS], v[ROWS], o[OUT ? ROWS : 1], dy[ROWS];
+  load_rows<TY, VW, ROWS>(g, a.g, a.gs, p, a.n, c, a.D);
+  load_rows<TY, VW, ROWS>(v, a.v, a.vs, p, a.n, c, a.D);
+  load_rows<TY, VW, ROWS>(dy, a.dy, a.dys, p, a.n, c, a.D);
+  if constexpr (OUT) load_rows<TY, VW, ROWS>(o, a.o, a.os, p, a.n, c, a.D);
+  float state[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) state[e] = c + e < a.D ? a.states[chunk * a.D + c + e] : 0.f;
+  const Marks m = marks_of<ROWS>(a, p);
+  const int64_t final_row = chunk * kBwdChunk + kBwdChunk - ROWS;
+  const Marks bottom = marks_of<ROWS>(a, final_row);
+  // row of h0 or dhN of the sequence of row i
   auto row = [&](const float* q, int i, float* x) {
-    const int64_t b = sequence_at(a, m, p, i);
+    const int64_t b = q ? sequence_at(a, m, p + i) : 0;
 #pragma unroll
-    for (int e = 0; e < VW; ++e) x[e] = q && b >= 0 && c + e < a.D ? q[b * a.D + c + e] : 0.f;
+    for (int e = 0; e < VW; ++e) x[e] = q && c + e < a.D ? q[b * a.D + c + e] : 0.f;
   };
-  float before[kRows][VW];                     // the state before each row
-  float A[VW], H[VW], x[VW];
-  if constexpr (APPLY) {
-    // forwards again: the states within the chunk
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      A[e] = 1.f;
-      H[e] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (!(m.in >> i & 1u)) continue;
-      if (m.begins >> i & 1u) {
-        row(a.h0, i, H);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) A[e] = -1.f;
-      }
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        float up, down;
-        sigmoids<TY>(g[i].at(e), &up, &down);
-        A[e] *= up;
-        H[e] = up * H[e] + down * v[i].at(e);
-      }
-    }
-    const Joined<VW> j = join_waves<VW, false>(room[0], A, H);
-    float h[VW];
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      const float s = c + e < a.D ? a.states[chunk * a.D + c + e] : 0.f;
-      h[e] = map_on(j.A[e], j.H[e], s);
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (m.begins >> i & 1u) row(a.h0, i, h);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        before[i][e] = h[e];
-        float up, down;
-        sigmoids<TY>(g[i].at(e), &up, &down);
-        if (m.in >> i & 1u) h[e] = up * h[e] + down * v[i].at(e);
-      }
-    }
-  }
-  // backwards: a map takes f dh of the row behind to f dh of the first row
+  float A[VW], H[VW], C[VW], K[VW];            // the map forwards, and backwards
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    A[e] = 1.f;
-    H[e] = 0.f;
+    A[e] = C[e] = 1.f;
+    H[e] = K[e] = 0.f;
   }
 #pragma unroll
-  for (int i = kRows - 1; i >= 0; --i) {
-    if (!(m.in >> i & 1u)) continue;
-    if (m.ends >> i & 1u) {
-      row(a.dhN, i, H);
+  for (int i = 0; i < ROWS; ++i) {
+    if (!(m.in >> i & 1)) continue;
+    if (m.begins >> i & 1) {
+      row(a.h0, i, H);
 #pragma unroll
       for (int e = 0; e < VW; ++e) A[e] = -1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      float up, down;
+      sigmoids<TY>(g[i].at(e), &up, &down);
+      A[e] *= up;
+      H[e] = up * H[e] + down * v[i].at(e);
+    }
+  }
+#pragma unroll
+  for (int i = ROWS - 1; i >= 0; --i) {
+    if (!(m.in >> i & 1)) continue;
+    if (m.ends >> i & 1) {
+      row(a.dhN, i, K);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) C[e] = -1.f;
     }
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
@@ -368,94 +466,61 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
         q *= z * zu;
       }
       sigmoids<TY>(g[i].at(e), &up, &down);
-      A[e] *= up;
-      H[e] = up * (q + H[e]);
+      C[e] *= up;
+      K[e] = up * (q + K[e]);
     }
   }
-  const Joined<VW> j = join_waves<VW, true>(room[1], A, H);
-  if constexpr (!APPLY) {
-    if (w == 0)
+  const Joined<VW> j = join_waves<VW, true>(room[1], C, K);
+  float carry[VW];
+  exchange<VW, true>(a, chunk, c, bottom.ends >> (ROWS - 1) & 1, j, back, carry);
 #pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (c + e < a.D) {
-          a.A[chunk * a.D + c + e] = j.allA[e];
-          a.H[chunk * a.D + c + e] = j.allH[e];
-        }
-  } else {
-    float carry[VW];
+  for (int e = 0; e < VW; ++e) carry[e] = map_on(j.A[e], j.H[e], carry[e]);
+  const Joined<VW> f = join_waves<VW, false>(room[0], A, H);
+  float before[ROWS][VW], h[VW];               // the state before each row
+#pragma unroll
+  for (int e = 0; e < VW; ++e) h[e] = map_on(f.A[e], f.H[e], state[e]);
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (m.begins >> i & 1) row(a.h0, i, h);
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      const float s = c + e < a.D ? a.carries[chunk * a.D + c + e] : 0.f;
-      carry[e] = map_on(j.A[e], j.H[e], s);
-    }
-#pragma unroll
-    for (int i = kRows - 1; i >= 0; --i) {
-      if (!(m.in >> i & 1u)) continue;
-      if (m.ends >> i & 1u) row(a.dhN, i, carry);
-      float dg[VW], dv[VW], dz[VW];
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        float up, down, q = dy[i].at(e);
-        sigmoids<TY>(g[i].at(e), &up, &down);
-        const float val = v[i].at(e);
-        if constexpr (OUT) {
-          float zu, zd;
-          const float z = o[i].at(e), h = up * before[i][e] + down * val;
-          sigmoids<TY>(z, &zu, &zd);
-          dz[e] = q * h * zu * (1.f + z * zd);
-          q *= z * zu;
-        }
-        const float dh = q + carry[e];
-        dv[e] = down * dh;
-        dg[e] = dh * (before[i][e] - val) * (up * down);
-        carry[e] = up * dh;
-      }
-      store_some<TY, VW>(a.dv, (p + i) * a.dvs + c, dv, a.D - c);
-      store_some<TY, VW>(a.dg, (p + i) * a.dgs + c, dg, a.D - c);
-      if constexpr (OUT) store_some<TY, VW>(a.dout, (p + i) * a.dos + c, dz, a.D - c);
-      if (a.dh0 && (m.begins >> i & 1u)) {
-        const int64_t b = sequence_at(a, m, p, i);
-#pragma unroll
-        for (int e = 0; e < VW; ++e)
-          if (b >= 0 && c + e < a.D) a.dh0[b * a.D + c + e] = carry[e];
-      }
+      before[i][e] = h[e];
+      float up, down;
+      sigmoids<TY>(g[i].at(e), &up, &down);
+      if (m.in >> i & 1) h[e] = up * h[e] + down * v[i].at(e);
     }
   }
-}
-
-// The chunks' maps one after the other (BACK: the last first): what comes into each.
-template <bool BACK>
-__global__ __launch_bounds__(64) void carry_kernel(const float* __restrict__ A,
-                                                   const float* __restrict__ H, int64_t chunks,
-                                                   int D, float* __restrict__ into) {
-  const int c = (int)blockIdx.x * 64 + threadIdx.x;
-  if (c >= D) return;
-  float s = 0.f;
-  constexpr int DEEP = 8;
-  for (int64_t i = 0; i < chunks; i += DEEP) {
-    float x[DEEP], y[DEEP];
 #pragma unroll
-    for (int k = 0; k < DEEP; ++k) {
-      const int64_t at = (BACK ? chunks - 1 - i - k : i + k) * D + c;
-      x[k] = i + k < chunks ? A[at] : 1.f;
-      y[k] = i + k < chunks ? H[at] : 0.f;
-    }
+  for (int i = ROWS - 1; i >= 0; --i) {
+    if (!(m.in >> i & 1)) continue;
+    if (m.ends >> i & 1) row(a.dhN, i, carry);
+    float dg[VW], dv[VW], dz[VW];
 #pragma unroll
-    for (int k = 0; k < DEEP; ++k) {
-      if (i + k < chunks) into[(BACK ? chunks - 1 - i - k : i + k) * D + c] = s;
-      s = map_on(x[k], y[k], s);
+    for (int e = 0; e < VW; ++e) {
+      float up, down, q = dy[i].at(e);
+      sigmoids<TY>(g[i].at(e), &up, &down);
+      const float val = v[i].at(e);
+      if constexpr (OUT) {
+        float zu, zd;
+        const float z = o[i].at(e), now = up * before[i][e] + down * val;
+        sigmoids<TY>(z, &zu, &zd);
+        dz[e] = q * now * zu * (1.f + z * zd);
+        q *= z * zu;
+      }
+      const float dh = q + carry[e];
+      dv[e] = down * dh;
+      dg[e] = dh * (before[i][e] - val) * (up * down);
+      carry[e] = up * dh;
     }
-  }
-}
-
-// Sequences without rows: their states, or the gradients of them, go through.
-__global__ __launch_bounds__(256) void empty_kernel(const int64_t* __restrict__ offsets, int64_t n,
-                                                    int64_t B, int D,
-                                                    const float* __restrict__ from,
-                                                    float* __restrict__ to) {
-  for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
-    if (offsets[b + 1] > offsets[b]) continue;
-    for (int c = threadIdx.x; c < D; c += 256) to[b * D + c] = from ? from[b * D + c] : 0.f;
+    store_some<TY, VW>(a.dv, (p + i) * a.dvs + c, dv, a.D - c);
+    store_some<TY, VW>(a.dg, (p + i) * a.dgs + c, dg, a.D - c);
+    if constexpr (OUT) store_some<TY, VW>(a.dout, (p + i) * a.dos + c, dz, a.D - c);
+    if (a.dh0 && (m.begins >> i & 1)) {
+      const int64_t b = sequence_at(a, m, p + i);
+#pragma unroll
+      for (int e = 0; e < VW; ++e)
+        if (c + e < a.D) a.dh0[b * a.D + c + e] = carry[e];
+    }
   }
 }
 
@@ -522,47 +587,68 @@ __global__ __launch_bounds__(256) void step_kernel(Args a, const int32_t* __rest
       if (c + e < a.D) next[slot * a.D + c + e] = h[e];
 }
 
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t pieces(int64_t n, int64_t size) { return (n + size - 1) / size; }
 
-// Two channels a lane where every row begins on 4 bytes (any row of binary32 does).
+// Four bytes a lane: a channel of binary32, or two of 16 bits where every row begins on 4 bytes.
 bool pairs(int dtype, const void* p, int64_t stride) {
-  return dtype == kEltF32 ||
-         (reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0);
+  return dtype != kEltF32 && reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
 }
 
-template <int TY, bool APPLY>
-void launch_fwd(const Args& a, bool two, hipStream_t s) {
-  const int64_t chunks = chunks_of(a.n);
-  auto go = [&](auto vw, auto out) {
-    constexpr int VW = decltype(vw)::value;
-    const dim3 grid((unsigned)chunks, (unsigned)((a.D + 64 * VW - 1) / (64 * VW)));
-    fwd_kernel<TY, VW, decltype(out)::value, APPLY><<<grid, kThreads, 0, s>>>(a);
-  };
-  auto by_out = [&](auto vw) { a.o ? go(vw, std::true_type{}) : go(vw, std::false_type{}); };
-  two ? by_out(std::integral_constant<int, 2>{}) : by_out(std::integral_constant<int, 1>{});
-}
-template <int TY, bool APPLY>
-void launch_bwd(const Args& a, bool two, hipStream_t s) {
-  const int64_t chunks = chunks_of(a.n);
-  auto go = [&](auto vw, auto out) {
-    constexpr int VW = decltype(vw)::value;
-    const dim3 grid((unsigned)chunks, (unsigned)((a.D + 64 * VW - 1) / (64 * VW)));
-    bwd_kernel<TY, VW, decltype(out)::value, APPLY><<<grid, kThreads, 0, s>>>(a);
-  };
-  auto by_out = [&](auto vw) { a.o ? go(vw, std::true_type{}) : go(vw, std::false_type{}); };
-  two ? by_out(std::integral_constant<int, 2>{}) : by_out(std::integral_constant<int, 1>{});
+// The workspace: counter, marks, words.
+size_t carve_scan(Args* a, void* workspace, int64_t n, int D, int chunk) {
+  const int64_t chunks = pieces(n, chunk);
+  size_t off = 256;
+  char* base = static_cast<char*>(workspace);
+  const size_t marks = off;
+  off += ((size_t)pieces(n, kGroup) * sizeof(Marks) + 255) / 256 * 256;
+  const size_t words = off;
+  off += (size_t)chunks * (size_t)D * 8;
+  if (a) {
+    a->chunks = chunks;
+    a->ticket = reinterpret_cast<uint32_t*>(base);
+    a->marks = reinterpret_cast<Marks*>(base + marks);
+    a->words = reinterpret_cast<unsigned long long*>(base + words);
+  }
+  return off;
 }
 
-unsigned empty_blocks(int64_t B) { return (unsigned)(B < 1024 ? B : 1024); }
+hipError_t run(Args a, int dtype, bool back, bool two, hipStream_t s) {
+  if (a.B == 0) return hipSuccess;
+  const float* from = back ? a.dhN : a.h0;
+  float* to = back ? a.dh0 : a.hN;
+  if (a.n == 0 && !to) return hipSuccess;
+  const int64_t work = a.chunks * a.D > a.B ? a.chunks * a.D : a.B;
+  const int64_t blocks = pieces(work, 1024);
+  prepare_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(a, from, to);
+  if (a.n == 0) return hipGetLastError();
+  a.tiles = (int)pieces(a.D, two ? 128 : 64);
+  const unsigned grid = (unsigned)(a.chunks * a.tiles);
+  return for_type(dtype, [&](auto ty) {
+    constexpr int TY = decltype(ty)::value;
+    auto go = [&](auto vw, auto out) {
+      constexpr int VW = decltype(vw)::value;
+      constexpr bool OUT = decltype(out)::value;
+      if (back) bwd_kernel<TY, VW, OUT><<<grid, kThreads, 0, s>>>(a);
+      else fwd_kernel<TY, VW, OUT><<<grid, kThreads, 0, s>>>(a);
+      return hipGetLastError();
+    };
+    auto by_out = [&](auto vw) {
+      return a.o ? go(vw, std::true_type{}) : go(vw, std::false_type{});
+    };
+    if constexpr (TY != kEltF32)
+      if (two) return by_out(std::integral_constant<int, 2>{});
+    return by_out(std::integral_constant<int, 1>{});
+  });
+}
 
 }  // namespace scan
 
-int64_t gated_scan_chunks(int64_t n) { return scan::chunks_of(n); }
+int64_t gated_scan_chunks(int64_t n) { return scan::pieces(n, scan::kBwdChunk); }
 size_t gated_scan_fwd_workspace_bytes(int64_t n, int D) {
-  return 3 * (size_t)scan::chunks_of(n) * (size_t)D * 4 + 256;
+  return scan::carve_scan(nullptr, nullptr, n, D, scan::kFwdChunk);
 }
 size_t gated_scan_bwd_workspace_bytes(int64_t n, int D) {
-  return 3 * (size_t)scan::chunks_of(n) * (size_t)D * 4 + 256;
+  return scan::carve_scan(nullptr, nullptr, n, D, scan::kBwdChunk);
 }
 
 hipError_t launch_gated_scan_fwd(const void* g, int64_t gs, const void* v, int64_t vs,
@@ -571,26 +657,11 @@ hipError_t launch_gated_scan_fwd(const void* g, int64_t gs, const void* v, int64
                                  float* hN, float* states, void* workspace, hipStream_t s) {
   scan::Args a{};
   a.g = g; a.gs = gs; a.v = v; a.vs = vs; a.o = o; a.os = os; a.offsets = offsets;
-  a.n = n; a.B = B; a.D = D; a.h0 = h0; a.y = y; a.ys = ys; a.hN = hN;
-  const int64_t chunks = scan::chunks_of(n), each = chunks * D;
-  a.A = static_cast<float*>(workspace);
-  a.H = a.A + each;
-  a.states = states ? states : a.H + each;
-  if (hN && B > 0)
-    scan::empty_kernel<<<scan::empty_blocks(B), 256, 0, s>>>(offsets, n, B, D, h0, hN);
-  if (n > 0 && B > 0) {
-    const bool two = scan::pairs(dtype, g, gs) && scan::pairs(dtype, v, vs) &&
-                     scan::pairs(dtype, o, os) && scan::pairs(dtype, y, ys);
-    for_type(dtype, [&](auto ty) {
-      constexpr int TY = decltype(ty)::value;
-      scan::launch_fwd<TY, false>(a, two, s);
-      scan::carry_kernel<false><<<(unsigned)((D + 63) / 64), 64, 0, s>>>(a.A, a.H, chunks, D,
-                                                                         a.states);
-      scan::launch_fwd<TY, true>(a, two, s);
-      return hipSuccess;
-    });
-  }
-  return hipGetLastError();
+  a.n = n; a.B = B; a.D = D; a.h0 = h0; a.y = y; a.ys = ys; a.hN = hN; a.states = states;
+  scan::carve_scan(&a, workspace, n, D, scan::kFwdChunk);
+  const bool two = scan::pairs(dtype, g, gs) && scan::pairs(dtype, v, vs) &&
+                   scan::pairs(dtype, o, os) && scan::pairs(dtype, y, ys);
+  return scan::run(a, dtype, false, two, s);
 }
 
 hipError_t launch_gated_scan_bwd(const void* g, int64_t gs, const void* v, int64_t vs,
@@ -604,27 +675,12 @@ hipError_t launch_gated_scan_bwd(const void* g, int64_t gs, const void* v, int64
   a.n = n; a.B = B; a.D = D; a.h0 = h0; a.states = const_cast<float*>(states);
   a.dy = dy; a.dys = dys; a.dhN = dhN; a.dg = dg; a.dgs = dgs; a.dv = dv; a.dvs = dvs;
   a.dout = dout; a.dos = dos; a.dh0 = dh0;
-  const int64_t chunks = scan::chunks_of(n), each = chunks * D;
-  a.A = static_cast<float*>(workspace);
-  a.H = a.A + each;
-  a.carries = a.H + each;
-  if (dh0 && B > 0)
-    scan::empty_kernel<<<scan::empty_blocks(B), 256, 0, s>>>(offsets, n, B, D, dhN, dh0);
-  if (n > 0 && B > 0) {
-    const bool two = scan::pairs(dtype, g, gs) && scan::pairs(dtype, v, vs) &&
-                     scan::pairs(dtype, o, os) && scan::pairs(dtype, dy, dys) &&
-                     scan::pairs(dtype, dg, dgs) && scan::pairs(dtype, dv, dvs) &&
-                     scan::pairs(dtype, dout, dos);
-    for_type(dtype, [&](auto ty) {
-      constexpr int TY = decltype(ty)::value;
-      scan::launch_bwd<TY, false>(a, two, s);
-      scan::carry_kernel<true><<<(unsigned)((D + 63) / 64), 64, 0, s>>>(a.A, a.H, chunks, D,
-                                                                        a.carries);
-      scan::launch_bwd<TY, true>(a, two, s);
-      return hipSuccess;
-    });
-  }
-  return hipGetLastError();
+  scan::carve_scan(&a, workspace, n, D, scan::kBwdChunk);
+  const bool two = scan::pairs(dtype, g, gs) && scan::pairs(dtype, v, vs) &&
+                   scan::pairs(dtype, o, os) && scan::pairs(dtype, dy, dys) &&
+                   scan::pairs(dtype, dg, dgs) && scan::pairs(dtype, dv, dvs) &&
+                   scan::pairs(dtype, dout, dos);
+  return scan::run(a, dtype, true, two, s);
 }
 
 hipError_t launch_gated_scan_step(const void* g, int64_t gs, const void* v, int64_t vs,
@@ -645,7 +701,10 @@ hipError_t launch_gated_scan_step(const void* g, int64_t gs, const void* v, int6
           <<<(unsigned)(B * tiles), 256, 0, s>>>(a, index, slots, state, next, tiles);
     };
     auto by_out = [&](auto vw) { o ? go(vw, std::true_type{}) : go(vw, std::false_type{}); };
-    two ? by_out(std::integral_constant<int, 2>{}) : by_out(std::integral_constant<int, 1>{});
+    bool done = false;
+    if constexpr (TY != kEltF32)
+      if (two) by_out(std::integral_constant<int, 2>{}), done = true;
+    if (!done) by_out(std::integral_constant<int, 1>{});
     return hipGetLastError();
   });
 }
