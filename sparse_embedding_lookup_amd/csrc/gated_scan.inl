@@ -25,6 +25,7 @@ namespace ctr {
 namespace scan {
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
+constexpr int kCounter = 64;                   // words from one counter to the next
 constexpr int kGroup = 16;                     // rows that one entry of marks tells of
 constexpr int kFwdRows = 16, kBwdRows = 8;     // rows a wave
 constexpr int kFwdChunk = kFwdRows * kWaves, kBwdChunk = kBwdRows * kWaves;
@@ -65,26 +66,26 @@ struct Args {
   int64_t dos;
   float* dh0;                   // nullable
   // workspace
-  uint32_t* ticket;
+  uint32_t* ticket;             // [tiles], kCounter apart
   Marks* marks;                 // [rows / kGroup]
   unsigned long long* words;    // [chunks, D]
   int64_t chunks;
 };
 
-// 1 / (1 + exp(-x)) and 1 / (1 + exp(x)), each to a few units of its last place.
+// 1 / (1 + exp(-x)) and 1 / (1 + exp(x)), each to a few units of its last place (the latter as 1
+// less the former where that loses nothing); NaN stays.
 template <int TY>
 __device__ __forceinline__ void sigmoids(float x, float* up, float* down) {
   float e, r;
   if constexpr (TY == kEltF32) {
-    e = expf(-fabsf(x));
+    e = expf(-x);
     r = 1.f / (1.f + e);
   } else {                      // inputs of 16 bits: the instructions' own exponential and inverse
-    e = __expf(-fabsf(x));
+    e = __builtin_amdgcn_exp2f(x * -1.44269504f);
     r = __builtin_amdgcn_rcpf(1.f + e);
   }
-  const float s = e * r;
-  *up = x >= 0.f ? r : x < 0.f ? s : x;        // NaN stays
-  *down = x >= 0.f ? s : x < 0.f ? r : x;
+  *up = r;
+  *down = x < 0.f ? 1.f - r : e * r;
 }
 
 // The last sequence of those in [0, B) that begin at or before row p; -1: none does.
@@ -106,38 +107,69 @@ __device__ __forceinline__ int64_t sequence_at(const Args& a, const Marks& m, in
   return b < 0 ? 0 : b;
 }
 
-// Before a scan: the counter and the words cleared, the marks made, and the states (or gradients
-// of them) of sequences without rows taken through.
+// Before a scan: the marks made, the counter and the words cleared, and the states (or gradients
+// of them) of sequences without rows taken through.  A thread makes a group's marks; the searches
+// go through LDS, which holds every offset, or where there are more than kSamples every so many-th.
+// (With searches in memory 28 us for 512 sequences of 131072 rows, each step a trip of its own.)
 constexpr unsigned long long kEmpty = ~0ull;   // a word that nobody has written
+constexpr int kSamples = 2048;
 __global__ __launch_bounds__(256) void prepare_kernel(Args a, const float* __restrict__ from,
                                                       float* __restrict__ to) {
+  __shared__ int64_t sample[kSamples];
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-  if (t == 0) *a.ticket = 0u;
-  for (int64_t i = t; i < a.chunks * a.D; i += step) a.words[i] = kEmpty;
   const int64_t groups = (a.n + kGroup - 1) / kGroup;
-  const int64_t lo = clamp64(a.offsets[0], 0, a.n), hi = clamp64(a.offsets[a.B], 0, a.n);
-  for (int64_t i = t; i < groups; i += step) {
-    const int64_t p = i * kGroup;
-    uint32_t in = 0u, at = 0u;                 // bit q of `at`: a sequence (or their end) at p + q
-    for (int q = 0; q < kGroup; ++q) in |= (p + q >= lo && p + q < hi ? 1u : 0u) << q;
-    int64_t b = sequence_of(a, p);
-    const int64_t seq = b;
-    if (b >= 0 && a.offsets[b] == p) at |= 1u;
-    // the next sequences, from one place where some begin to the next (B: the end of them)
-    for (int k = 0; k <= kGroup && b < a.B; ++k) {
-      const int64_t off = a.offsets[b + 1];
-      if (off > p + kGroup) break;
-      if (off >= p) at |= 1u << (int)(off - p);
-      b = b + 2 <= a.B && a.offsets[b + 2] > off ? b + 1 : off > p ? sequence_of(a, off) : b + 1;
+  const int64_t every = (a.B + kSamples - 1) / kSamples;
+  if ((int64_t)blockIdx.x * 256 < groups) {
+    const int64_t lo = clamp64(a.offsets[0], 0, a.n), hi = clamp64(a.offsets[a.B], 0, a.n);
+    const int samples = (int)((a.B + every - 1) / every);
+    for (int i = threadIdx.x; i < samples; i += 256) sample[i] = a.offsets[i * every];
+    __syncthreads();
+    auto offset = [&](int64_t b) { return every == 1 && b < a.B ? sample[b] : a.offsets[b]; };
+    auto search = [&](int64_t p) {             // sequence_of
+      int x = -1, y = samples;
+      while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if (sample[mid] <= p) x = mid;
+        else y = mid;
+      }
+      int64_t b = x * every, e = b + every < a.B ? b + every : a.B;
+      if (x < 0) return (int64_t)-1;
+      while (e - b > 1) {
+        const int64_t mid = (b + e) >> 1;
+        if (a.offsets[mid] <= p) b = mid;
+        else e = mid;
+      }
+      return b;
+    };
+    for (int64_t i = t; i < groups; i += step) {
+      const int64_t p = i * kGroup;
+      // rows [0, n) of a mask
+      auto rows = [](int64_t n) { return n <= 0 ? 0u : n >= kGroup ? 0xFFFFu : (1u << (int)n) - 1u; };
+      const uint32_t in = rows(hi - p) & ~rows(lo - p);
+      int64_t b = search(p);
+      Marks m;
+      m.seq = (int32_t)b;
+      uint32_t at = b >= 0 && offset(b) == p ? 1u : 0u;  // bit q: a sequence (or their end) at p + q
+      // the sequences after b, from one row where some begin to the next such row
+      for (int k = 0; k <= kGroup && b < a.B; ++k) {
+        const int64_t off = offset(b + 1);
+        if (off > p + kGroup) break;
+        if (off > p) at |= 1u << (int)(off - p);
+        ++b;
+        if (b < a.B && offset(b + 1) <= off) {
+          const int64_t next = search(off);
+          b = next > b ? next : b;
+        }
+      }
+      m.in = (uint16_t)in;
+      m.begins = (uint16_t)(at & in);
+      m.ends = (uint16_t)((at >> 1) & in);
+      m.pad = 0;
+      a.marks[i] = m;
     }
-    Marks m;
-    m.seq = (int32_t)seq;
-    m.in = (uint16_t)in;
-    m.begins = (uint16_t)(at & in);
-    m.ends = (uint16_t)((at >> 1) & in);
-    m.pad = 0;
-    a.marks[i] = m;
   }
+  for (int64_t i = t; i < a.tiles; i += step) a.ticket[i * kCounter] = 0u;
+  for (int64_t i = t; i < a.chunks * a.D; i += step) a.words[i] = kEmpty;
   if (!to) return;
   for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (a.offsets[b + 1] > a.offsets[b]) continue;
@@ -152,76 +184,90 @@ __device__ __forceinline__ Marks marks_of(const Args& a, int64_t p) {
   if (p >= a.n) return m;
   m = a.marks[p / kGroup];
   const int by = (int)(p % kGroup);
-  m.seq = __builtin_amdgcn_readfirstlane(m.seq);
-  const uint32_t mask = (1u << ROWS) - 1u;
+  // nothing outside the arrays, whatever the offsets were
+  const uint32_t mask = (1u << (a.n - p < ROWS ? (int)(a.n - p) : ROWS)) - 1u;
+  const int32_t seq = m.seq < -1 ? -1 : m.seq < a.B ? m.seq : (int32_t)(a.B - 1);
+  m.seq = __builtin_amdgcn_readfirstlane(seq);
   m.in = (uint16_t)__builtin_amdgcn_readfirstlane((m.in >> by) & mask);
   m.begins = (uint16_t)__builtin_amdgcn_readfirstlane((m.begins >> by) & mask);
   m.ends = (uint16_t)__builtin_amdgcn_readfirstlane((m.ends >> by) & mask);
   return m;
 }
 
-// The block's chunk and its column tile.
+// The block's column tile, and its chunk of that: the next one of the tile's counter.  The tiles
+// go round by one with every chunk, so that an XCD's blocks (every eighth) have all tiles of a row
+// in turn and not the same one each time (131072 x 1024: forward 330 and 312 us, backward 539 and
+// 485).
 __device__ __forceinline__ void take_ticket(const Args& a, int64_t* chunk, int* tile) {
   __shared__ uint32_t mine;
-  if (threadIdx.x == 0) mine = atomicAdd(a.ticket, 1u);
+  *tile = (int)((blockIdx.x + blockIdx.x / (uint32_t)a.tiles) % (uint32_t)a.tiles);
+  if (threadIdx.x == 0) mine = atomicAdd(a.ticket + *tile * kCounter, 1u);
   __syncthreads();
-  const uint32_t t = __builtin_amdgcn_readfirstlane(mine);
-  *chunk = t / (uint32_t)a.tiles;
-  *tile = (int)(t % (uint32_t)a.tiles);
+  *chunk = __builtin_amdgcn_readfirstlane(mine);
 }
 
-// The wave's runs of VW channels of its rows.  (Rows outside the sequences are read and not used.)
+// VW channels of a row from its column c on.  The row is the same in the whole wave, so that its
+// address is scalar; all columns of a lane are in the row, or none (then it loads the first ones,
+// and stores nothing).
+template <int TY, int VW>
+__device__ __forceinline__ const char* row_at(const void* p, int64_t stride, int64_t row) {
+  return static_cast<const char*>(p) + row * stride * kEltSize<TY>;
+}
 template <int TY, int VW, int ROWS>
 __device__ __forceinline__ void load_rows(Run<TY, VW> (&x)[ROWS], const void* p, int64_t stride,
-                                          int64_t row, int64_t n, int c, int D) {
+                                          int64_t row, int64_t n, uint32_t c) {
+  // (Rows outside the sequences are read and not used; behind the last row, the last once more.)
 #pragma unroll
   for (int i = 0; i < ROWS; ++i)
-    x[i].load_some(p, (row + i) * stride + c, row + i < n ? D - c : 0);
+    x[i].load(row_at<TY, VW>(p, stride, row + i < n ? row + i : n - 1), c);
+}
+template <int TY, int VW>
+__device__ __forceinline__ void store_row(void* p, int64_t stride, int64_t row, uint32_t c,
+                                          const float* v) {
+  store_run<TY, VW>(const_cast<char*>(row_at<TY, VW>(p, stride, row)), c, v);
+}
+// The same of fp32 rows of D values, one for each sequence or chunk.
+template <int VW>
+__device__ __forceinline__ void load_state(const float* p, int64_t row, int D, uint32_t c, float* v) {
+  Run<kEltF32, VW> x;
+  x.load(p + row * D, c);
+#pragma unroll
+  for (int e = 0; e < VW; ++e) v[e] = x.at(e);
 }
 
-// A map applied to what comes in, and one map after another.
+// A map applied to what comes in.
 __device__ __forceinline__ bool constant(float A) { return __float_as_uint(A) >> 31; }
 __device__ __forceinline__ float map_on(float A, float H, float h) {
   return constant(A) ? H : A * h + H;
 }
-__device__ __forceinline__ void map_after(float A, float H, float* a, float* h) {
-  *h = map_on(A, H, *h);
-  *a = constant(A) ? A : A * *a;
-}
 
-// The maps of all waves of a block: of those before wave w (in the scan's direction), and of all.
+// The maps of a block's waves, and what comes into each of them.
 template <int VW>
-struct Joined {
-  float A[VW], H[VW], allA[VW], allH[VW];
+struct Room {
+  float A[kWaves][64 * VW], H[kWaves][64 * VW], in[kWaves][64 * VW];
 };
 template <int VW>
-using Room = float[kWaves][2][64 * VW];
-template <int VW, bool BACK>
-__device__ __forceinline__ Joined<VW> join_waves(Room<VW>& room, const float* A, const float* H) {
+__device__ __forceinline__ void put_map(Room<VW>& room, const float* A, const float* H) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    room[w][0][e * 64 + lane] = A[e];
-    room[w][1][e * 64 + lane] = H[e];
+    room.A[w][e * 64 + lane] = A[e];
+    room.H[w][e * 64 + lane] = H[e];
   }
-  __syncthreads();
-  Joined<VW> j;
+}
+// By one wave: `state` goes through the waves' maps, left for each what comes into it.
+template <int VW, bool BACK>
+__device__ __forceinline__ void pass_state(Room<VW>& room, float* state) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int e = 0; e < VW; ++e) {
-    float pa = 1.f, ph = 0.f;
+  for (int i = 0; i < kWaves; ++i) {
+    const int u = BACK ? kWaves - 1 - i : i;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-      const int u = BACK ? kWaves - 1 - i : i;
-      if (u == w) {
-        j.A[e] = pa;
-        j.H[e] = ph;
-      }
-      map_after(room[u][0][e * 64 + lane], room[u][1][e * 64 + lane], &pa, &ph);
+    for (int e = 0; e < VW; ++e) {
+      room.in[u][e * 64 + lane] = state[e];
+      state[e] = map_on(room.A[u][e * 64 + lane], room.H[u][e * 64 + lane], state[e]);
     }
-    j.allA[e] = pa;
-    j.allH[e] = ph;
   }
-  return j;
 }
 
 // A chunk's word: its map, later the constant map of the state that goes out of it.  The A of a
@@ -233,165 +279,175 @@ __device__ __forceinline__ void leave(unsigned long long* word, float A, float H
                          __float_as_uint(H),
                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ unsigned long long look(const unsigned long long* word) {
+  return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
-// What comes into the block's chunk: wave w looks at the chunk w + 1 before it (in the scan's
-// direction), then the next kWaves, until the joined maps are constant in every channel.
+// What comes into a chunk, by one wave: the words of the kAhead chunks before it (in the scan's
+// direction) together, then the next, until the joined maps are constant in every channel.
+constexpr int kAhead = 2;
 template <int VW, bool BACK>
-__device__ __forceinline__ void look_back(const Args& a, int64_t chunk, int c, Room<VW>& room,
+__device__ __forceinline__ void look_back(const Args& a, int64_t chunk, int c, bool in,
                                           float* state) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   float A[VW], H[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    A[e] = 1.f;
+    A[e] = in ? 1.f : -1.f;
     H[e] = 0.f;
   }
-  for (int64_t k = 1;; k += kWaves) {
-    const int64_t at = BACK ? chunk + k + w : chunk - k - w;
-    const bool there = at >= 0 && at < a.chunks;
+  for (int64_t k = 1;; k += kAhead) {
+    unsigned long long word[kAhead][VW];
 #pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      float x = -1.f, y = 0.f;                 // before the first chunk there is nothing
-      if (there && c + e < a.D) {
-        unsigned long long word;
-        while ((word = __hip_atomic_load(a.words + at * a.D + c + e, __ATOMIC_RELAXED,
-                                         __HIP_MEMORY_SCOPE_AGENT)) == kEmpty)
-          __builtin_amdgcn_s_sleep(1);
-        x = __uint_as_float((uint32_t)(word >> 32));
-        y = __uint_as_float((uint32_t)word);
-      }
-      room[w][0][e * 64 + lane] = x;
-      room[w][1][e * 64 + lane] = y;
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t at = BACK ? chunk + k + u : chunk - k - u;
+      const bool there = at >= 0 && at < a.chunks;
+#pragma unroll
+      for (int e = 0; e < VW; ++e)             // before the first chunk there is nothing
+        word[u][e] = there && in ? look(a.words + at * a.D + c + e)
+                                 : 0xBF800000ull << 32;
     }
-    __syncthreads();
     bool open = false;
 #pragma unroll
-    for (int e = 0; e < VW; ++e) {
+    for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-      for (int u = 0; u < kWaves; ++u) {
-        // A, H after the map of chunk u
-        const float x = room[u][0][e * 64 + lane], y = room[u][1][e * 64 + lane];
-        if (!constant(A[e])) {
-          H[e] = A[e] * y + H[e];
-          A[e] = constant(x) ? x : A[e] * x;
+      for (int e = 0; e < VW; ++e) {
+        if (constant(A[e])) continue;
+        const int64_t at = BACK ? chunk + k + u : chunk - k - u;
+        while (word[u][e] == kEmpty) {
+          __builtin_amdgcn_s_sleep(1);
+          word[u][e] = look(a.words + at * a.D + c + e);
         }
+        const float x = __uint_as_float((uint32_t)(word[u][e] >> 32));
+        H[e] = A[e] * __uint_as_float((uint32_t)word[u][e]) + H[e];
+        A[e] = constant(x) ? x : A[e] * x;
       }
-      open |= !constant(A[e]);
-    }
-    if (!__any(open)) break;                   // the same in every wave
-    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VW; ++e) open |= !constant(A[e]);
+    if (!__any(open)) break;
   }
 #pragma unroll
   for (int e = 0; e < VW; ++e) state[e] = H[e];
 }
 
-// The chunk's map left, the state that comes in (unless a sequence begins with it), and the state
-// that goes out left.
+// By one wave, when all maps are in the room: the chunk's map left for those behind it, the state
+// that comes in (unless a sequence begins with it, as every map is constant then), the state that
+// goes out left, and what comes into each wave.
 template <int VW, bool BACK>
-__device__ __forceinline__ void exchange(const Args& a, int64_t chunk, int c, bool begins,
-                                         const Joined<VW>& j, Room<VW>& room, float* state) {
+__device__ __forceinline__ void exchange(const Args& a, int64_t chunk, int c, bool in,
+                                         bool begins, Room<VW>& room) {
+  const int lane = threadIdx.x & 63;
   unsigned long long* words = a.words + chunk * a.D + c;
-  const bool mine = threadIdx.x < 64;
-  if (mine)
+  float A[VW], H[VW], state[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    A[e] = 1.f;
+    H[e] = state[e] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    const int u = BACK ? kWaves - 1 - i : i;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      const float x = room.A[u][e * 64 + lane];
+      H[e] = map_on(x, room.H[u][e * 64 + lane], H[e]);
+      A[e] = constant(x) ? x : x * A[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e)
+    if (in) leave(words + e, A[e], H[e]);
+  if (!begins) {
+    look_back<VW, BACK>(a, chunk, c, in, state);
 #pragma unroll
     for (int e = 0; e < VW; ++e)
-      if (c + e < a.D) leave(words + e, j.allA[e], j.allH[e]);
-#pragma unroll
-  for (int e = 0; e < VW; ++e) state[e] = 0.f;
-  if (begins) return;                          // every map is constant then
-  look_back<VW, BACK>(a, chunk, c, room, state);
-  if (mine)
-#pragma unroll
-    for (int e = 0; e < VW; ++e)
-      if (c + e < a.D && !constant(j.allA[e]))
-        leave(words + e, -1.f, map_on(j.allA[e], j.allH[e], state[e]));
+      if (in && !constant(A[e])) leave(words + e, -1.f, map_on(A[e], H[e], state[e]));
+  }
+  pass_state<VW, BACK>(room, state);
 }
 
 template <int TY, int VW, bool OUT>
 __global__ __launch_bounds__(kThreads, 4) void fwd_kernel(Args a) {
   constexpr int ROWS = kFwdRows;
-  __shared__ Room<VW> room, back;
+  __shared__ Room<VW> room;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t chunk;
   int tile;
   take_ticket(a, &chunk, &tile);
-  const int c = (tile * 64 + lane) * VW;
+  const int first = (tile * 64 + lane) * VW;
+  const bool in = first < a.D;
+  const uint32_t c = in ? first : 0;
   const int64_t p = chunk * kFwdChunk + w * ROWS;
-  Run<TY, VW> g[ROWS], v[ROWS], o[OUT ? ROWS : 1];
-  load_rows<TY, VW, ROWS>(g, a.g, a.gs, p, a.n, c, a.D);
-  load_rows<TY, VW, ROWS>(v, a.v, a.vs, p, a.n, c, a.D);
-  if constexpr (OUT) load_rows<TY, VW, ROWS>(o, a.o, a.os, p, a.n, c, a.D);
-  const Marks m = marks_of<ROWS>(a, p);
-  const Marks top = marks_of<ROWS>(a, chunk * kFwdChunk);
-  float A[VW], H[VW], start[VW];
+  Run<TY, VW> o[OUT ? ROWS : 1];
+  float f[ROWS][VW], x[ROWS][VW];
+  Marks m;
+  auto row = [&](const float* q, int i, float* h) {            // of the sequence of row i
 #pragma unroll
-  for (int e = 0; e < VW; ++e) {
-    A[e] = 1.f;
-    H[e] = 0.f;
-  }
-  // the state that a sequence begins with
-  auto begin = [&](int i) {
-    const int64_t b = a.h0 ? sequence_at(a, m, p + i) : 0;
-#pragma unroll
-    for (int e = 0; e < VW; ++e) start[e] = a.h0 && c + e < a.D ? a.h0[b * a.D + c + e] : 0.f;
+    for (int e = 0; e < VW; ++e) h[e] = 0.f;
+    if (q) load_state<VW>(q, sequence_at(a, m, p + i), a.D, c, h);
   };
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (!(m.in >> i & 1)) continue;
-    if (m.begins >> i & 1) {
-      begin(i);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        A[e] = -1.f;
-        H[e] = start[e];
-      }
-    }
+  {
+    Run<TY, VW> g[ROWS], v[ROWS];
+    load_rows<TY, VW, ROWS>(g, a.g, a.gs, p, a.n, c);
+    load_rows<TY, VW, ROWS>(v, a.v, a.vs, p, a.n, c);
+    if constexpr (OUT) load_rows<TY, VW, ROWS>(o, a.o, a.os, p, a.n, c);
+    m = marks_of<ROWS>(a, p);
+    float A[VW], H[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      float up, down;
-      sigmoids<TY>(g[i].at(e), &up, &down);
-      A[e] *= up;
-      H[e] = up * H[e] + down * v[i].at(e);
+      A[e] = 1.f;
+      H[e] = 0.f;
     }
-  }
-  const Joined<VW> j = join_waves<VW, false>(room, A, H);
-  float state[VW], h[VW];
-  exchange<VW, false>(a, chunk, c, top.begins & 1, j, back, state);
 #pragma unroll
-  for (int e = 0; e < VW; ++e) {
-    h[e] = map_on(j.A[e], j.H[e], state[e]);
-    if (a.states && w * ROWS % kBwdChunk == 0 && p < a.n && c + e < a.D)
-      a.states[p / kBwdChunk * a.D + c + e] = h[e];
+    for (int i = 0; i < ROWS; ++i) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        float down;
+        sigmoids<TY>(g[i].at(e), &f[i][e], &down);
+        x[i][e] = down * v[i].at(e);
+      }
+      if (!(m.in >> i & 1)) continue;
+      if (m.begins >> i & 1) {
+        row(a.h0, i, H);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) A[e] = -1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        A[e] *= f[i][e];
+        H[e] = f[i][e] * H[e] + x[i][e];
+      }
+    }
+    put_map<VW>(room, A, H);
   }
+  __syncthreads();
+  if (w == 0) exchange<VW, false>(a, chunk, c, in, m.begins & 1, room);
+  __syncthreads();
+  if (!in) return;
+  float h[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) h[e] = room.in[w][e * 64 + lane];
+  if (a.states && w * ROWS % kBwdChunk == 0 && p < a.n)
+    store_run<kEltF32, VW>(a.states + p / kBwdChunk * a.D, c, h);
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     if (!(m.in >> i & 1)) continue;
-    if (m.begins >> i & 1) {
-      begin(i);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) h[e] = start[e];
-    }
+    if (m.begins >> i & 1) row(a.h0, i, h);
     float y[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      float up, down;
-      sigmoids<TY>(g[i].at(e), &up, &down);
-      h[e] = up * h[e] + down * v[i].at(e);
+      h[e] = f[i][e] * h[e] + x[i][e];
       y[e] = h[e];
       if constexpr (OUT) {
+        float up, down;
         const float z = o[i].at(e);
         sigmoids<TY>(z, &up, &down);
         y[e] *= z * up;
       }
     }
-    store_some<TY, VW>(a.y, (p + i) * a.ys + c, y, a.D - c);
-    if (a.hN && (m.ends >> i & 1)) {
-      const int64_t b = sequence_at(a, m, p + i);
-#pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (c + e < a.D) a.hN[b * a.D + c + e] = h[e];
-    }
+    store_row<TY, VW>(a.y, a.ys, p + i, c, y);
+    if (a.hN && (m.ends >> i & 1))
+      store_run<kEltF32, VW>(a.hN + sequence_at(a, m, p + i) * a.D, c, h);
   }
 }
 
@@ -400,94 +456,113 @@ __global__ __launch_bounds__(kThreads, 4) void fwd_kernel(Args a) {
 template <int TY, int VW, bool OUT>
 __global__ __launch_bounds__(kThreads, 4) void bwd_kernel(Args a) {
   constexpr int ROWS = kBwdRows;
-  __shared__ Room<VW> room[2], back;
+  __shared__ Room<VW> room, back;              // forwards and backwards
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t chunk;
   int tile;
   take_ticket(a, &chunk, &tile);
   chunk = a.chunks - 1 - chunk;
-  const int c = (tile * 64 + lane) * VW;
+  const int first = (tile * 64 + lane) * VW;
+  const bool in = first < a.D;
+  const uint32_t c = in ? first : 0;
   const int64_t p = chunk * kBwdChunk + w * ROWS;
-  Run<TY, VW> g[ROWS], v[ROWS], o[OUT ? ROWS : 1], dy[ROWS];
-  load_rows<TY, VW, ROWS>(g, a.g, a.gs, p, a.n, c, a.D);
-  load_rows<TY, VW, ROWS>(v, a.v, a.vs, p, a.n, c, a.D);
-  load_rows<TY, VW, ROWS>(dy, a.dy, a.dys, p, a.n, c, a.D);
-  if constexpr (OUT) load_rows<TY, VW, ROWS>(o, a.o, a.os, p, a.n, c, a.D);
-  float state[VW];
+  Run<TY, VW> v[ROWS];
+  // of each row: f and 1 - f, what reaches h, and (in LDS, for want of registers: a thread reads
+  // back what it wrote) the gradient of o over h
+  float f[ROWS][VW], d[ROWS][VW], q[ROWS][VW];
+  __shared__ float over[OUT ? ROWS : 1][VW][OUT ? kThreads : 1];
+  Marks m;
+  auto row = [&](const float* s, int i, float* h) {            // of the sequence of row i
 #pragma unroll
-  for (int e = 0; e < VW; ++e) state[e] = c + e < a.D ? a.states[chunk * a.D + c + e] : 0.f;
-  const Marks m = marks_of<ROWS>(a, p);
-  const int64_t final_row = chunk * kBwdChunk + kBwdChunk - ROWS;
-  const Marks bottom = marks_of<ROWS>(a, final_row);
-  // row of h0 or dhN of the sequence of row i
-  auto row = [&](const float* q, int i, float* x) {
-    const int64_t b = q ? sequence_at(a, m, p + i) : 0;
-#pragma unroll
-    for (int e = 0; e < VW; ++e) x[e] = q && c + e < a.D ? q[b * a.D + c + e] : 0.f;
+    for (int e = 0; e < VW; ++e) h[e] = 0.f;
+    if (s) load_state<VW>(s, sequence_at(a, m, p + i), a.D, c, h);
   };
-  float A[VW], H[VW], C[VW], K[VW];            // the map forwards, and backwards
+  {
+    Run<TY, VW> g[ROWS], o[OUT ? ROWS : 1], dy[ROWS];
+    load_rows<TY, VW, ROWS>(g, a.g, a.gs, p, a.n, c);
+    load_rows<TY, VW, ROWS>(v, a.v, a.vs, p, a.n, c);
+    load_rows<TY, VW, ROWS>(dy, a.dy, a.dys, p, a.n, c);
+    if constexpr (OUT) load_rows<TY, VW, ROWS>(o, a.o, a.os, p, a.n, c);
+    m = marks_of<ROWS>(a, p);
+    float A[VW], H[VW];
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      A[e] = 1.f;
+      H[e] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        sigmoids<TY>(g[i].at(e), &f[i][e], &d[i][e]);
+        q[i][e] = dy[i].at(e);
+        if constexpr (OUT) {
+          float up, down;
+          const float z = o[i].at(e);
+          sigmoids<TY>(z, &up, &down);
+          over[i][e][threadIdx.x] = q[i][e] * (up * (1.f + z * down));
+          q[i][e] *= z * up;
+        }
+      }
+      if (!(m.in >> i & 1)) continue;
+      if (m.begins >> i & 1) {
+        row(a.h0, i, H);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) A[e] = -1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        A[e] *= f[i][e];
+        H[e] = f[i][e] * H[e] + d[i][e] * v[i].at(e);
+      }
+    }
+    put_map<VW>(room, A, H);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      A[e] = 1.f;
+      H[e] = 0.f;
+    }
+#pragma unroll
+    for (int i = ROWS - 1; i >= 0; --i) {
+      if (!(m.in >> i & 1)) continue;
+      if (m.ends >> i & 1) {
+        row(a.dhN, i, H);
+#pragma unroll
+        for (int e = 0; e < VW; ++e) A[e] = -1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        A[e] *= f[i][e];
+        H[e] = f[i][e] * (q[i][e] + H[e]);
+      }
+    }
+    put_map<VW>(back, A, H);
+  }
+  __syncthreads();
+  // the first wave that the carry comes into, and another for the states
+  if (w == kWaves - 1) {
+    exchange<VW, true>(a, chunk, c, in, m.ends >> (ROWS - 1) & 1, back);
+  } else if (w == 0) {
+    float state[VW];
+    load_state<VW>(a.states, chunk, a.D, c, state);
+    pass_state<VW, false>(room, state);
+  }
+  __syncthreads();
+  if (!in) return;
+  float before[ROWS][VW], h[VW], carry[VW];    // the state before each row
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    A[e] = C[e] = 1.f;
-    H[e] = K[e] = 0.f;
+    h[e] = room.in[w][e * 64 + lane];
+    carry[e] = back.in[w][e * 64 + lane];
   }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (!(m.in >> i & 1)) continue;
-    if (m.begins >> i & 1) {
-      row(a.h0, i, H);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) A[e] = -1.f;
-    }
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      float up, down;
-      sigmoids<TY>(g[i].at(e), &up, &down);
-      A[e] *= up;
-      H[e] = up * H[e] + down * v[i].at(e);
-    }
-  }
-#pragma unroll
-  for (int i = ROWS - 1; i >= 0; --i) {
-    if (!(m.in >> i & 1)) continue;
-    if (m.ends >> i & 1) {
-      row(a.dhN, i, K);
-#pragma unroll
-      for (int e = 0; e < VW; ++e) C[e] = -1.f;
-    }
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      float up, down, q = dy[i].at(e);
-      if constexpr (OUT) {
-        float zu, zd;
-        const float z = o[i].at(e);
-        sigmoids<TY>(z, &zu, &zd);
-        q *= z * zu;
-      }
-      sigmoids<TY>(g[i].at(e), &up, &down);
-      C[e] *= up;
-      K[e] = up * (q + K[e]);
-    }
-  }
-  const Joined<VW> j = join_waves<VW, true>(room[1], C, K);
-  float carry[VW];
-  exchange<VW, true>(a, chunk, c, bottom.ends >> (ROWS - 1) & 1, j, back, carry);
-#pragma unroll
-  for (int e = 0; e < VW; ++e) carry[e] = map_on(j.A[e], j.H[e], carry[e]);
-  const Joined<VW> f = join_waves<VW, false>(room[0], A, H);
-  float before[ROWS][VW], h[VW];               // the state before each row
-#pragma unroll
-  for (int e = 0; e < VW; ++e) h[e] = map_on(f.A[e], f.H[e], state[e]);
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     if (m.begins >> i & 1) row(a.h0, i, h);
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
       before[i][e] = h[e];
-      float up, down;
-      sigmoids<TY>(g[i].at(e), &up, &down);
-      if (m.in >> i & 1) h[e] = up * h[e] + down * v[i].at(e);
+      if (m.in >> i & 1) h[e] = f[i][e] * h[e] + d[i][e] * v[i].at(e);
     }
   }
 #pragma unroll
@@ -497,30 +572,18 @@ __global__ __launch_bounds__(kThreads, 4) void bwd_kernel(Args a) {
     float dg[VW], dv[VW], dz[VW];
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
-      float up, down, q = dy[i].at(e);
-      sigmoids<TY>(g[i].at(e), &up, &down);
       const float val = v[i].at(e);
-      if constexpr (OUT) {
-        float zu, zd;
-        const float z = o[i].at(e), now = up * before[i][e] + down * val;
-        sigmoids<TY>(z, &zu, &zd);
-        dz[e] = q * now * zu * (1.f + z * zd);
-        q *= z * zu;
-      }
-      const float dh = q + carry[e];
-      dv[e] = down * dh;
-      dg[e] = dh * (before[i][e] - val) * (up * down);
-      carry[e] = up * dh;
+      if constexpr (OUT) dz[e] = over[i][e][threadIdx.x] * (f[i][e] * before[i][e] + d[i][e] * val);
+      const float dh = q[i][e] + carry[e];
+      dv[e] = d[i][e] * dh;
+      dg[e] = dh * (before[i][e] - val) * (f[i][e] * d[i][e]);
+      carry[e] = f[i][e] * dh;
     }
-    store_some<TY, VW>(a.dv, (p + i) * a.dvs + c, dv, a.D - c);
-    store_some<TY, VW>(a.dg, (p + i) * a.dgs + c, dg, a.D - c);
-    if constexpr (OUT) store_some<TY, VW>(a.dout, (p + i) * a.dos + c, dz, a.D - c);
-    if (a.dh0 && (m.begins >> i & 1)) {
-      const int64_t b = sequence_at(a, m, p + i);
-#pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (c + e < a.D) a.dh0[b * a.D + c + e] = carry[e];
-    }
+    store_row<TY, VW>(a.dv, a.dvs, p + i, c, dv);
+    store_row<TY, VW>(a.dg, a.dgs, p + i, c, dg);
+    if constexpr (OUT) store_row<TY, VW>(a.dout, a.dos, p + i, c, dz);
+    if (a.dh0 && (m.begins >> i & 1))
+      store_run<kEltF32, VW>(a.dh0 + sequence_at(a, m, p + i) * a.D, c, carry);
   }
 }
 
@@ -589,15 +652,17 @@ __global__ __launch_bounds__(256) void step_kernel(Args a, const int32_t* __rest
 
 int64_t pieces(int64_t n, int64_t size) { return (n + size - 1) / size; }
 
-// Four bytes a lane: a channel of binary32, or two of 16 bits where every row begins on 4 bytes.
-bool pairs(int dtype, const void* p, int64_t stride) {
-  return dtype != kEltF32 && reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
+// Four bytes a lane: a channel of binary32, or two of 16 bits where every row is whole pairs that
+// begin on 4 bytes.
+bool pairs(int dtype, int D, const void* p, int64_t stride) {
+  return dtype != kEltF32 && D % 2 == 0 && reinterpret_cast<uintptr_t>(p) % 4 == 0 &&
+         stride % 2 == 0;
 }
 
 // The workspace: counter, marks, words.
 size_t carve_scan(Args* a, void* workspace, int64_t n, int D, int chunk) {
   const int64_t chunks = pieces(n, chunk);
-  size_t off = 256;
+  size_t off = (size_t)pieces(D, 64) * kCounter * 4;
   char* base = static_cast<char*>(workspace);
   const size_t marks = off;
   off += ((size_t)pieces(n, kGroup) * sizeof(Marks) + 255) / 256 * 256;
@@ -617,11 +682,12 @@ hipError_t run(Args a, int dtype, bool back, bool two, hipStream_t s) {
   const float* from = back ? a.dhN : a.h0;
   float* to = back ? a.dh0 : a.hN;
   if (a.n == 0 && !to) return hipSuccess;
-  const int64_t work = a.chunks * a.D > a.B ? a.chunks * a.D : a.B;
-  const int64_t blocks = pieces(work, 1024);
+  const int64_t clear = pieces(a.chunks * a.D, 1024), marks = pieces(a.n, 256 * kGroup);
+  int64_t blocks = clear > marks ? clear : marks;
+  if (to && blocks < a.B) blocks = a.B;
+  a.tiles = (int)pieces(a.D, two ? 128 : 64);
   prepare_kernel<<<(unsigned)(blocks < 2048 ? blocks : 2048), 256, 0, s>>>(a, from, to);
   if (a.n == 0) return hipGetLastError();
-  a.tiles = (int)pieces(a.D, two ? 128 : 64);
   const unsigned grid = (unsigned)(a.chunks * a.tiles);
   return for_type(dtype, [&](auto ty) {
     constexpr int TY = decltype(ty)::value;
@@ -659,8 +725,8 @@ hipError_t launch_gated_scan_fwd(const void* g, int64_t gs, const void* v, int64
   a.g = g; a.gs = gs; a.v = v; a.vs = vs; a.o = o; a.os = os; a.offsets = offsets;
   a.n = n; a.B = B; a.D = D; a.h0 = h0; a.y = y; a.ys = ys; a.hN = hN; a.states = states;
   scan::carve_scan(&a, workspace, n, D, scan::kFwdChunk);
-  const bool two = scan::pairs(dtype, g, gs) && scan::pairs(dtype, v, vs) &&
-                   scan::pairs(dtype, o, os) && scan::pairs(dtype, y, ys);
+  const bool two = scan::pairs(dtype, D, g, gs) && scan::pairs(dtype, D, v, vs) &&
+                   scan::pairs(dtype, D, o, os) && scan::pairs(dtype, D, y, ys);
   return scan::run(a, dtype, false, two, s);
 }
 
@@ -676,10 +742,10 @@ hipError_t launch_gated_scan_bwd(const void* g, int64_t gs, const void* v, int64
   a.dy = dy; a.dys = dys; a.dhN = dhN; a.dg = dg; a.dgs = dgs; a.dv = dv; a.dvs = dvs;
   a.dout = dout; a.dos = dos; a.dh0 = dh0;
   scan::carve_scan(&a, workspace, n, D, scan::kBwdChunk);
-  const bool two = scan::pairs(dtype, g, gs) && scan::pairs(dtype, v, vs) &&
-                   scan::pairs(dtype, o, os) && scan::pairs(dtype, dy, dys) &&
-                   scan::pairs(dtype, dg, dgs) && scan::pairs(dtype, dv, dvs) &&
-                   scan::pairs(dtype, dout, dos);
+  const bool two = scan::pairs(dtype, D, g, gs) && scan::pairs(dtype, D, v, vs) &&
+                   scan::pairs(dtype, D, o, os) && scan::pairs(dtype, D, dy, dys) &&
+                   scan::pairs(dtype, D, dg, dgs) && scan::pairs(dtype, D, dv, dvs) &&
+                   scan::pairs(dtype, D, dout, dos);
   return scan::run(a, dtype, true, two, s);
 }
 
@@ -690,8 +756,8 @@ hipError_t launch_gated_scan_step(const void* g, int64_t gs, const void* v, int6
   if (B == 0) return hipSuccess;
   scan::Args a{};
   a.g = g; a.gs = gs; a.v = v; a.vs = vs; a.o = o; a.os = os; a.B = B; a.D = D; a.y = y; a.ys = ys;
-  const bool two = scan::pairs(dtype, g, gs) && scan::pairs(dtype, v, vs) &&
-                   scan::pairs(dtype, o, os) && scan::pairs(dtype, y, ys);
+  const bool two = scan::pairs(dtype, D, g, gs) && scan::pairs(dtype, D, v, vs) &&
+                   scan::pairs(dtype, D, o, os) && scan::pairs(dtype, D, y, ys);
   return for_type(dtype, [&](auto ty) {
     constexpr int TY = decltype(ty)::value;
     auto go = [&](auto vw, auto out) {
