@@ -45,24 +45,32 @@ struct Args {
   int col_tiles;
 };
 
-__device__ __forceinline__ float activate(float x, int act) {
-  if (act == kRelu) return x > 0.f ? x : 0.f;                  // NaN gives 0
-  if (act == kSilu) return x / (1.f + expf(-x));
-  if (act == kGelu) return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
-  return x;
+// act of E values; a NaN stays, but relu makes it 0.
+template <int E>
+__device__ __forceinline__ void activate(float* v, int act) {
+  if (act == kRelu) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = v[e] > 0.f ? v[e] : 0.f;
+  } else if (act == kSilu) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = v[e] / (1.f + expf(-v[e]));
+  } else if (act == kGelu) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.5f * v[e] * (1.f + erff(v[e] * 0.70710678118654752f));
+  }
 }
 
-// What becomes of E sums of row m, columns c on (all in the row but for the last `N - c`).
+// What becomes of E sums, times their row's scale, of row m, columns c on (of which the last
+// `N - c` are there), and of the residual's values at the same places.
 template <int TO, int E>
-__device__ __forceinline__ void finish(const Args& g, int64_t m, int c, float* v, float xs,
-                                       const float* ws, const float* b) {
-  Run<TO, E> r;
-  if (g.R) r.load_some(g.R, m * g.rs + c, g.N - c);
+__device__ __forceinline__ void finish(const Args& g, int64_t m, int c, float* v, const float* ws,
+                                       const float* b, const Run<TO, E>& r) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    v[e] = activate(v[e] * xs * ws[e] + b[e], g.act);
-    if (g.R) v[e] += r.at(e);
-  }
+  for (int e = 0; e < E; ++e) v[e] = v[e] * ws[e] + b[e];
+  activate<E>(v, g.act);
+  if (g.R)
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += r.at(e);
   store_some<TO, E>(g.Y, m * g.ys + c, v, g.N - c);
 }
 template <int E>
@@ -85,14 +93,180 @@ __device__ __forceinline__ void column_values(const Args& g, int c, float* ws, f
 // row r is at c ^ (r / 2 & 7) of its row, so that sixteen lanes that read piece c of sixteen rows
 // touch all banks.  A round has two half steps of 64 values: one matrix instruction each for
 // every 32 x 32 tile, whose operands are two pieces of a row.  (Which 32 of the 64 values a lane
-// holds is free, as long as both operands agree.)  With eight waves the second four run one part
-// behind the first: while one of a SIMD's waves computes, the other moves data.
+// holds is free, as long as both operands agree.)
 constexpr int kRound = 128, kHalf = 64;        // reduction values
+
+// 16 bytes a lane from base + off + more to lds + 16 * lane (all but off the same in the whole
+// wave), zeros from base + end on.
+__device__ __forceinline__ void to_lds(const uint8_t* base, uint32_t end, uint32_t off,
+                                       uint32_t more, uint16_t* lds) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(base), (short)0, (int)end, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
+                                           (int)off, (int)more, 0, 0);
+}
+// One round of an operand to LDS, its reduction values [k, k + 128): LOADS loads a wave, number
+// q * WAVES + w of wave w eight rows from base on, lane i row i / 8 and its piece at `off`.  Rows
+// from `rows` on are zeros by the buffer's end, and so are pieces from K on by `piece`.
+template <int WAVES, int LOADS>
+__device__ __forceinline__ void load_round(uint16_t* to, const uint8_t* base, int64_t stride,
+                                           uint32_t off, int piece, int rows, int K, int k, int w) {
+  const int left = K - k > 0 ? K - k : 0;
+  const uint32_t from = piece < left ? off : experts::kNowhere;
+  const uint32_t end = left > 0 ? (uint32_t)((rows - 1) * stride + left) : 0u;
+#pragma unroll
+  for (int q = 0; q < LOADS; ++q) {
+    const int i = q * WAVES + w;
+    to_lds(base + k, end, from, (uint32_t)(8 * i * stride), to + i * 512);
+  }
+}
+
+// Neighbouring tiles, which share operands, to one XCD.
+__device__ __forceinline__ uint32_t tile_of() {
+  const uint32_t per = gridDim.x / kXcds;
+  return blockIdx.x < per * kXcds ? blockIdx.x % kXcds * per + blockIdx.x / kXcds : blockIdx.x;
+}
+
+// A lane's 32 values of half step h from LDS: two pieces of its row, whose first is at `from`.
+template <typename H>
+__device__ __forceinline__ i32x8 fragment(const uint16_t* L, uint32_t from, H) {
+  const char* p = reinterpret_cast<const char*>(L);
+  const i32x4 lo = *reinterpret_cast<const i32x4*>(p + (from ^ (64 * H::value)));
+  const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (from ^ (64 * H::value + 32)));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The products of a half step: rows a, columns b.  The matrix cores take the columns as their
+// rows: a lane then holds four neighbouring columns of one output row.
+template <int TO, int TI, int TJ>
+__device__ __forceinline__ void multiply_part(const i32x8 (&a)[TI], const i32x8 (&b)[TJ],
+                                              f32x16 (&acc)[TI][TJ]) {
+  if constexpr (TO == kEltF32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      experts::f16x8 x[TI], y[TJ];
+#pragma unroll
+      for (int i = 0; i < TI; ++i) x[i] = widen(a[i][2 * q], a[i][2 * q + 1]);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) y[j] = widen(b[j][2 * q], b[j][2 * q + 1]);
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[j], x[i], acc[i][j], 0, 0, 0);
+    }
+  } else {
+    // both operands e4m3, scales of the matrix instruction 2^0
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            b[j], a[i], acc[i][j], 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+  }
+}
+
+// The lane, from a number that the compiler does not know: what it made of it would stay in
+// registers over the products.
+__device__ __forceinline__ int late_lane() {
+  int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// 32 rows of a wave's sums, times their rows' scale, into its part of LDS: row lane % 32 and column
+// 32 j + 8 (v / 4) + 4 (lane / 32) + v % 4 are in acc[j][v].
+// (The comments to the assembler keep the parts' code apart: joined, it would index the sums.)
+template <int PART, int TJ>
+__device__ __forceinline__ void stage_rows(const f32x16 (&acc)[TJ], float xs, char* out) {
+  asm volatile("; part %0" ::"n"(PART));
+  constexpr int WN = 32 * TJ;
+  const int lane = late_lane(), rl = lane & 31, kg = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < TJ; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int at4 = 8 * j + 2 * q + kg;
+      *reinterpret_cast<f32x4*>(out + rl * WN * 4 + (at4 ^ (rl & (WN / 4 - 1))) * 16) =
+          f32x4{acc[j][4 * q] * xs, acc[j][4 * q + 1] * xs, acc[j][4 * q + 2] * xs,
+                acc[j][4 * q + 3] * xs};
+    }
+  asm volatile("; end of part %0" ::"n"(PART));
+}
+
+// What a lane needs for its sums: the scales of its row in each 32, scales and biases of its columns.
+template <int TI>
+struct With {
+  float xs[TI], ws[8], b[8];
+};
+template <int TI, int TJ>
+__device__ __forceinline__ void load_with(const Args& g, int64_t m0, int c0, With<TI>& with) {
+  const int lane = late_lane();
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int64_t m = m0 + 32 * i + (lane & 31);
+    with.xs[i] = g.x_scale[m < g.M ? m : g.M - 1];
+  }
+  column_values<8>(g, c0 + 8 * (lane % (4 * TJ)), with.ws, with.b);
+}
+
+// All of a wave's sums, from row m0 and column c0 on, 32 rows at a time through its part of LDS
+// (`out`), so that a lane has eight neighbouring columns of a row.  Batches of NB rows a lane; the
+// residual's rows of the next batch are loaded ahead.  A loop and not written out, for it is the
+// instructions' way from memory that takes the time of what runs once (32768 x 2208 x 2048: 224 us
+// written out); only the staging is, for the sums stay in registers if no index of theirs is left.
+template <int TO, int TI, int TJ>
+__device__ __forceinline__ void store_part(const Args& g, const f32x16 (&acc)[TI][TJ],
+                                           const With<TI>& with, char* out, int64_t m0, int c0) {
+  constexpr int WN = 32 * TJ, LR = WN / 8, PASSES = 32 * LR / 64, NB = PASSES < 4 ? PASSES : 4;
+  constexpr int EACH = PASSES / NB, BATCHES = TI * EACH, STEP = 64 / LR;
+  const int lane = late_lane(), l = lane % LR, rr = lane / LR, c = c0 + 8 * l;
+  const auto& [xs, ws, b] = with;
+  Run<TO, 8> r[NB], next[NB];
+  auto residual = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const int64_t m = m0 + (k * NB + u) * STEP + rr;
+      next[u].load_some(g.R, m * g.rs + c, m < g.M ? g.N - c : 0);
+    }
+  };
+  if (g.R) residual(0);
+#pragma unroll 1
+  for (int k = 0; k < BATCHES; ++k) {
+    if (k % EACH == 0) {
+      __builtin_amdgcn_wave_barrier();
+      const int i = k / EACH;
+      if (i == 0) stage_rows<0>(acc[0], xs[0], out);
+      if constexpr (TI > 1)
+        if (i == 1) stage_rows<1>(acc[1], xs[1], out);
+      if constexpr (TI > 2)
+        if (i == 2) stage_rows<2>(acc[2], xs[2], out);
+      if constexpr (TI > 3)
+        if (i == 3) stage_rows<3>(acc[3], xs[3], out);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int u = 0; u < NB; ++u) r[u] = next[u];
+    if (g.R && k + 1 < BATCHES) residual(k + 1);
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const int at = (k * NB + u) * STEP + rr, row = at % 32;
+      const f32x4 lo =
+          *reinterpret_cast<const f32x4*>(out + row * WN * 4 + ((2 * l) ^ (row & (WN / 4 - 1))) * 16);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(
+          out + row * WN * 4 + ((2 * l + 1) ^ (row & (WN / 4 - 1))) * 16);
+      if (m0 + at < g.M && c < g.N) {
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        finish<TO, 8>(g, m0 + at, c, v, ws, b, r[u]);
+      }
+    }
+  }
+}
 
 template <int TO, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void tile_kernel(Args g) {
   constexpr int WAVES = (BM / WM) * (BN / WN), WN_WAVES = BN / WN;
-  constexpr bool PAIRED = WAVES == 8;
   constexpr int TI = WM / 32, TJ = WN / 32;
   constexpr int AL = BM / 8 / WAVES, BL = BN / 8 / WAVES;      // loads a wave and round
   constexpr int SLOT = (BM > BN ? BM : BN) * kRound / 2;       // in 16-bit units
@@ -102,37 +276,22 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void tile_kernel(Arg
   const int wm = w / WN_WAVES, wn = w % WN_WAVES;
   const int rl = lane & 31, kg = lane >> 5;
 
-  // neighbouring tiles, which share operands, to one XCD
-  const uint32_t per = gridDim.x / kXcds;
-  const uint32_t at = blockIdx.x < per * kXcds
-                          ? blockIdx.x % kXcds * per + blockIdx.x / kXcds : blockIdx.x;
+  const uint32_t at = tile_of();
   const int64_t m0 = (int64_t)(at / (uint32_t)g.col_tiles) * BM;
   const int n0 = (int)(at % (uint32_t)g.col_tiles) * BN;
   const int arows = (int)(g.M - m0 < BM ? g.M - m0 : BM), brows = g.N - n0 < BN ? g.N - n0 : BN;
 
   // load q of wave w is number q * WAVES + w: eight rows, lane i row i / 8 and its piece
   const int piece = ((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) * 16;
-  const uint8_t* abase = g.X + m0 * g.xs;
-  const uint8_t* bbase = g.W + (int64_t)n0 * g.ws;
+  const uint8_t* const abase = g.X + m0 * g.xs;
+  const uint8_t* const bbase = g.W + (int64_t)n0 * g.ws;
   const uint32_t aoff = (uint32_t)((lane >> 3) * g.xs) + piece;
   const uint32_t boff = (uint32_t)((lane >> 3) * g.ws) + piece;
   auto load_a = [&](uint16_t* A, int k) {
-#pragma unroll
-    for (int q = 0; q < AL; ++q) {
-      const int i = q * WAVES + w;
-      const bool in = piece < g.K - k && (lane >> 3) < arows - 8 * i;
-      experts::to_lds(abase, in ? aoff : experts::kNowhere, (uint32_t)(8 * i * g.xs), A + i * 512);
-    }
-    abase += kRound;
+    load_round<WAVES, AL>(A, abase, g.xs, aoff, piece, arows, g.K, k, w);
   };
   auto load_b = [&](uint16_t* B, int k) {
-#pragma unroll
-    for (int q = 0; q < BL; ++q) {
-      const int i = q * WAVES + w;
-      const bool in = piece < g.K - k && (lane >> 3) < brows - 8 * i;
-      experts::to_lds(bbase, in ? boff : experts::kNowhere, (uint32_t)(8 * i * g.ws), B + i * 512);
-    }
-    bbase += kRound;
+    load_round<WAVES, BL>(B, bbase, g.ws, boff, piece, brows, g.K, k, w);
   };
 
   const uint32_t afrag = (WM * wm + rl) * kRound + (kg ^ (rl >> 1 & 7)) * 16;
@@ -150,43 +309,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void tile_kernel(Arg
     i32x8 a[TI], b[TJ];
     uint32_t aat = afrag, bat = bfrag;
     asm volatile("" : "+v"(aat), "+v"(bat));
-    auto frag = [&](const uint16_t* L, uint32_t from) {
-      const char* p = reinterpret_cast<const char*>(L);
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(p + (from ^ (64 * decltype(h)::value)));
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (from ^ (64 * decltype(h)::value + 32)));
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    };
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) b[j] = frag(B + 32 * j * kRound / 2, bat);
+    for (int j = 0; j < TJ; ++j) b[j] = fragment(B + 32 * j * kRound / 2, bat, h);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) a[i] = frag(A + 32 * i * kRound / 2, aat);
+    for (int i = 0; i < TI; ++i) a[i] = fragment(A + 32 * i * kRound / 2, aat, h);
     ahead();
     __builtin_amdgcn_s_setprio(1);
-    if constexpr (TO == kEltF32) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        experts::f16x8 x[TI], y[TJ];
-#pragma unroll
-        for (int i = 0; i < TI; ++i) x[i] = widen(a[i][2 * q], a[i][2 * q + 1]);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) y[j] = widen(b[j][2 * q], b[j][2 * q + 1]);
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-          for (int j = 0; j < TJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(y[j], x[i], acc[i][j], 0, 0, 0);
-      }
-    } else {
-      // both operands e4m3, scales of the matrix instruction 2^0
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              b[j], a[i], acc[i][j], 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-    }
+    multiply_part<TO, TI, TJ>(a, b, acc);
     __builtin_amdgcn_s_setprio(0);
-    if constexpr (PAIRED) experts::arrive_only();
   };
 
   // Loads past the last round read nowhere: the counts of loads in flight stay the same, and all
@@ -210,7 +340,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void tile_kernel(Arg
       });
   };
   experts::arrive<AL>();
-  if (PAIRED && w >= WAVES / 2) experts::arrive_only();
   for (int j = 0; j < rounds; j += 5) {
     round(R0, R1, R3, R4, j);
     if (j + 1 < rounds) round(R2, R3, R0, R1, j + 1);
@@ -218,45 +347,131 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void tile_kernel(Arg
     if (j + 3 < rounds) round(R1, R2, R4, R0, j + 3);
     if (j + 4 < rounds) round(R3, R4, R1, R2, j + 4);
   }
-  if (PAIRED && w < WAVES / 2) experts::arrive_only();
   __syncthreads();
 
-  // acc[i][j][v] is row 32 i + rl, column 32 j + 8 (v / 4) + 4 kg + v % 4 of the wave's part.  32
-  // rows at a time go through LDS, so that a lane has eight neighbouring columns of a row.
-  constexpr int LR = WN / 8, BYTES = 32 * WN * 4, EACH = SLOT * 2 / BYTES;
+  constexpr int BYTES = 32 * WN * 4, EACH = SLOT * 2 / BYTES;
   static_assert(2 * EACH >= WAVES, "the waves' parts fit");
-  char* const out = reinterpret_cast<char*>(w < EACH ? R0 : R1) + (w % EACH) * BYTES;
-  const int l = lane % LR, rr = lane / LR, c = n0 + WN * wn + 8 * l;
-  float ws[8], b[8];
-  column_values<8>(g, c, ws, b);
+  With<TI> with;
+  load_with<TI, TJ>(g, m0 + WM * wm, n0 + WN * wn, with);
+  store_part<TO, TI, TJ>(g, acc, with,
+                         reinterpret_cast<char*>(w < EACH ? R0 : R1) + (w % EACH) * BYTES,
+                         m0 + WM * wm, n0 + WN * wn);
+}
+
+// The largest tiles: 256 x 256, a wave 128 x 128 of it, so that a fragment from LDS serves four
+// matrix instructions (with eight waves of 128 x 64 LDS was busy all the time: 96 KB of fragments
+// and 32 KB of loads in the 1024 cycles of a half step's instructions).  One wave a SIMD: the
+// next half step's fragments are read into registers of their own while this one's instructions
+// run.  All reads of round j end with its first half step, so one barrier a round, in its second
+// one, frees both of its slots and says that round j + 1 has landed; B of round j + 2 and A of
+// round j + 3 are loaded into them.
+// (Blocks that stay, with the next tile's first loads before this one's results are stored: the
+// registers ran out, 214 us for 177 at 32768 x 2208 x 2048.)
+template <int TO>
+__global__ __launch_bounds__(256, 1) void big_kernel(Args g) {
+  constexpr int BM = 256, WAVES = 4, T = 4;
+  constexpr int L = BM / 8 / WAVES;                            // loads a wave, round and operand
+  constexpr int SLOT = BM * kRound / 2;                        // in 16-bit units
+  __shared__ __attribute__((aligned(16))) uint16_t R0[SLOT], R1[SLOT], R2[SLOT], R3[SLOT], R4[SLOT];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w >> 1, wn = w & 1, rl = lane & 31, kg = lane >> 5;
+  const int piece = ((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) * 16;
+  const uint32_t aoff = (uint32_t)((lane >> 3) * g.xs) + piece;
+  const uint32_t boff = (uint32_t)((lane >> 3) * g.ws) + piece;
+  const uint32_t at = tile_of();
+  const int64_t m0 = (int64_t)(at / (uint32_t)g.col_tiles) * BM;
+  const int n0 = (int)(at % (uint32_t)g.col_tiles) * BM;
+  const int arows = (int)(g.M - m0 < BM ? g.M - m0 : BM), brows = g.N - n0 < BM ? g.N - n0 : BM;
+  const uint8_t* const abase = g.X + m0 * g.xs;
+  const uint8_t* const bbase = g.W + (int64_t)n0 * g.ws;
+  auto load_a = [&](uint16_t* to, int j) {
+    load_round<WAVES, L>(to, abase, g.xs, aoff, piece, arows, g.K, j * kRound, w);
+  };
+  auto load_b = [&](uint16_t* to, int j) {
+    load_round<WAVES, L>(to, bbase, g.ws, boff, piece, brows, g.K, j * kRound, w);
+  };
+  const uint32_t afrag = (128 * wm + rl) * kRound + (kg ^ (rl >> 1 & 7)) * 16;
+  const uint32_t bfrag = (128 * wn + rl) * kRound + (kg ^ (rl >> 1 & 7)) * 16;
+  f32x16 acc[T][T];
+  i32x8 x[2][T], y[2][T];                      // fragments of this half step and the next
+  auto read = [&](const uint16_t* A, const uint16_t* B, auto h) {
+    constexpr int H = decltype(h)::value;
+    // the addresses are made here each time: kept for all slots they would take the registers
+    // that the fragments need
+    uint32_t a = afrag, b = bfrag;
+    asm volatile("" : "+v"(a), "+v"(b));
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
-#pragma unroll
-    for (int j = 0; j < TJ; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at4 = 8 * j + 2 * q + kg;
-        *reinterpret_cast<f32x4*>(out + rl * WN * 4 + (at4 ^ (rl & (WN / 4 - 1))) * 16) =
-            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                  acc[i][j][4 * q + 3]};
-      }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int t = 0; t < 32 * LR / 64; ++t) {
-      const int r = t * (64 / LR) + rr;
-      const int64_t m = m0 + WM * wm + 32 * i + r;
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(
-          out + r * WN * 4 + ((2 * l) ^ (r & (WN / 4 - 1))) * 16);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(
-          out + r * WN * 4 + ((2 * l + 1) ^ (r & (WN / 4 - 1))) * 16);
-      if (m < g.M && c < g.N) {
-        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        finish<TO, 8>(g, m, c, v, g.x_scale[m], ws, b);
-      }
+    for (int i = 0; i < T; ++i) {
+      x[H][i] = fragment(A + 32 * i * kRound / 2, a, h);
+      y[H][i] = fragment(B + 32 * i * kRound / 2, b, h);
     }
-    __builtin_amdgcn_wave_barrier();
+  };
+  auto multiply = [&](auto h) {
+    constexpr int H = decltype(h)::value;
+    multiply_part<TO, T, T>(x[H], y[H], acc);
+  };
+  constexpr std::integral_constant<int, 0> first{};
+  constexpr std::integral_constant<int, 1> second{};
+
+  // Behind every matrix instruction one load to LDS (if there are any) and one read from it.
+  auto interleave = [&] {
+#pragma unroll
+    for (int i = 0; i < T * T; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // matrix instructions
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);       // loads from memory
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);       // LDS reads
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int rounds = (g.K + kRound - 1) / kRound;
+  // Round j from A and B, read from already; An and Bn hold round j + 1.  (Loads past the last
+  // round read nowhere, and so the counts of loads in flight stay the same.)
+  auto round = [&](uint16_t* A, uint16_t* B, const uint16_t* An, const uint16_t* Bn, int j) {
+    __builtin_amdgcn_sched_barrier(0);
+    read(A, B, second);
+    multiply(first);
+    interleave();
+    experts::arrive<L>();
+    load_b(A, j + 2);
+    load_a(B, j + 3);
+    read(An, Bn, first);
+    multiply(second);
+    interleave();
+  };
+  load_a(R0, 0);
+  load_b(R1, 0);
+  load_a(R2, 1);
+  load_b(R3, 1);
+  load_a(R4, 2);
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  experts::arrive<3 * L>();
+  read(R0, R1, first);
+  // (No way from the middle of the loop to its head: the compiler would wait for all loads there.)
+  int j = 0;
+  for (; j + 5 <= rounds; j += 5) {
+    round(R0, R1, R2, R3, j);
+    round(R2, R3, R4, R0, j + 1);
+    round(R4, R0, R1, R2, j + 2);
+    round(R1, R2, R3, R4, j + 3);
+    round(R3, R4, R0, R1, j + 4);
   }
+  if (j < rounds) round(R0, R1, R2, R3, j);
+  if (j + 1 < rounds) round(R2, R3, R4, R0, j + 1);
+  if (j + 2 < rounds) round(R4, R0, R1, R2, j + 2);
+  if (j + 3 < rounds) round(R1, R2, R3, R4, j + 3);
+  experts::arrive<0>();
+  With<T> with;
+  load_with<T, T>(g, m0 + 128 * wm, n0 + 128 * wn, with);
+  constexpr int BYTES = 32 * 128 * 4;
+  static_assert(SLOT * 2 == 2 * BYTES, "two waves' parts a slot");
+  store_part<TO, T, T>(g, acc, with, reinterpret_cast<char*>(w < 2 ? R0 : R1) + (w & 1) * BYTES,
+                       m0 + 128 * wm, n0 + 128 * wn);
 }
 
 // -------------------------------------------------------------------------------- few rows
@@ -319,9 +534,12 @@ __global__ __launch_bounds__(kThreads) void few_kernel(Args g) {
   const int c = n0 + 4 * kg;
   if (w < RT && m < g.M && c < g.N) {
     const f32x4 s = ((red[0][w][lane] + red[1][w][lane]) + red[2][w][lane]) + red[3][w][lane];
-    float v[4] = {s[0], s[1], s[2], s[3]}, ws[4], b[4];
+    const float xs = g.x_scale[m];
+    float v[4] = {s[0] * xs, s[1] * xs, s[2] * xs, s[3] * xs}, ws[4], b[4];
     column_values<4>(g, c, ws, b);
-    finish<TO, 4>(g, m, c, v, g.x_scale[m], ws, b);
+    Run<TO, 4> r;
+    if (g.R) r.load_some(g.R, m * g.rs + c, g.N - c);
+    finish<TO, 4>(g, m, c, v, ws, b, r);
   }
 }
 
@@ -345,7 +563,7 @@ hipError_t launch_quant_dense_fwd(const void* X, int64_t xs, int64_t M, int K,
   g.X = static_cast<const uint8_t*>(X); g.xs = xs; g.x_scale = x_scale;
   g.W = static_cast<const uint8_t*>(W); g.ws = ws; g.w_scale = w_scale;
   g.b = b; g.R = R; g.rs = rs; g.Y = Y; g.ys = ys; g.M = M; g.N = N; g.K = K; g.act = act;
-  return for_type(dtype, [&](auto ty) {
+  return for_type(dtype, [&](auto ty) -> hipError_t {
     constexpr int TO = decltype(ty)::value;
     const unsigned cols = (unsigned)((N + 15) / 16);
     if (M <= 16) {
@@ -361,7 +579,14 @@ hipError_t launch_quant_dense_fwd(const void* X, int64_t xs, int64_t M, int K,
       return hipGetLastError();
     }
     auto tiles = [&](int64_t b) { return (M + b - 1) / b * ((N + b - 1) / b); };
-    if (tiles(256) >= 256) return quant::launch_tiles<TO, 256, 256, 128, 64>(g, s);
+    // 256 x 256 takes 19 us and 11.4 ns a reduction value a round of 256 tiles, the same in tiles of
+    // 128 x 128 7 us and 21.9 ns (16384 x 512 x 2048, 8192 x 1024 x 4096 and 32768 x 2208 x 2048:
+    // 128 38, 59 and 221 us, 256 -, 61 and 177 us)
+    if (tiles(256) >= 256 && K >= 1152) {
+      g.col_tiles = (N + 255) / 256;
+      quant::big_kernel<TO><<<(unsigned)tiles(256), 256, 0, s>>>(g);
+      return hipGetLastError();
+    }
     if (tiles(128) >= 256) return quant::launch_tiles<TO, 128, 128, 64, 64>(g, s);
     return quant::launch_tiles<TO, 64, 64, 32, 32>(g, s);
   });
