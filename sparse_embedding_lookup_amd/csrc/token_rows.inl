@@ -1,5 +1,5 @@
 // token_rows.inl -- rows of a table by token, scaled, and the gradient of the whole table by
-// sorted tokens.  Part of the translation unit of unique.hip, whose radix sort it uses.
+// sorted tokens.  Part of the translation unit of unique.hip, some of whose device code it uses.
 //
 //   Y[i, :]  = scale * table[ids[i], :]                        (ids[i] < 0: zeros)
 //   dT[v, :] = scale * sum over i with ids[i] == v of dY[i, :]  (fp32, rows of no token zero)
@@ -57,10 +57,11 @@ __device__ __forceinline__ uint32_t key_of(const void* ids, int64_t i, int64_t V
   return (uint32_t)(id >= 0 && id < V ? id : V);
 }
 
-// `count` floats from p on cleared by the blocks from `first` on.
-__device__ __forceinline__ void clear(float* p, int64_t count, int first) {
-  const int64_t t = (int64_t)(blockIdx.x - first) * kThreads + threadIdx.x;
-  const int64_t step = (int64_t)(gridDim.x - first) * kThreads;
+// Floats [begin, end) of p cleared by the blocks from `first` on.
+__device__ __forceinline__ void clear(float* p, int64_t begin, int64_t end, int first) {
+  p += begin;
+  const int64_t count = end - begin, t = (int64_t)(blockIdx.x - first) * blockDim.x + threadIdx.x;
+  const int64_t step = (int64_t)(gridDim.x - first) * blockDim.x;
   const int64_t head = (4 - (reinterpret_cast<uintptr_t>(p) >> 2 & 3)) & 3;   // to 16 bytes
   const int64_t h = head < count ? head : count, whole = (count - h) / 4;
   float4* q = reinterpret_cast<float4*>(p + h);
@@ -69,19 +70,174 @@ __device__ __forceinline__ void clear(float* p, int64_t count, int first) {
   if (t < count - h - 4 * whole) p[h + 4 * whole + t] = 0.f;
 }
 
-// The keys in token order, and the table's gradient cleared.
-template <bool ID64>
-__global__ __launch_bounds__(kThreads) void keys_kernel(const void* __restrict__ ids, int64_t n,
-                                                        int64_t V, int key_blocks,
-                                                        uint32_t* __restrict__ keys,
-                                                        float* __restrict__ dT, int64_t count) {
-  if ((int)blockIdx.x >= key_blocks) {
-    clear(dT, count, key_blocks);
+// Many tokens: a stable radix sort by digits of up to kDigit bits, from the lowest.  A tile is
+// kSortThreads * ITEMS tokens; a pass counts the tiles' digits, scans every digit's counts over the
+// tiles (by themselves in the third launch where tiles are few) and moves the tokens.  All of it
+// waits more than it moves, so every launch has blocks beside that clear a share of the gradient.
+// (65536 tokens of 100003 rows, 128 wide: with the table-wide clearing first and digits of 6 bits
+// in tiles of 1024 44 us up to the sums, and here 27; 2^20 tokens of 10^6 rows 154 and 104 us, of
+// which the clearing alone is 82.)
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kDigit = 10;
+constexpr int kBins = 1 << kDigit, kFewTiles = 64;
+struct Sort {
+  const void* ids;              // the first pass reads the tokens themselves
+  int64_t V;
+  const uint32_t* keys_in;
+  const uint32_t* vals_in;
+  uint32_t* keys_out;
+  uint32_t* vals_out;
+  int64_t n;
+  int shift, bits, tiles, ld;
+  uint32_t* counts;             // [bins, ld]
+  uint32_t* totals;             // [bins]
+  float* dT;
+  int64_t clear_from, clear_to;
+};
+// 0: later passes; 1 and 2: the first, of 32- and 64-bit tokens.
+template <int FIRST>
+__device__ __forceinline__ uint32_t sort_key(const Sort& g, int64_t i) {
+  if constexpr (FIRST) return key_of<FIRST == 2>(g.ids, i, g.V);
+  else return g.keys_in[i];
+}
+
+template <int FIRST, int ITEMS>
+__global__ __launch_bounds__(kSortThreads) void count_kernel(Sort g) {
+  if ((int)blockIdx.x >= g.tiles) {
+    clear(g.dT, g.clear_from, g.clear_to, g.tiles);
     return;
   }
-  const int64_t step = (int64_t)key_blocks * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step)
-    keys[i] = key_of<ID64>(ids, i, V);
+  __shared__ uint32_t bins[kBins];
+  const uint32_t mask = (1u << g.bits) - 1u;
+  bins[threadIdx.x] = 0u;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kSortThreads * ITEMS;
+  uint32_t key[ITEMS];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int64_t i = base + k * kSortThreads + threadIdx.x;
+    key[k] = i < g.n ? sort_key<FIRST>(g, i) : 0u;
+  }
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k)
+    count_digit(bins, key[k] >> g.shift & mask,
+                base + k * kSortThreads + threadIdx.x < g.n);
+  __syncthreads();
+  if (threadIdx.x <= mask) g.counts[(int64_t)threadIdx.x * g.ld + blockIdx.x] = bins[threadIdx.x];
+}
+
+// A wave a digit: its counts become the tokens of it in the tiles before each.
+__global__ __launch_bounds__(kSortThreads) void scan_kernel(Sort g) {
+  const int blocks = ((1 << g.bits) + kSortWaves - 1) / kSortWaves;
+  if ((int)blockIdx.x >= blocks) {
+    clear(g.dT, g.clear_from, g.clear_to, blocks);
+    return;
+  }
+  const int lane = threadIdx.x & 63, d = (int)blockIdx.x * kSortWaves + (threadIdx.x >> 6);
+  if (d >= 1 << g.bits) return;
+  uint32_t run = 0u;
+  uint32_t* row = g.counts + (int64_t)d * g.ld;
+  for (int i0 = 0; i0 < g.tiles; i0 += 64) {
+    const int i = i0 + lane;
+    const uint32_t c = i < g.tiles ? row[i] : 0u;
+    uint32_t s = c;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const uint32_t v = __shfl_up(s, o);
+      if (lane >= o) s += v;
+    }
+    if (i < g.tiles) row[i] = run + s - c;
+    run += __shfl(s, 63);
+  }
+  if (lane == 0) g.totals[d] = run;
+}
+
+template <int FIRST, int ITEMS>
+__global__ __launch_bounds__(kSortThreads) void move_kernel(Sort g) {
+  if ((int)blockIdx.x >= g.tiles) {
+    clear(g.dT, g.clear_from, g.clear_to, g.tiles);
+    return;
+  }
+  __shared__ uint32_t waves[kSortWaves][kBins];   // tokens of a digit in a wave, then before it
+  __shared__ uint32_t start[kBins], sums[kSortWaves];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, me = (int)blockIdx.x;
+  const int bins = 1 << g.bits;
+  const uint32_t mask = (uint32_t)bins - 1u;
+  // a wave has ITEMS * 64 neighbouring tokens, in their order
+  const int64_t base = (int64_t)me * kSortThreads * ITEMS + w * 64 * ITEMS;
+  uint32_t key[ITEMS], val[ITEMS];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int64_t i = base + k * 64 + lane;
+    key[k] = i < g.n ? sort_key<FIRST>(g, i) : 0u;
+    val[k] = FIRST ? (uint32_t)i : i < g.n ? g.vals_in[i] : 0u;
+  }
+  // digit t: its tokens in all tiles, and in the tiles before this one
+  uint32_t total = 0u, before = 0u;
+  if (t < bins) {
+    if (g.tiles <= kFewTiles) {
+      const uint4* row = reinterpret_cast<const uint4*>(g.counts + (int64_t)t * g.ld);
+#pragma unroll 4
+      for (int q = 0; q < g.ld / 4; ++q) {
+        const uint4 v = row[q];
+        const uint32_t c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = 4 * q + j < g.tiles ? c[j] : 0u;
+          total += x;
+          before += 4 * q + j < me ? x : 0u;
+        }
+      }
+    } else {
+      total = g.totals[t];
+      before = g.counts[(int64_t)t * g.ld + me];
+    }
+  }
+  for (int i = t; i < kSortWaves * bins; i += kSortThreads) waves[i >> g.bits][i & mask] = 0u;
+  uint32_t upto = total;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t v = __shfl_up(upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 63) sums[w] = upto;
+  __syncthreads();
+  for (int u = 0; u < w; ++u) upto += sums[u];
+  start[t] = upto - total + before;
+  // a token's place among those of its digit in the wave: by the lanes that share it
+  uint64_t same[ITEMS];
+  uint32_t first[ITEMS];
+  const uint64_t lower = lanemask_lt();
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const bool live = base + k * 64 + lane < g.n;
+    const uint32_t d = key[k] >> g.shift & mask;
+    same[k] = match_digit(d, g.bits, __ballot(live));
+    first[k] = 0u;
+    if (live && (same[k] & lower) == 0ull)
+      first[k] = atomicAdd(&waves[w][d], (uint32_t)__popcll(same[k]));
+  }
+  __syncthreads();
+  if (t < bins) {
+    uint32_t run = start[t];
+#pragma unroll
+    for (int u = 0; u < kSortWaves; ++u) {
+      const uint32_t c = waves[u][t];
+      waves[u][t] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int leader = same[k] ? (int)__builtin_ctzll(same[k]) : 0;
+    const uint32_t rank = (uint32_t)__shfl((int)first[k], leader) +
+                          (uint32_t)__popcll(same[k] & lower);
+    if (base + k * 64 + lane < g.n) {
+      const uint32_t at = waves[w][key[k] >> g.shift & mask] + rank;
+      g.keys_out[at] = key[k];
+      g.vals_out[at] = val[k];
+    }
+  }
 }
 
 // Few tokens: sorted in this launch.  A token's place is the number of tokens before it in
@@ -95,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void rank_kernel(const void* __restrict__
                                                         uint32_t* __restrict__ sv,
                                                         float* __restrict__ dT, int64_t count) {
   if ((int)blockIdx.x >= key_blocks) {
-    clear(dT, count, key_blocks);
+    clear(dT, 0, count, key_blocks);
     return;
   }
   __shared__ uint32_t tile[kRankTile];
@@ -322,13 +478,19 @@ int chunk_of(int64_t n, int G) {
 struct Workspace {
   uint32_t* keys[2];
   uint32_t* vals[2];
-  uint32_t* hist;
+  uint32_t* counts;
   uint32_t* totals;
   float* part;
   uint32_t* part_key;
   int64_t blocks;
   size_t bytes;
 };
+// Tokens a thread in a sort's tile: one as long as the tiles stay few.
+int sort_items(int64_t n) { return n <= (int64_t)kFewTiles * kSortThreads ? 1 : 4; }
+int64_t sort_tiles(int64_t n) {
+  const int64_t tile = (int64_t)kSortThreads * sort_items(n);
+  return (n + tile - 1) / tile;
+}
 Workspace carve_tokens(void* base, int64_t n, int D, int E) {
   Workspace w{};
   size_t off = 0;
@@ -339,8 +501,9 @@ Workspace carve_tokens(void* base, int64_t n, int D, int E) {
   };
   for (int i = 0; i < 2; ++i) w.keys[i] = reinterpret_cast<uint32_t*>(take(4 * (size_t)n));
   for (int i = 0; i < 2; ++i) w.vals[i] = reinterpret_cast<uint32_t*>(take(4 * (size_t)n));
-  w.hist = reinterpret_cast<uint32_t*>(take(4 * (size_t)kBuckets * kMaxBlocks));
-  w.totals = reinterpret_cast<uint32_t*>(take(4 * (size_t)kBuckets));
+  const size_t ld = n > kRankMost ? (size_t)(sort_tiles(n) + 3) / 4 * 4 : 0;
+  w.counts = reinterpret_cast<uint32_t*>(take(4 * kBins * ld));
+  w.totals = reinterpret_cast<uint32_t*>(take(4 * (size_t)kBins));
   const int G = lanes(D, E);
   const int64_t each = (int64_t)(kThreads / G) * chunk_of(n, G);
   w.blocks = (n + each - 1) / each;
@@ -402,22 +565,58 @@ hipError_t launch_token_embed_bwd(const void* dY, int dtype, int64_t dys, const 
       tokens::rank_kernel<false><<<(unsigned)(kb + clear), tokens::kThreads, 0, s>>>(
           ids, (int)n, V, kb, w.keys[0], w.vals[0], dT, count);
   } else {
-    int64_t kb = (n + 4 * tokens::kThreads - 1) / (4 * tokens::kThreads);
-    if (kb > 2048) kb = 2048;
-    if (ids64)
-      tokens::keys_kernel<true><<<(unsigned)(kb + clear), tokens::kThreads, 0, s>>>(
-          ids, n, V, (int)kb, w.keys[0], dT, count);
-    else
-      tokens::keys_kernel<false><<<(unsigned)(kb + clear), tokens::kThreads, 0, s>>>(
-          ids, n, V, (int)kb, w.keys[0], dT, count);
-    const uint16_t* none;
-    const int bits = tokens::key_bits(V);
-    if (n <= (1 << 20))
-      radix_sort<uint32_t, 4>(bits, w.keys[0], w.keys[1], w.vals[0], w.vals[1], nullptr, nullptr,
-                              n, w.hist, w.totals, &sk, &sv, &none, nullptr, s);
-    else
-      radix_sort<uint32_t, 8>(bits, w.keys[0], w.keys[1], w.vals[0], w.vals[1], nullptr, nullptr,
-                              n, w.hist, w.totals, &sk, &sv, &none, nullptr, s);
+    tokens::Sort q{};
+    q.ids = ids; q.V = V; q.n = n; q.dT = dT; q.counts = w.counts; q.totals = w.totals;
+    const int items = tokens::sort_items(n), bits = tokens::key_bits(V);
+    const int passes = (bits + tokens::kDigit - 1) / tokens::kDigit;
+    q.tiles = (int)tokens::sort_tiles(n);
+    q.ld = (q.tiles + 3) / 4 * 4;
+    const bool scan = q.tiles > tokens::kFewTiles;
+    const int launches = passes * (scan ? 3 : 2);
+    int launched = 0;
+    // the grid of a launch with `own` blocks of its own, and its share of the clearing
+    auto grid = [&](int own) {
+      q.clear_from = count / launches * launched;
+      q.clear_to = ++launched == launches ? count : count / launches * launched;
+      const int64_t share = q.clear_to - q.clear_from, each = 16 * tokens::kSortThreads;
+      const int64_t blocks = (share + each - 1) / each;
+      return (unsigned)(own + (blocks < 4096 ? blocks : 4096));
+    };
+    for (int p = 0; p < passes; ++p) {
+      q.bits = (bits - q.shift) / (passes - p);            // spread evenly
+      q.keys_out = w.keys[p & 1];
+      q.vals_out = w.vals[p & 1];
+      auto by_items = [&](auto kernel) {
+        return items == 1 ? kernel(std::integral_constant<int, 1>{})
+                          : kernel(std::integral_constant<int, 4>{});
+      };
+      auto by_pass = [&](auto kernel) {
+        if (p > 0) kernel(std::integral_constant<int, 0>{});
+        else if (ids64) kernel(std::integral_constant<int, 2>{});
+        else kernel(std::integral_constant<int, 1>{});
+      };
+      unsigned blocks = grid(q.tiles);
+      by_pass([&](auto f) {
+        by_items([&](auto k) {
+          tokens::count_kernel<decltype(f)::value, decltype(k)::value>
+              <<<blocks, tokens::kSortThreads, 0, s>>>(q);
+        });
+      });
+      if (scan) {
+        blocks = grid(((1 << q.bits) + tokens::kSortWaves - 1) / tokens::kSortWaves);
+        tokens::scan_kernel<<<blocks, tokens::kSortThreads, 0, s>>>(q);
+      }
+      blocks = grid(q.tiles);
+      by_pass([&](auto f) {
+        by_items([&](auto k) {
+          tokens::move_kernel<decltype(f)::value, decltype(k)::value>
+              <<<blocks, tokens::kSortThreads, 0, s>>>(q);
+        });
+      });
+      q.shift += q.bits;
+      sk = q.keys_in = q.keys_out;
+      sv = q.vals_in = q.vals_out;
+    }
   }
   if (n == 0) return hipGetLastError();
   tokens::Sums g{};

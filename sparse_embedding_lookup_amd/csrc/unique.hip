@@ -913,6 +913,6 @@ hipError_t launch_unique(const void* ids, bool ids64, int64_t n, const int64_t* 
 
 }  // namespace ctr
 
-// The rows by token belong to this translation unit for its radix sort.
+// The rows by token belong to this translation unit for its ranking of digits.
 #include "run_io.h"
 #include "token_rows.inl"

@@ -1109,11 +1109,40 @@ ACTS = {"none": CTR_ACT_NONE, "relu": CTR_ACT_RELU, "silu": CTR_ACT_SILU, "gelu"
 
 def _launch_here(name: str, device: torch.device, args: tuple, prepare: bool, result=None,
                  keep=None):
-    """_launch of arguments that are all on the current device, whose current stream it takes."""
-    if device.type == "cuda" and device.index != torch._C._cuda_getDevice():
-        raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
-                         % (name, device, torch._C._cuda_getDevice()))
+    """_launch of arguments that are all on the current device, whose current stream it takes.
+    (Written out for the immediate call: these operators' smallest calls are host time.)"""
+    index = device.index
+    if device.type == "cuda":
+        if index != torch._C._cuda_getDevice():
+            raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
+                             % (name, device, torch._C._cuda_getDevice()))
+        if not prepare:
+            st = getattr(_lib or load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+            if st != CTR_OK:
+                _check(name, st)
+            return result
     return _launch(name, device, args, prepare, result, keep)
+
+
+def _rows_in(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype,
+             device: torch.device) -> tuple:
+    """_rows_arg, by the short way where nothing is wrong."""
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        stride, inner = t.stride()
+        rows, width = shape
+        if (inner == 1 or width == 1) and (stride >= width or rows <= 1):
+            return t.data_ptr(), stride if stride > width else width
+    return _rows_arg(t, name, shape, dtype, device)
+
+
+def _rows_out(out: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype,
+              device: torch.device) -> tuple:
+    """An output in rows: (tensor, address, row stride), checked, or made if it is None."""
+    if out is None:
+        width = shape[1]
+        out = torch.empty_strided(shape, (width, 1), dtype=dtype, device=device)
+        return out, out.data_ptr(), width
+    return (out,) + _rows_in(out, name, shape, dtype, device)
 
 
 def _queried(name: str, args: tuple) -> int:
@@ -1179,7 +1208,7 @@ def ctr_token_embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float = 1
     out_dtype = out_dtype or (table.dtype if Y is None else Y.dtype)
     if out_dtype not in _DTYPE_CODES:
         raise TypeError("Y must be float32, bfloat16 or float16, not %s" % out_dtype)
-    Y, yp, ys = _matrix(Y, "Y", n, D, out_dtype, dev)
+    Y, yp, ys = _rows_out(Y, "Y", (n, D), out_dtype, dev)
     args = (tp, code, V, D, ip, itype, n, float(scale), yp, _DTYPE_CODES[out_dtype], ys)
     return _launch_here("ctr_token_embed_fwd", dev, args, prepare, Y)
 
@@ -1196,7 +1225,7 @@ def ctr_token_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, num_rows: int, scal
     code, dev = _expert_type(dY, "dY"), dY.device
     ip, itype, n = _token_ids(ids, dev)
     D = dY.shape[-1]
-    yp, dys = _rows_arg(dY, "dY", (n, D), dY.dtype, dev)
+    yp, dys = _rows_in(dY, "dY", (n, D), dY.dtype, dev)
     dtable, tp = _dense(dtable, "dtable", (num_rows, D), (D, 1), torch.float32, dev)
     if workspace is None:
         workspace = _workspace(token_embed_bwd_workspace_bytes(n, num_rows, D, code), dev)
@@ -1208,7 +1237,7 @@ def ctr_token_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, num_rows: int, scal
 
 def _codes_out(out: Optional[torch.Tensor], name: str, rows: int, width: int, dev) -> tuple:
     """An output of 8-bit rows: (tensor [rows, width to a multiple of 16], address, row stride)."""
-    return _matrix(out, name, rows, (width + 15) // 16 * 16, F8, dev)
+    return _rows_out(out, name, (rows, (width + 15) // 16 * 16), F8, dev)
 
 
 def ctr_rms_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor],
@@ -1229,8 +1258,8 @@ def ctr_rms_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor],
     n, D = X.shape
     rp, rs, sp, ss = None, D, None, D
     if residual is not None:
-        rp, rs = _rows_arg(residual, "residual", (n, D), X.dtype, dev)
-        S, sp, ss = _matrix(S, "S", n, D, X.dtype, dev)
+        rp, rs = _rows_in(residual, "residual", (n, D), X.dtype, dev)
+        S, sp, ss = _rows_out(S, "S", (n, D), X.dtype, dev)
     elif S is not None:
         raise ValueError("S needs a residual")
     wp = None if weight is None else _expert_arg(weight, "weight", (D,), torch.float32, dev)
@@ -1244,7 +1273,7 @@ def ctr_rms_norm_fwd(X: torch.Tensor, weight: Optional[torch.Tensor],
     else:
         if y_scale is not None:
             raise ValueError("y_scale needs quantize")
-        Y, yp, ys = _matrix(Y, "Y", n, D, X.dtype, dev)
+        Y, yp, ys = _rows_out(Y, "Y", (n, D), X.dtype, dev)
     args = (X.data_ptr(), code, xs, n, D, rp, rs, wp, float(eps), sp, ss, yp, ycode, ys, cp, qp)
     return _launch_here("ctr_rms_norm_fwd", dev, args, prepare,
                         (Y, y_scale, S if residual is not None else X, rstd))
@@ -1264,9 +1293,9 @@ def ctr_rms_norm_bwd(dY: torch.Tensor, S: torch.Tensor, rstd: torch.Tensor,
                    workspace, prepare=prepare)
     code, ys, dev = _expert_type(dY, "dY"), _row_stride(dY, "dY"), dY.device
     n, D = dY.shape
-    sp, ss = _rows_arg(S, "S", (n, D), dY.dtype, dev)
-    gp, gs = (None, D) if dS is None else _rows_arg(dS, "dS", (n, D), dY.dtype, dev)
-    dX, xp, xs = _matrix(dX, "dX", n, D, dY.dtype, dev)
+    sp, ss = _rows_in(S, "S", (n, D), dY.dtype, dev)
+    gp, gs = (None, D) if dS is None else _rows_in(dS, "dS", (n, D), dY.dtype, dev)
+    dX, xp, xs = _rows_out(dX, "dX", (n, D), dY.dtype, dev)
     wp = None if weight is None else _expert_arg(weight, "weight", (D,), torch.float32, dev)
     dwp = None
     if want_dw:
@@ -1314,15 +1343,15 @@ def ctr_quant_dense_fwd(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor,
         raise ValueError("X must be [M, K] and W [N, K]")
     M, K = X.shape
     N = W.shape[0]
-    xp, xs = _rows_arg(X, "X", (M, K), F8, dev)
-    wp, ws = _rows_arg(W, "W", (N, K), F8, dev)
+    xp, xs = _rows_in(X, "X", (M, K), F8, dev)
+    wp, ws = _rows_in(W, "W", (N, K), F8, dev)
     given = Y if Y is not None else residual
     out_dtype = out_dtype or (torch.bfloat16 if given is None else given.dtype)
     if out_dtype not in _DTYPE_CODES:
         raise TypeError("Y must be float32, bfloat16 or float16, not %s" % out_dtype)
-    rp, rs = (None, N) if residual is None else _rows_arg(residual, "residual", (M, N), out_dtype,
+    rp, rs = (None, N) if residual is None else _rows_in(residual, "residual", (M, N), out_dtype,
                                                           dev)
-    Y, yp, ys = _matrix(Y, "Y", M, N, out_dtype, dev)
+    Y, yp, ys = _rows_out(Y, "Y", (M, N), out_dtype, dev)
     bp = None if b is None else _expert_arg(b, "b", (N,), torch.float32, dev)
     args = (xp, xs, M, K, _expert_arg(x_scale, "x_scale", (M,), torch.float32, dev), wp, ws,
             _expert_arg(w_scale, "w_scale", (N,), torch.float32, dev), N, bp, ACTS[act], rp, rs,
@@ -1337,12 +1366,17 @@ def ctr_gated_scan_chunks(n: int) -> int:
 
 def _scan_args(gate, value, out_gate):
     """The rows of a scan: (their first arguments, n, D, type)."""
-    code, gs, dev = _expert_type(gate, "gate"), _row_stride(gate, "gate"), gate.device
-    n, D = gate.shape
-    vp, vs = _rows_arg(value, "value", (n, D), gate.dtype, dev)
-    op, os_ = (None, D) if out_gate is None else _rows_arg(out_gate, "out_gate", (n, D),
-                                                           gate.dtype, dev)
-    return (gate.data_ptr(), gs, vp, vs, op, os_, code), n, D, dev
+    dtype, dev, shape = gate.dtype, gate.device, gate.shape
+    code = _DTYPE_CODES.get(dtype)
+    if code is None or len(shape) != 2:
+        code = _expert_type(gate, "gate")
+        raise ValueError("gate must be 2-D")
+    gp, gs = _rows_in(gate, "gate", shape, dtype, dev)
+    vp, vs = _rows_in(value, "value", shape, dtype, dev)
+    op, os_ = None, shape[1]
+    if out_gate is not None:
+        op, os_ = _rows_in(out_gate, "out_gate", shape, dtype, dev)
+    return (gp, gs, vp, vs, op, os_, code), shape[0], shape[1], dev
 
 
 def _sequence_args(offsets, dev):
@@ -1372,7 +1406,7 @@ def ctr_gated_scan_fwd(gate: torch.Tensor, value: torch.Tensor, offsets: torch.T
                    want_last, Y, hN, states, workspace, prepare=prepare)
     first, n, D, dev = _scan_args(gate, value, out_gate)
     fp, B = _sequence_args(offsets, dev)
-    Y, yp, ys = _matrix(Y, "Y", n, D, gate.dtype, dev)
+    Y, yp, ys = _rows_out(Y, "Y", (n, D), gate.dtype, dev)
     np_, sp = None, None
     if want_last or hN is not None:
         hN, np_ = _dense(hN, "hN", (B, D), (D, 1), torch.float32, dev)
@@ -1405,12 +1439,12 @@ def ctr_gated_scan_bwd(gate: torch.Tensor, value: torch.Tensor, offsets: torch.T
                    want_dh0, dgate, dvalue, dout_gate, dh0, workspace, prepare=prepare)
     first, n, D, dev = _scan_args(gate, value, out_gate)
     fp, B = _sequence_args(offsets, dev)
-    yp, dys = _rows_arg(dY, "dY", (n, D), gate.dtype, dev)
-    dgate, gp, gs = _matrix(dgate, "dgate", n, D, gate.dtype, dev)
-    dvalue, vp, vs = _matrix(dvalue, "dvalue", n, D, gate.dtype, dev)
+    yp, dys = _rows_in(dY, "dY", (n, D), gate.dtype, dev)
+    dgate, gp, gs = _rows_out(dgate, "dgate", (n, D), gate.dtype, dev)
+    dvalue, vp, vs = _rows_out(dvalue, "dvalue", (n, D), gate.dtype, dev)
     op, os_, hp = None, D, None
     if out_gate is not None:
-        dout_gate, op, os_ = _matrix(dout_gate, "dout_gate", n, D, gate.dtype, dev)
+        dout_gate, op, os_ = _rows_out(dout_gate, "dout_gate", (n, D), gate.dtype, dev)
     elif dout_gate is not None:
         raise ValueError("dout_gate needs an out_gate")
     if want_dh0 or dh0 is not None:
@@ -1450,7 +1484,7 @@ def ctr_gated_scan_step(gate: torch.Tensor, value: torch.Tensor, state: torch.Te
             raise ValueError("a new state needs a row for every slot")
         to, tp = _dense(None if new_state is True else new_state, "new_state", (slots, D), (D, 1),
                         torch.float32, dev)
-    Y, yp, ys = _matrix(Y, "Y", B, D, gate.dtype, dev)
+    Y, yp, ys = _rows_out(Y, "Y", (B, D), gate.dtype, dev)
     args = first + (B, D, ip, slots, sp, tp, yp, ys)
     return _launch_here("ctr_gated_scan_step", dev, args, prepare, (Y, to))
 
