@@ -1,0 +1,262 @@
+"""Refusals of the click-history operators on the host alone (every call below fails its checks
+before any HIP call, or is a workspace query, so the addresses are never used), and the definitions
+that the GPU tests compare with, against differences."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from sparse_embedding_lookup_amd import ctr
+from tests import history_ref as ref
+
+A = ctypes.c_void_p(0x10000)
+ODD = ctypes.c_void_p(0x10001)
+EIGHT = ctypes.c_void_p(0x10008)
+BAD, UNS, SMALL = ctr.CTR_ERR_INVALID_ARGUMENT, ctr.CTR_ERR_UNSUPPORTED, \
+    ctr.CTR_ERR_WORKSPACE_TOO_SMALL
+F32, BF16, F16, F8 = 0, 1, 2, 3
+
+
+def lib():
+    if not os.path.exists(ctr.LIB_PATH):
+        from sparse_embedding_lookup_amd import build
+        build.build()
+    return ctr.load()
+
+
+def check(call, ok, cases):
+    for want, change in cases:
+        assert set(change) <= set(ok)
+        assert call(**dict(ok, **change)) == want, change
+        assert lib().ctr_last_error_message() != b"", change
+
+
+def size(a):
+    return None if a["wsb"] is None else ctypes.byref(ctypes.c_size_t(a["wsb"]))
+
+
+WORKSPACES = [(BAD, dict(wsb=None)), (SMALL, dict(wsb=1)), (UNS, dict(ws=EIGHT))]
+
+
+def test_token_refusals():
+    ok = dict(t=A, dt=BF16, V=100, D=64, ids=A, it=1, n=5, y=A, od=BF16, ys=64, ws=A, wsb=1 << 30)
+
+    def fwd(**a):
+        return lib().ctr_token_embed_fwd(a["t"], a["dt"], a["V"], a["D"], a["ids"], a["it"], a["n"],
+                                         2.0, a["y"], a["od"], a["ys"], None)
+
+    def bwd(**a):
+        return lib().ctr_token_embed_bwd(a["y"], a["dt"], a["ys"], a["ids"], a["it"], a["n"],
+                                         a["V"], a["D"], 2.0, a["t"], a["ws"], size(a), None)
+    both = [(BAD, dict(dt=3)), (BAD, dict(dt=-1)), (BAD, dict(V=0)), (BAD, dict(V=(1 << 31) - 1)),
+            (BAD, dict(D=0)), (BAD, dict(D=65537, ys=1 << 17)), (BAD, dict(it=2)),
+            (BAD, dict(n=-1)), (UNS, dict(n=(1 << 25) + 1)), (BAD, dict(t=None)),
+            (BAD, dict(ids=None)), (BAD, dict(y=None)), (BAD, dict(ys=63)), (UNS, dict(t=ODD)),
+            (UNS, dict(y=ODD)), (UNS, dict(ids=ctypes.c_void_p(0x10004)))]
+    check(fwd, ok, both + [(BAD, dict(od=3)), (UNS, dict(ids=ODD, it=0))])
+    check(bwd, ok, both + WORKSPACES + [(BAD, dict(n=0, t=None))])
+    assert ctr.token_embed_bwd_workspace_bytes(0, 1, 1, F32) >= 0
+    # keys and places twice, counts and sums: a small multiple of the tokens
+    assert ctr.token_embed_bwd_workspace_bytes(1 << 20, 1 << 20, 128, BF16) < 40 << 20
+
+
+def test_norm_refusals():
+    ok = dict(x=A, dt=BF16, xs=64, n=5, D=64, r=A, rs=64, w=A, eps=1e-6, s=A, ss=64, y=A, yt=BF16,
+              ys=64, sc=A, q=A, ds=A, dss=64, dx=A, dxs=64, dw=A, ws=A, wsb=1 << 30)
+
+    def fwd(**a):
+        return lib().ctr_rms_norm_fwd(a["x"], a["dt"], a["xs"], a["n"], a["D"], a["r"], a["rs"],
+                                      a["w"], a["eps"], a["s"], a["ss"], a["y"], a["yt"], a["ys"],
+                                      a["sc"], a["q"], None)
+
+    def bwd(**a):
+        return lib().ctr_rms_norm_bwd(a["x"], a["dt"], a["xs"], a["n"], a["D"], a["s"], a["ss"],
+                                      a["q"], a["w"], a["ds"], a["dss"], a["dx"], a["dxs"], a["dw"],
+                                      a["ws"], size(a), None)
+
+    def rows(**a):
+        return lib().ctr_quantize_rows(a["x"], a["dt"], a["xs"], a["n"], a["D"], a["y"], a["ys"],
+                                       a["sc"], None)
+    all_ = [(BAD, dict(dt=3)), (BAD, dict(xs=63)), (BAD, dict(n=-1)), (BAD, dict(n=1 << 31)),
+            (BAD, dict(D=0)), (UNS, dict(D=8193)), (BAD, dict(x=None)), (UNS, dict(x=ODD))]
+    codes = [(BAD, dict(yt=F8, ys=63)), (BAD, dict(yt=F8, D=50, ys=63)), (UNS, dict(yt=F8, y=EIGHT)),
+             (UNS, dict(yt=F8, ys=72)), (BAD, dict(yt=F8, sc=None)), (UNS, dict(yt=F8, sc=ODD))]
+    check(fwd, ok, all_ + codes + [
+        (BAD, dict(yt=F32)), (BAD, dict(yt=4)), (BAD, dict(rs=63)), (BAD, dict(ss=63)),
+        (BAD, dict(ys=63)), (BAD, dict(s=None)), (BAD, dict(y=None)), (UNS, dict(r=ODD)),
+        (UNS, dict(s=ODD)), (UNS, dict(y=ODD)), (UNS, dict(w=ODD)), (UNS, dict(q=ODD)),
+        (BAD, dict(eps=-1.0)), (BAD, dict(eps=float("nan")))])
+    check(bwd, ok, all_ + WORKSPACES + [
+        (BAD, dict(s=None)), (BAD, dict(q=None)), (BAD, dict(dx=None)), (BAD, dict(ss=63)),
+        (BAD, dict(dxs=63)), (BAD, dict(dss=63)), (UNS, dict(s=ODD)), (UNS, dict(ds=ODD)),
+        (UNS, dict(dx=ODD)), (UNS, dict(dw=ODD)), (UNS, dict(q=ODD)), (UNS, dict(w=ODD))])
+    check(rows, ok, all_ + [(BAD, dict(y=None)), (BAD, dict(sc=None)), (BAD, dict(ys=63)),
+                            (UNS, dict(ys=72)), (UNS, dict(y=EIGHT)), (UNS, dict(sc=ODD))])
+
+
+def test_dense_refusals():
+    ok = dict(x=A, xs=64, M=5, K=64, xc=A, w=A, ws=64, wc=A, N=32, b=A, act=1, r=A, rs=32, dt=BF16,
+              y=A, ys=32)
+
+    def call(**a):
+        return lib().ctr_quant_dense_fwd(a["x"], a["xs"], a["M"], a["K"], a["xc"], a["w"], a["ws"],
+                                         a["wc"], a["N"], a["b"], a["act"], a["r"], a["rs"],
+                                         a["dt"], a["y"], a["ys"], None)
+    check(call, ok, [
+        (BAD, dict(dt=3)), (BAD, dict(M=-1)), (BAD, dict(M=1 << 31)), (BAD, dict(K=0)),
+        (UNS, dict(K=40)), (BAD, dict(K=65552, xs=1 << 17, ws=1 << 17)), (BAD, dict(N=0)),
+        (BAD, dict(N=65537, ys=1 << 17, rs=1 << 17)), (BAD, dict(act=4)), (BAD, dict(act=-1)),
+        (BAD, dict(xs=48)), (BAD, dict(ws=48)), (UNS, dict(xs=72)), (UNS, dict(ws=72)),
+        (UNS, dict(x=EIGHT)), (UNS, dict(w=EIGHT)), (UNS, dict(xs=1 << 22)),
+        (UNS, dict(ws=1 << 22)), (BAD, dict(ys=31)), (BAD, dict(rs=31)), (BAD, dict(x=None)),
+        (BAD, dict(xc=None)), (BAD, dict(w=None)), (BAD, dict(wc=None)), (BAD, dict(y=None)),
+        (UNS, dict(y=ODD)), (UNS, dict(r=ODD)), (UNS, dict(xc=ODD)), (UNS, dict(wc=ODD)),
+        (UNS, dict(b=ODD)), (UNS, dict(M=(1 << 31) - 1, N=1024, ys=1024, rs=1024))])
+
+
+def test_scan_refusals():
+    ok = dict(g=A, gs=64, v=A, vs=64, o=A, os=64, dt=BF16, off=A, n=50, B=3, D=64, h0=A, y=A, ys=64,
+              hN=A, st=A, dy=A, dys=64, dN=A, dg=A, dgs=64, dv=A, dvs=64, do=A, dos=64, d0=A,
+              ix=A, sl=9, ws=A, wsb=1 << 30)
+
+    def fwd(**a):
+        return lib().ctr_gated_scan_fwd(a["g"], a["gs"], a["v"], a["vs"], a["o"], a["os"], a["dt"],
+                                        a["off"], a["n"], a["B"], a["D"], a["h0"], a["y"], a["ys"],
+                                        a["hN"], a["st"], a["ws"], size(a), None)
+
+    def bwd(**a):
+        return lib().ctr_gated_scan_bwd(
+            a["g"], a["gs"], a["v"], a["vs"], a["o"], a["os"], a["dt"], a["off"], a["n"], a["B"],
+            a["D"], a["h0"], a["st"], a["dy"], a["dys"], a["dN"], a["dg"], a["dgs"], a["dv"],
+            a["dvs"], a["do"], a["dos"], a["d0"], a["ws"], size(a), None)
+
+    def step(**a):
+        return lib().ctr_gated_scan_step(a["g"], a["gs"], a["v"], a["vs"], a["o"], a["os"], a["dt"],
+                                         a["n"], a["D"], a["ix"], a["sl"], a["h0"], a["hN"], a["y"],
+                                         a["ys"], None)
+    all_ = [(BAD, dict(dt=3)), (BAD, dict(n=-1)), (BAD, dict(D=0)), (BAD, dict(gs=63)),
+            (BAD, dict(vs=63)), (BAD, dict(os=63)), (BAD, dict(g=None)), (BAD, dict(v=None)),
+            (UNS, dict(g=ODD)), (UNS, dict(v=ODD)), (UNS, dict(o=ODD)), (UNS, dict(h0=ODD))]
+    both = all_ + WORKSPACES + [
+        (UNS, dict(n=(1 << 29) + 1)), (BAD, dict(B=-1)), (BAD, dict(B=1 << 31)),
+        (BAD, dict(off=None)), (UNS, dict(off=ctypes.c_void_p(0x10004))), (UNS, dict(st=ODD)),
+        (BAD, dict(D=65537, gs=1 << 17))]
+    check(fwd, ok, both + [(BAD, dict(y=None)), (BAD, dict(ys=63)), (UNS, dict(y=ODD)),
+                           (UNS, dict(hN=ODD))])
+    check(bwd, ok, both + [
+        (BAD, dict(st=None)), (BAD, dict(dy=None)), (BAD, dict(dg=None)), (BAD, dict(dv=None)),
+        (BAD, dict(do=None)), (BAD, dict(o=None)), (BAD, dict(dys=63)), (BAD, dict(dgs=63)),
+        (BAD, dict(dvs=63)), (BAD, dict(dos=63)), (UNS, dict(dy=ODD)), (UNS, dict(dg=ODD)),
+        (UNS, dict(dv=ODD)), (UNS, dict(do=ODD)), (UNS, dict(dN=ODD)), (UNS, dict(d0=ODD))])
+    check(step, ok, all_ + [
+        (BAD, dict(y=None)), (BAD, dict(ys=63)), (UNS, dict(y=ODD)), (BAD, dict(sl=-1)),
+        (BAD, dict(ix=None)), (BAD, dict(h0=None)), (BAD, dict(hN=None)), (UNS, dict(ix=ODD)),
+        (UNS, dict(hN=ODD)), (UNS, dict(n=1 << 24))])
+    assert ctr.ctr_gated_scan_chunks(0) == 0 and ctr.ctr_gated_scan_chunks(-5) == 0
+    assert ctr.ctr_gated_scan_chunks(64) == 1 and ctr.ctr_gated_scan_chunks(65) == 2
+
+
+def test_binding_refusals():
+    """What the binding refuses before the library is called; nothing runs on the CPU."""
+    z, f = torch.zeros, torch.float32
+    ids = torch.arange(4)
+    with pytest.raises(ValueError, match="on a GPU"):
+        ctr.ctr_token_embed_fwd(z(9, 8), ids)
+    for call in (lambda: ctr.ctr_token_embed_fwd(z(9, 8, dtype=torch.float64), ids),
+                 lambda: ctr.ctr_token_embed_fwd(z(9, 8), ids.float()),
+                 lambda: ctr.ctr_token_embed_fwd(z(9, 8), ids, out_dtype=torch.int8),
+                 lambda: ctr.ctr_rms_norm_fwd(z(4, 8), z(8, dtype=torch.bfloat16)),
+                 lambda: ctr.ctr_rms_norm_fwd(z(4, 8), z(8), z(4, 8).bfloat16()),
+                 lambda: ctr.ctr_quant_dense_fwd(z(4, 16), z(4), z(4, 16).to(ctr.F8), z(4)),
+                 lambda: ctr.ctr_gated_scan_fwd(z(4, 8), z(4, 8), ids.int()),
+                 lambda: ctr.ctr_gated_scan_step(z(4, 8), z(4, 8), z(4, 8), index=ids)):
+        with pytest.raises(TypeError):
+            call()
+    q = z(4, 16).to(ctr.F8)
+    for call in (lambda: ctr.ctr_token_embed_fwd(z(9, 8).t(), ids),
+                 lambda: ctr.ctr_token_embed_fwd(z(9, 8), ids.view(2, 2)),
+                 lambda: ctr.ctr_token_embed_bwd(z(5, 8), ids, 9),
+                 lambda: ctr.ctr_token_embed_bwd(z(4, 8), ids, 9, dtable=z(9, 7)),
+                 lambda: ctr.ctr_rms_norm_fwd(z(4, 8), z(9)),
+                 lambda: ctr.ctr_rms_norm_fwd(z(4, 8), z(8), S=z(4, 8)),
+                 lambda: ctr.ctr_rms_norm_fwd(z(4, 8), z(8), y_scale=z(4)),
+                 lambda: ctr.ctr_rms_norm_fwd(z(4, 8), z(8), quantize=True, Y=z(4, 8).to(ctr.F8)),
+                 lambda: ctr.ctr_rms_norm_bwd(z(4, 8), z(4, 8), z(3), z(8)),
+                 lambda: ctr.ctr_quant_dense_fwd(q, z(4), q[:, :8], z(4)),
+                 lambda: ctr.ctr_quant_dense_fwd(q, z(3), q, z(4)),
+                 lambda: ctr.ctr_quant_dense_fwd(q, z(4), q, z(4), act="tanh"),
+                 lambda: ctr.ctr_quant_dense_fwd(q, z(4), q, z(4), z(5)),
+                 lambda: ctr.ctr_gated_scan_fwd(z(4, 8), z(4, 9), ids),
+                 lambda: ctr.ctr_gated_scan_fwd(z(8), z(8), ids),
+                 lambda: ctr.ctr_gated_scan_fwd(z(4, 8), z(4, 8), ids, h0=z(4, 8)),
+                 lambda: ctr.ctr_gated_scan_bwd(z(4, 8), z(4, 8), ids, z(4, 8), z(2, 8)),
+                 lambda: ctr.ctr_gated_scan_bwd(z(4, 8), z(4, 8), ids, z(4, 8), z(1, 8),
+                                                dout_gate=z(4, 8)),
+                 lambda: ctr.ctr_gated_scan_step(z(4, 8), z(4, 8), z(5, 8), new_state=True),
+                 lambda: ctr.ctr_gated_scan_step(z(4, 8), z(4, 8), z(4, 8), ids.int(),
+                                                 new_state=True)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_another_device_than_the_current_one_is_refused(monkeypatch):
+    """The library launches on the current device; tensors of another are not its."""
+    class Device:
+        type, index = "cuda", 1
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="current device"):
+        ctr._launch_here("ctr_quantize_rows", Device(), (), False)
+
+
+# ------------------------------------------------------------------------- the definitions
+def test_scan_gradients_against_differences():
+    g = torch.Generator().manual_seed(0)
+
+    def rand(*s):
+        return torch.randn(s, generator=g).double()
+    off, D = [0, 3, 3, 9, 10], 4
+    x = {"gate": rand(10, D), "value": rand(10, D), "out": rand(10, D), "h0": rand(4, D)}
+    dY, dhN = rand(10, D), rand(4, D)
+    res = ref.scan(x["gate"], x["value"], off, x["out"], x["h0"], dY, dhN)
+
+    def loss(y):
+        r = ref.scan(y["gate"], y["value"], off, y["out"], y["h0"])
+        return (r["Y"][0] * dY).sum() + (r["hN"][0] * dhN).sum()
+    for name, grad in (("gate", "dgate"), ("value", "dvalue"), ("out", "dout"), ("h0", "dh0")):
+        move = rand(*x[name].shape)
+        h = 1e-5
+        up = loss(dict(x, **{name: x[name] + h * move}))
+        down = loss(dict(x, **{name: x[name] - h * move}))
+        slope, want = float(up - down) / (2 * h), float((res[grad][0] * move).sum())
+        assert abs(slope - want) <= 1e-7 * float((res[grad][0] * move).abs().sum()) + 1e-9, name
+    for _, err in res.values():
+        assert (err >= 0).all()
+    # the state of a sequence without rows goes through, and so does its gradient
+    assert torch.equal(res["hN"][0][1], x["h0"][1]) and torch.equal(res["dh0"][0][1], dhN[1])
+    # row by row it is the same
+    state = x["h0"][:1].clone()
+    for t in range(3):
+        Y, _, state, _ = ref.scan_step(x["gate"][t:t + 1], x["value"][t:t + 1], state, None,
+                                       x["out"][t:t + 1])
+        assert torch.allclose(Y[0], res["Y"][0][t], rtol=1e-14)
+
+
+def test_norm_gradients_are_autograds():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((6, 10), generator=g).double().requires_grad_(True)
+    w = torch.randn(10, generator=g).double().requires_grad_(True)
+    dY, dS = (torch.randn((6, 10), generator=g).double() for _ in range(2))
+    y, rstd, _ = ref.norm_fwd(x, w, 1e-3)
+    ((y * dY).sum() + (x * dS).sum()).backward()
+    dx, _, dw, _ = ref.norm_bwd(dY, x.detach(), rstd.detach()[:, 0], w.detach(), dS)
+    assert torch.allclose(dx, x.grad, rtol=1e-12) and torch.allclose(dw, w.grad, rtol=1e-12)
+
+
+def test_codes_are_torchs():
+    """The definition of an 8-bit code agrees with torch's conversion, ties to even."""
+    codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    codes = codes[torch.isfinite(codes)].unique()
+    x = torch.cat([codes, (codes[1:] + codes[:-1]) / 2, torch.linspace(-448, 448, 4001),
+                   torch.linspace(-0.03, 0.03, 4001)])
+    assert torch.equal(ref.e4m3(x.double()).float(), x.to(torch.float8_e4m3fn).float())
