@@ -835,9 +835,11 @@ int32_t ctr_quantize_rows(const void* X, int32_t dtype, int64_t x_stride, int64_
  *   Y[m, n] = act(x_scale[m] w_scale[n] sum_k X[m, k] W[n, k] + b[n]) + R[m, n]
  * X: CTR_F8 [M, K] and W: CTR_F8 [N, K], 16-byte aligned rows whose strides (bytes) and K are
  * multiples of 16, as ctr_rms_norm_fwd and ctr_quantize_rows write them (the padding is part of
- * K); products exact, sums fp32.  b: fp32 [N] or NULL.  act: CTR_ACT_*; silu x sigmoid(x), gelu
+ * K).  Sums are fp32.  The products are exact for an fp32 Y; for a Y of 16 bits what lies below 2^-13
+ * of the largest of eight neighbouring products is cut off, far below Y's rounding.  b: fp32 [N] or NULL.  act: CTR_ACT_*; silu x sigmoid(x), gelu
  * x (1 + erf(x / sqrt 2)) / 2.  R: rows of dtype or NULL; Y: rows of dtype; Y may be R.
- * 16 <= K <= 65536, 1 <= N <= 65536.
+ * 16 <= K <= 65536, 1 <= N <= 65536, row strides of codes below 2^22, fewer than 2^24 tiles of 128
+ * x 128 of Y.
  */
 enum { CTR_ACT_NONE = 0, CTR_ACT_RELU = 1, CTR_ACT_SILU = 2, CTR_ACT_GELU = 3 };
 int32_t ctr_quant_dense_fwd(const void* X, int64_t x_stride, int64_t M, int32_t K,
@@ -848,15 +850,16 @@ int32_t ctr_quant_dense_fwd(const void* X, int64_t x_stride, int64_t M, int32_t 
 
 /*
  * ctr_gated_scan_fwd -- a gated linear recurrence over num_seqs sequences that lie one after the
- * other: sequence b has the rows [offsets[b], offsets[b + 1]) of n; rows outside all of them are
- * neither read nor written.  For every channel, with f = sigmoid(gate):
+ * other: sequence b has the rows [offsets[b], offsets[b + 1]) of n; rows outside all of them count
+ * for nothing and are not written.  For every channel, with f = sigmoid(gate):
  *   h_t = f_t h_{t-1} + (1 - f_t) value_t,   before the first row h = h0[b]  (NULL: 0)
  *   Y_t = h_t, or h_t silu(out_gate_t)       (out_gate NULL: the former)
  *   hN[b] = h after the last row of b, h0[b] where b has none               (nullable)
  * gate, value, out_gate, Y: rows of D values (parts of one wider row, if need be); h0, hN: fp32
  * [num_seqs, D]; offsets: int64 [num_seqs + 1], non-decreasing (else some numbers are wrong, and
  * nothing outside the arrays is touched).  states: fp32 [ctr_gated_scan_chunks(n), D] or NULL, the
- * states that the backward takes.  n <= 2^29, num_seqs < 2^31, 1 <= D <= 65536.
+ * states that the backward takes.  n <= 2^29, num_seqs < 2^31, 1 <= D <= 65536, and
+ * fewer than 2^23 pieces of 64 rows and 64 channels.
  * ctr_gated_scan_bwd -- from dY and dhN (or NULL) the gradients of gate, value, out_gate (with an
  * out_gate; else NULL) and h0 (nullable); the arrays otherwise as in the forward, states its own.
  * Workspaces: two-call queries.

@@ -1380,8 +1380,9 @@ int32_t ctr_quant_dense_fwd(const void* X, int64_t x_stride, int64_t M, int32_t 
     return fail(CTR_ERR_UNSUPPORTED, "x_stride and w_stride must be below 2^22");
   if (y_stride < N || (R && r_stride < N))
     return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride and r_stride must be at least N");
-  if ((M / 256 + 1) * (N / 256 + 1) > ((int64_t)1 << 22))
-    return fail(CTR_ERR_UNSUPPORTED, "more than 2^22 tiles of 256 x 256");
+  // a launch has fewer than 2^32 threads, a tile 256
+  if ((M + 127) / 128 * ((N + 127) / 128) >= (int64_t)1 << 24)
+    return fail(CTR_ERR_UNSUPPORTED, "2^24 tiles of 128 x 128 or more");
   if (M > 0 && (!X || !x_scale || !W || !w_scale || !Y))
     return fail(CTR_ERR_INVALID_ARGUMENT, "X, x_scale, W, w_scale and Y are required");
   if (!elt_aligned(R, dtype) || !elt_aligned(Y, dtype) || !aligned4(x_scale) ||
@@ -1409,8 +1410,7 @@ static int32_t check_scan(const void* gate, int64_t gs, const void* value, int64
     return fail(CTR_ERR_UNSUPPORTED, "an array is not aligned to its elements");
   return CTR_OK;
 }
-static int32_t check_sequences(const int64_t* offsets, int64_t n, int64_t num_seqs) {
-  if (n > ((int64_t)1 << 29)) return fail(CTR_ERR_UNSUPPORTED, "n above 2^29");
+static int32_t check_sequences(const int64_t* offsets, int64_t num_seqs) {
   if (num_seqs < 0 || num_seqs > kMaxElems)
     return fail(CTR_ERR_INVALID_ARGUMENT, "num_seqs must be in [0, 2^31)");
   if (!offsets) return fail(CTR_ERR_INVALID_ARGUMENT, "offsets is required");
@@ -1423,6 +1423,9 @@ static int32_t check_scan_query(int64_t n, int32_t D) {
   if (n < 0 || D < 1 || D > kMaxWidth)
     return fail(CTR_ERR_INVALID_ARGUMENT, "need n >= 0 and D in [1, 65536]");
   if (n > ((int64_t)1 << 29)) return fail(CTR_ERR_UNSUPPORTED, "n above 2^29");
+  // a launch has fewer than 2^32 threads, a chunk's tile 512
+  if (ctr::gated_scan_chunks(n) * ((D + 63) / 64) >= kMaxBlocks)
+    return fail(CTR_ERR_UNSUPPORTED, "2^23 pieces of 64 rows and 64 channels or more");
   return CTR_OK;
 }
 
@@ -1440,7 +1443,7 @@ int32_t ctr_gated_scan_fwd(const void* gate, int64_t gate_stride, const void* va
   if (st || query) return st;
   st = check_scan(gate, gate_stride, value, value_stride, out_gate, out_stride, dtype, n, D);
   if (st) return st;
-  st = check_sequences(offsets, n, num_seqs);
+  st = check_sequences(offsets, num_seqs);
   if (st) return st;
   if (y_stride < D) return fail(CTR_ERR_INVALID_ARGUMENT, "y_stride < D");
   if (n > 0 && !Y) return fail(CTR_ERR_INVALID_ARGUMENT, "Y is required");
@@ -1470,7 +1473,7 @@ int32_t ctr_gated_scan_bwd(const void* gate, int64_t gate_stride, const void* va
   if (st || query) return st;
   st = check_scan(gate, gate_stride, value, value_stride, out_gate, out_stride, dtype, n, D);
   if (st) return st;
-  st = check_sequences(offsets, n, num_seqs);
+  st = check_sequences(offsets, num_seqs);
   if (st) return st;
   if ((out_gate != nullptr) != (dout_gate != nullptr) && n > 0)
     return fail(CTR_ERR_INVALID_ARGUMENT, "out_gate and dout_gate go together");

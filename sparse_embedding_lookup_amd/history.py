@@ -123,7 +123,7 @@ class HistoryEncoder:
     def forward(self) -> torch.Tensor:
         self.used[1:].copy_(self.offsets[-1:])
         self.last.copy_(torch.where(self.offsets[1:] > self.offsets[:-1], self.offsets[1:] - 1,
-                                    self.nowhere))
+                                    self.nowhere)).clamp_(0, self.rows)
         for call in self._forward:
             call()
         return self.U.copy_(self.F[self.last])
@@ -199,7 +199,7 @@ class HistoryServer:
         there = offsets[1:] > offsets[:-1]
         if F.shape[0] == 0:
             return torch.zeros((len(users), self.dim), dtype=self.dtype, device=ids.device)
-        return torch.where(there[:, None], F[(offsets[1:] - 1).clamp(min=0)], 0)
+        return torch.where(there[:, None], F[(offsets[1:] - 1).clamp(0, F.shape[0] - 1)], 0)
 
     def step(self, ids: torch.Tensor, users: torch.Tensor) -> torch.Tensor:
         """The vectors [B, dim] after one more click ids[b] of each user users[b] (int32, on the

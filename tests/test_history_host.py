@@ -112,7 +112,8 @@ def test_dense_refusals():
         (UNS, dict(ws=1 << 22)), (BAD, dict(ys=31)), (BAD, dict(rs=31)), (BAD, dict(x=None)),
         (BAD, dict(xc=None)), (BAD, dict(w=None)), (BAD, dict(wc=None)), (BAD, dict(y=None)),
         (UNS, dict(y=ODD)), (UNS, dict(r=ODD)), (UNS, dict(xc=ODD)), (UNS, dict(wc=ODD)),
-        (UNS, dict(b=ODD)), (UNS, dict(M=(1 << 31) - 1, N=1024, ys=1024, rs=1024))])
+        (UNS, dict(b=ODD)), (UNS, dict(M=(1 << 31) - 1, N=1024, ys=1024, rs=1024)),
+        (UNS, dict(M=(1 << 31) - 1, N=1))])
 
 
 def test_scan_refusals():
@@ -139,7 +140,7 @@ def test_scan_refusals():
             (BAD, dict(vs=63)), (BAD, dict(os=63)), (BAD, dict(g=None)), (BAD, dict(v=None)),
             (UNS, dict(g=ODD)), (UNS, dict(v=ODD)), (UNS, dict(o=ODD)), (UNS, dict(h0=ODD))]
     both = all_ + WORKSPACES + [
-        (UNS, dict(n=(1 << 29) + 1)), (BAD, dict(B=-1)), (BAD, dict(B=1 << 31)),
+        (UNS, dict(n=(1 << 29) + 1)), (UNS, dict(n=1 << 29, D=1)), (BAD, dict(B=-1)), (BAD, dict(B=1 << 31)),
         (BAD, dict(off=None)), (UNS, dict(off=ctypes.c_void_p(0x10004))), (UNS, dict(st=ODD)),
         (BAD, dict(D=65537, gs=1 << 17))]
     check(fwd, ok, both + [(BAD, dict(y=None)), (BAD, dict(ys=63)), (UNS, dict(y=ODD)),
