@@ -21,6 +21,11 @@
 // counter, in order: who is waited for has begun, and waits for none behind it, so every wait ends.
 // What a block leaves is one 64-bit word a channel, map and all, so that no word has to be ordered
 // with another.
+//
+// Bound by memory, with the wait for the chunks before: 131072 x 1024 bf16 in 512 sequences with an
+// output gate forward 285 us (3.8 TB/s; without any look back 282), backward 496 (3.8 TB/s; 442); one
+// sequence of 65537 x 512 69 us.  In two passes over the inputs, with the chunks' maps joined by a
+// launch between them, both directions took 1790 us and the long sequence 161 for 745 and 74.
 namespace ctr {
 namespace scan {
 
@@ -284,7 +289,8 @@ __device__ __forceinline__ unsigned long long look(const unsigned long long* wor
 }
 
 // What comes into a chunk, by one wave: the words of the kAhead chunks before it (in the scan's
-// direction) together, then the next, until the joined maps are constant in every channel.
+// direction) together, then the next, until the joined maps are constant in every channel.  (One or
+// four at a time: no difference beyond the noise.)
 constexpr int kAhead = 2;
 template <int VW, bool BACK>
 __device__ __forceinline__ void look_back(const Args& a, int64_t chunk, int c, bool in,
@@ -589,7 +595,8 @@ __global__ __launch_bounds__(kThreads, 4) void bwd_kernel(Args a) {
 
 // ---------------------------------------------------------------------------------- one step
 // Row i of B takes the state of slot index[i] (or i) one row further.  Rows of one slot follow each
-// other in their order: the first of them takes the others along, from registers.
+// other in their order: the first of them takes the others along, from registers.  (64 rows of 1024
+// channels 3.4 us, latency.)
 template <int TY, int VW, bool OUT>
 __global__ __launch_bounds__(256) void step_kernel(Args a, const int32_t* __restrict__ index,
                                                    int64_t slots, const float* __restrict__ state,
@@ -653,7 +660,7 @@ __global__ __launch_bounds__(256) void step_kernel(Args a, const int32_t* __rest
 int64_t pieces(int64_t n, int64_t size) { return (n + size - 1) / size; }
 
 // Four bytes a lane: a channel of binary32, or two of 16 bits where every row is whole pairs that
-// begin on 4 bytes.
+// begin on 4 bytes.  (65536 x 1024 forward with an output gate, one and two: 187 and 138 us.)
 bool pairs(int dtype, int D, const void* p, int64_t stride) {
   return dtype != kEltF32 && D % 2 == 0 && reinterpret_cast<uintptr_t>(p) % 4 == 0 &&
          stride % 2 == 0;

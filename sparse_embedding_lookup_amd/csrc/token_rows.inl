@@ -19,7 +19,8 @@ __device__ __forceinline__ int64_t id_of(const void* ids, int64_t i) {
 
 // ------------------------------------------------------------------------------ forward
 // G lanes (a power of two, at most 64) take a row in runs of E elements, ROWS rows at a time, so
-// that as many loads of far rows are in flight.
+// that as many loads of far rows are in flight.  Bound by memory: 2^20 tokens of 10^6 bf16 rows, 128
+// wide, 77 us, 0.27 GB written and as much gathered; 64 tokens of 64 fp32 2.6 us.
 template <int TT, int TO, bool ID64, int ROWS>
 __global__ __launch_bounds__(kThreads) void fwd_kernel(const void* __restrict__ table, int64_t V,
                                                        int D, const void* __restrict__ ids,
@@ -75,8 +76,9 @@ __device__ __forceinline__ void clear(float* p, int64_t begin, int64_t end, int 
 // tiles (by themselves in the third launch where tiles are few) and moves the tokens.  All of it
 // waits more than it moves, so every launch has blocks beside that clear a share of the gradient.
 // (65536 tokens of 100003 rows, 128 wide: with the table-wide clearing first and digits of 6 bits
-// in tiles of 1024 44 us up to the sums, and here 27; 2^20 tokens of 10^6 rows 154 and 104 us, of
-// which the clearing alone is 82.)
+// in tiles of 1024 44 us up to the sums, and here 29; 2^20 tokens of 10^6 rows 154 and 124 us, of
+// which the clearing alone is 82.  All of a digit's counts loaded at once in the third launch: no
+// difference.)
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kDigit = 10;
 constexpr int kBins = 1 << kDigit, kFewTiles = 64;
 struct Sort {
@@ -240,9 +242,9 @@ __global__ __launch_bounds__(kSortThreads) void move_kernel(Sort g) {
   }
 }
 
-// Few tokens: sorted in this launch.  A token's place is the number of tokens before it in
-// order; a block has 16 tokens and each of them 16 threads, which compare it with every
-// sixteenth of all.
+// Few tokens: sorted in this launch, for a sort of several would be latency alone.  A token's place
+// is the number of tokens before it in order; a block has 16 tokens and each of them 16 threads, which
+// compare it with every sixteenth of all.
 constexpr int kRankTile = 4096, kRankOf = 16;
 template <bool ID64>
 __global__ __launch_bounds__(kThreads) void rank_kernel(const void* __restrict__ ids, int n,
@@ -254,19 +256,23 @@ __global__ __launch_bounds__(kThreads) void rank_kernel(const void* __restrict__
     clear(dT, 0, count, key_blocks);
     return;
   }
-  __shared__ uint32_t tile[kRankTile];
+  __shared__ __attribute__((aligned(16))) uint32_t tile[kRankTile];
   const int t = threadIdx.x, i = (int)blockIdx.x * kRankOf + t / kRankOf, part = t % kRankOf;
   const uint32_t key = i < n ? key_of<ID64>(ids, i, V) : kNone;
   int before = 0;
   for (int t0 = 0; t0 < n; t0 += kRankTile) {
     const int m = n - t0 < kRankTile ? n - t0 : kRankTile;
     __syncthreads();
-    for (int j = t; j < m; j += kThreads) tile[j] = key_of<ID64>(ids, t0 + j, V);
-    __syncthreads();
 #pragma unroll 8
-    for (int j = part; j < m; j += kRankOf) {
-      const uint32_t k = tile[j];
-      before += k < key || (k == key && t0 + j < i);
+    for (int j = t; j < (m + 3) / 4 * 4; j += kThreads)
+      tile[j] = j < m ? key_of<ID64>(ids, t0 + j, V) : kNone;
+    __syncthreads();
+#pragma unroll 4
+    for (int j = 4 * part; j < m; j += 4 * kRankOf) {
+      const uint4 k = *reinterpret_cast<const uint4*>(tile + j);
+      const int at = i - (t0 + j);             // equal keys count where they come before
+      before += (k.x < key + (at > 0)) + (k.y < key + (at > 1)) + (k.z < key + (at > 2)) +
+                (k.w < key + (at > 3));
     }
   }
 #pragma unroll
@@ -279,9 +285,13 @@ __global__ __launch_bounds__(kThreads) void rank_kernel(const void* __restrict__
 
 // Sums of the sorted tokens' rows.  A block has 256 / G groups of G lanes, a group `chunk`
 // neighbouring sorted positions and a lane E columns of them.  A group stores the sums of the
-// rows that begin and end inside it; its first and its last go through LDS, where one group
-// joins them in order.  What a block shares with its neighbours (the rows of its first and last
+// rows that begin and end inside it; its first and its last go through LDS, where the group where
+// a row begins joins what the groups after it have of it, in order.  What a block shares with its neighbours (the rows of its first and last
 // position) goes to `part`, two sums a block, for join_kernel.
+// Bound by the gather of dY's rows in the order of the keys: 2^20 rows of 128 bf16 131 us, 0.27 GB
+// gathered and the sums written; 65536 10 us.  (Chunks of 8 to 128 positions and rows through LDS
+// ahead of their use were all within 5 % of that.  With one group that joins the firsts and lasts of
+// all, one after the other, 136 and 16 us, and 19 for 256 rows of 64, now 5.)
 struct Sums {
   const uint32_t* sk;
   const uint32_t* sv;
@@ -317,6 +327,9 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(Sums g) {
   const int there = c < g.D ? g.D - c : 0;
   const int64_t a = ((int64_t)blockIdx.x * groups + group) * g.chunk;
   const int64_t b = a + g.chunk < g.n ? a + g.chunk : g.n;
+  // the block's positions, and the rows before and behind them
+  const int64_t lo = (int64_t)blockIdx.x * groups * g.chunk, hi = lo + (int64_t)groups * g.chunk;
+  const uint32_t came = lo > 0 ? g.sk[lo - 1] : kNone, goes = hi < g.n ? g.sk[hi] : kNone;
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -363,50 +376,57 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(Sums g) {
   keys[0][t] = first;
   keys[1][t] = cur;
   __syncthreads();
-  if (group != 0) return;
-  const int64_t lo = (int64_t)blockIdx.x * groups * g.chunk;
-  const int64_t hi = lo + (int64_t)groups * g.chunk < g.n ? lo + (int64_t)groups * g.chunk : g.n;
-  const uint32_t came = lo > 0 ? g.sk[lo - 1] : kNone, goes = hi < g.n ? g.sk[hi] : kNone;
-  uint32_t in = kNone, on = kNone;
-  float s[E];
-  uint32_t run = kNone;
-  auto emit = [&] {
-    if (run >= g.V) return;                    // no row, or that of no token
-    if (run == came) {
-      in = run;
-      if (there > 0) put_sum<E>(g.part + (int64_t)blockIdx.x * 2 * g.D, c, g.D, s, 1.f);
-    } else if (run == goes) {
-      on = run;
-      if (there > 0) put_sum<E>(g.part + ((int64_t)blockIdx.x * 2 + 1) * g.D, c, g.D, s, 1.f);
-    } else if (there > 0) {
-      put_sum<E>(g.dT + (int64_t)run * g.D, c, g.D, s, g.scale);
-    }
+  // The runs of one row over the groups' firsts and lasts: each by the group where it begins.
+  auto emit = [&](uint32_t run, const float* v) {
+    if (run >= g.V || there <= 0) return;      // that of no token
+    if (run == came) put_sum<E>(g.part + (int64_t)blockIdx.x * 2 * g.D, c, g.D, v, 1.f);
+    else if (run == goes) put_sum<E>(g.part + ((int64_t)blockIdx.x * 2 + 1) * g.D, c, g.D, v, 1.f);
+    else put_sum<E>(g.dT + (int64_t)run * g.D, c, g.D, v, g.scale);
   };
-  for (int u = 0; u < groups; ++u)
-    for (int q = 0; q < 2; ++q) {
-      const int at = u * g.G + l;
-      const uint32_t key = keys[q][at];
-      if (key == kNone) continue;
-      if (key != run) {
-        emit();
-        run = key;
+  const uint32_t left = group > 0 ? keys[1][t - g.G] : kNone;
+  if (first != kNone && first != left) {       // and its last is another
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[e] = sums[q][e * kThreads + at];
-      } else {
+    for (int e = 0; e < E; ++e) acc[e] = sums[0][e * kThreads + t];
+    emit(first, acc);
+  }
+  if (cur != kNone && (first != kNone || cur != left)) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[e] += sums[q][e * kThreads + at];
+    for (int e = 0; e < E; ++e) acc[e] = sums[1][e * kThreads + t];
+    constexpr int STEP = 4;
+    bool on = true;
+    for (int u = group + 1; on && u < groups; u += STEP) {
+      float x[STEP][E];
+      bool same[STEP], whole[STEP];            // its first or all of it is of this row
+#pragma unroll
+      for (int i = 0; i < STEP; ++i) {
+        const int at = (u + i < groups ? u + i : groups - 1) * g.G + l;
+        const uint32_t head = keys[0][at];
+        whole[i] = head == kNone;
+        same[i] = u + i < groups && (whole[i] ? keys[1][at] : head) == cur;
+        const float* from = sums[whole[i] ? 1 : 0] + at;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i][e] = from[e * kThreads];
+      }
+#pragma unroll
+      for (int i = 0; i < STEP; ++i) {
+        on = on && same[i];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = on ? acc[e] + x[i][e] : acc[e];
+        on = on && whole[i];
       }
     }
-  emit();
-  if (l == 0 && blockIdx.y == 0) {
-    g.part_key[2 * blockIdx.x] = in;
-    g.part_key[2 * blockIdx.x + 1] = on;
+    emit(cur, acc);
+  }
+  if (t == 0 && blockIdx.y == 0) {
+    g.part_key[2 * blockIdx.x] = came < g.V && g.sk[lo] == came ? came : kNone;
+    g.part_key[2 * blockIdx.x + 1] =
+        goes < g.V && goes != came && g.sk[hi - 1] == goes ? goes : kNone;
   }
 }
 
 // The rows that several blocks share: the block where one begins adds what goes on from there
 // and what came into the blocks after it, each group every 256 / G-th of them, then the groups'
-// sums in order.
+// sums in order.  (Latency: 4.6 us for 512 blocks' sums, 6.1 for 2048.)
 template <int E>
 __global__ __launch_bounds__(kThreads) void join_kernel(Sums g, int64_t blocks) {
   __shared__ float sums[kThreads * E];
@@ -458,6 +478,8 @@ int lanes(int D, int E) {
   return G;
 }
 
+// (The whole gradient, 64 wide, of 1000 and of 10^6 rows by ranks and by the sort: 1024 tokens 14 and
+// 18, 43 and 48 us; 4096 19 and 19, 45 and 49; 8192 27 and 20, 48 and 49.)
 constexpr int64_t kRankMost = 4096;
 
 int key_bits(int64_t V) {
@@ -485,8 +507,10 @@ struct Workspace {
   int64_t blocks;
   size_t bytes;
 };
-// Tokens a thread in a sort's tile: one as long as the tiles stay few.
-int sort_items(int64_t n) { return n <= (int64_t)kFewTiles * kSortThreads ? 1 : 4; }
+// Tokens a thread in a sort's tile: one until there is a tile for every compute unit, then four.
+// (The whole gradient, 64 wide, of 10^6 rows: 262144 tokens 96 us with one and 103 with four, 524288
+// 143 and 127.)
+int sort_items(int64_t n) { return n <= (int64_t)256 * kSortThreads ? 1 : 4; }
 int64_t sort_tiles(int64_t n) {
   const int64_t tile = (int64_t)kSortThreads * sort_items(n);
   return (n + tile - 1) / tile;
@@ -527,7 +551,8 @@ hipError_t launch_token_embed_fwd(const void* table, int dtype, int64_t V, int D
     return for_type(out_dtype, [&](auto to) {
       constexpr int TT = decltype(tt)::value, TO = decltype(to)::value;
       const int G = tokens::lanes(D, TT == kEltF32 && TO == kEltF32 ? 4 : 8);
-      // one row a group until that fills the chip, then four
+      // one row a group until the chip is full several times over, then four (128 bf16 of 10^6 rows:
+      // 4096 tokens 2.7 and 3.2 us, 65536 6.6 and 6.6, 2^20 107 and 85)
       auto launch = [&](auto id64, auto rows) {
         constexpr int R = decltype(rows)::value;
         const int64_t groups = (n + R - 1) / R, per = tokens::kThreads / G;
@@ -539,7 +564,7 @@ hipError_t launch_token_embed_fwd(const void* table, int dtype, int64_t V, int D
       auto by_id = [&](auto rows) {
         return ids64 ? launch(std::true_type{}, rows) : launch(std::false_type{}, rows);
       };
-      return n * G < (int64_t)1 << 18 ? by_id(std::integral_constant<int, 1>{})
+      return n * G < (int64_t)1 << 20 ? by_id(std::integral_constant<int, 1>{})
                                       : by_id(std::integral_constant<int, 4>{});
     });
   });
