@@ -24,9 +24,11 @@
 //
 // Bound by memory, with the wait for the chunks before: 131072 x 1024 bf16 in 512 sequences with an
 // output gate forward 285 us (3.8 TB/s; without any look back 282), backward 496 (3.8 TB/s; 442); one
-// sequence of 65537 x 512 69 us.  (Four waves a block 289, 510 and 79 us; eight waves of 8 rows
-// forward and 4 backward 290, 563 and 80.)  In two passes over the inputs, with the chunks' maps joined by a
+// sequence of 65537 x 512 69 us.  In two passes over the inputs, with the chunks' maps joined by a
 // launch between them, both directions took 1790 us and the long sequence 161 for 745 and 74.
+// (Four waves a block 289, 510 and 79 us; eight waves of 8 rows forward and 4 backward 290, 563 and
+// 80; blocks that stay and take chunk after chunk 324, 668 and 81, as the next chunk waits for the
+// stores of this one.)
 namespace ctr {
 namespace scan {
 
