@@ -13,11 +13,6 @@ template <int TY>
 constexpr int kEltSize = TY == kEltF32 ? 4 : 2;
 
 template <int TY>
-__device__ __forceinline__ float load_elt(const void* p, int64_t i) {
-  if constexpr (TY == kEltF32) return static_cast<const float*>(p)[i];
-  else return half_lo<TY>(static_cast<const uint16_t*>(p)[i]);
-}
-template <int TY>
 __device__ __forceinline__ void store_elt(void* p, int64_t i, float v) {
   if constexpr (TY == kEltF32) static_cast<float*>(p)[i] = v;
   else static_cast<uint16_t*>(p)[i] = (uint16_t)to_half<TY, false>(v, 0u);
@@ -51,10 +46,6 @@ struct Run {
         if constexpr (TY == kEltF32) u[e] = static_cast<const uint32_t*>(p)[i + e];
         else u[e / 2] |= (uint32_t) static_cast<const uint16_t*>(p)[i + e] << (e & 1 ? 16 : 0);
       }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) u[w] = 0u;
   }
   __device__ __forceinline__ float at(int e) const {
     if constexpr (TY == kEltF32) return __uint_as_float(u[e]);
