@@ -11,8 +11,8 @@
 // of E elements a lane, so that memory is read once; statistics are fp32 sums of the lanes' own
 // sums.  Groups stay and take row after row, with the weights in registers.
 // Bound by memory: 65536 x 1024 bf16 with the residual's sum written 93 us (5.8 TB/s), backward with
-// the other gradient 114 us (4.7 TB/s) and 6 for the weight's partial sums; 16387 x 479 fp32 12, 17
-// and 6 us (5.3 and 5.4 TB/s); 48 x 1024 into 8 bits 5.1 us, latency.
+// the other gradient 114 us (4.7 TB/s) and 5 for the weight's partial sums; 16387 x 479 fp32 12, 17
+// and 4 us (5.3 and 5.4 TB/s); 48 x 1024 into 8 bits 5.1 us, latency.
 namespace ctr {
 namespace norm {
 
@@ -263,30 +263,33 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
   }
 }
 
-// dw: a block has 64 columns, its sixteen waves every sixteenth block's partial sums, sixteen in
-// flight, joined in order.  (Four waves with eight in flight, 32 trips to memory one after the
-// other: 13 us for 3.)
-constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(const float* __restrict__ part,
-                                                               int blocks, int D,
-                                                               float* __restrict__ dw) {
-  __shared__ float sums[kJoinWaves][64];
-  constexpr int DEEP = 16;
-  const int l = threadIdx.x & 63, v = threadIdx.x >> 6, c = (int)blockIdx.x * 64 + l;
+// dw: a block has 16 columns, its 64 groups of 16 lanes every 64th block's partial sums, sixteen in
+// flight, joined in order: one trip to memory where 1024 blocks left theirs.  (64 columns a block and
+// every sixteenth block's sums a wave 5.6 us for 3.9, four waves with eight in flight 13.)
+constexpr int kJoinCols = 16, kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const float* __restrict__ part,
+                                                            int blocks, int D,
+                                                            float* __restrict__ dw) {
+  __shared__ float sums[kJoinWaves][kJoinCols];
+  constexpr int DEEP = 16, GROUPS = kJoinThreads / kJoinCols;
+  const int l = threadIdx.x % kJoinCols, c = (int)blockIdx.x * kJoinCols + l;
   float s = 0.f;
-  for (int b = v; b < blocks; b += DEEP * kJoinWaves) {
+  for (int b = threadIdx.x / kJoinCols; b < blocks; b += DEEP * GROUPS) {
     float x[DEEP];
 #pragma unroll
     for (int i = 0; i < DEEP; ++i) {
-      const int at = b + i * kJoinWaves;
+      const int at = b + i * GROUPS;
       x[i] = at < blocks && c < D ? part[(int64_t)at * D + c] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < DEEP; ++i) s += x[i];
   }
-  sums[v][l] = s;
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  if ((threadIdx.x & 63) < kJoinCols) sums[threadIdx.x >> 6][l] = s;
   __syncthreads();
-  if (v != 0 || c >= D) return;
+  if (threadIdx.x >= kJoinCols || c >= D) return;
+  s = sums[0][l];
   for (int i = 1; i < kJoinWaves; ++i) s += sums[i][l];
   dw[c] = s;
 }
@@ -391,7 +394,8 @@ hipError_t launch_rms_norm_bwd(const void* dY, int dtype, int64_t dys, int64_t n
     if (e != hipSuccess) return e;
   }
   if (dw)
-    norm::join_kernel<<<(unsigned)((D + 63) / 64), norm::kJoinWaves * 64, 0, s>>>(a.part, blocks, D, dw);
+    norm::join_kernel<<<(unsigned)((D + norm::kJoinCols - 1) / norm::kJoinCols),
+                        norm::kJoinThreads, 0, s>>>(a.part, blocks, D, dw);
   return hipGetLastError();
 }
 
