@@ -233,3 +233,36 @@ def test_server_of_odd_widths(dtype, D):
         assert torch.equal(out, other.step(click, index))
         for a, b in zip(server.state, other.state):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,V,D,dtype", [(300001, 5000, 8, BF16), (270000, 3000001, 4, F32),
+                                         (1000003, 60, 12, torch.float16)])
+def test_embed_bwd_of_many_tokens(n, V, D, dtype):
+    """Sorts of many tiles, of one to three digits, with a quarter of all tokens the same."""
+    say("many tokens", n, V, D, dtype)
+    g = torch.Generator().manual_seed(1)
+    ids = torch.randint(-1, V + 1, (n,), generator=g)
+    ids[torch.rand(n, generator=g) < 0.25] = V // 3
+    dY = normal(2, n, D, dtype=dtype)
+    want, m, terms = ref.embed_bwd(dY, ids, V, 1.5)
+    for kind in (torch.int64, torch.int32):
+        got = ctr.ctr_token_embed_bwd(dY.to(DEV), ids.to(kind).to(DEV), V, 1.5)
+        assert_near(got, want, (terms + 4) * 2.0 ** -24 * m, "dtable")
+
+
+@pytest.mark.parametrize("K", [1152, 1168, 1280, 1424, 1600, 1664])
+@pytest.mark.parametrize("out", [F32, BF16, torch.float16])
+def test_dense_large_tiles_of_any_depth(K, out):
+    """The largest tiles at every number of rounds that their loop ends with, ragged ones too."""
+    M, N = 4100, 4099
+    say("large tiles", K, out)
+    Xq, xs = ctr.ctr_quantize_rows(normal(1, M, K, dtype=BF16, scale=2.0).to(DEV))
+    Wq, ws = ctr.ctr_quantize_rows(normal(2, N, K, dtype=BF16, scale=K ** -0.5).to(DEV))
+    b, R = normal(3, N), normal(4, M, N, dtype=out)
+    rows = torch.cat([torch.arange(0, M, 331), torch.arange(M - 5, M)])
+    for act, bias, res in (("silu", True, True), ("relu", False, False)):
+        Y = ctr.ctr_quant_dense_fwd(Xq, xs, Wq, ws, b.to(DEV) if bias else None, act,
+                                    R.to(DEV) if res else None, out_dtype=out)
+        want, err = ref.dense(Xq.cpu()[rows], xs.cpu()[rows], Wq.cpu(), ws.cpu(),
+                              b if bias else None, act, R[rows] if res else None, out)
+        assert_near(Y.cpu()[rows], want, stored(want, err, out), act)
